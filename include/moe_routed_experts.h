@@ -1,6 +1,7 @@
 /*
  * moe_routed_experts.h -- C ABI of the routed top-k mixture-of-experts expert layer (forward,
- * backward and block-scaled forwards) for NVIDIA GB300 (sm_103a).
+ * backward and block-scaled forwards) and of the operators around it in a training step (layer norm,
+ * top-k router, vocabulary losses) for NVIDIA GB300 (sm_103a).
  *
  * The layer (the expert path shared by the TeraMoE README, Dist-MoE 0.1.0 and the Primus MegaMoE
  * guide; the MoonEP page describes its weight layout):
@@ -62,11 +63,15 @@ typedef enum {
 /* Bits of the device status word (read with moe_get_status). */
 enum {
     MOE_DEV_BAD_EXPERT_ID = 1u, /* an id outside [0, E): that (token, k) pair contributes 0 */
-    MOE_DEV_TIMEOUT = 2u        /* a kernel's bounded wait expired; its results are invalid */
+    MOE_DEV_TIMEOUT = 2u,       /* a kernel's bounded wait expired; its results are invalid */
+    MOE_DEV_BAD_TARGET = 4u     /* a label or teacher id outside the vocabulary: it counts as absent */
 };
 
 /* Dtype of topk_scores. */
 enum { MOE_SCORES_F32 = 0, MOE_SCORES_BF16 = 1 };
+
+/* Element types of the layer norm and router entry points. */
+enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 };
 
 /* Regions of the forward workspace, for moe_workspace_layout. */
 enum {
@@ -540,11 +545,141 @@ moe_status_t moe_routing_static_scratch(const int32_t *topk_ids, int64_t T, int3
                                         int32_t *counts, int32_t *offsets, int32_t *perm, int32_t *inv,
                                         uint32_t *device_status, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------ */
+/* The operators around the layer in a training step: the norm before it, the router that makes */
+/* its ids and scores, and the losses at the end of the model. The conventions above hold, but   */
+/* for the alignment and shape limits, which each entry point states. All are deterministic.     */
+/* ------------------------------------------------------------------------------------------ */
+
 /*
- * Reads the device status word at the start of `workspace` (a forward or a routing workspace)
- * into *device_bits (host memory): 0, or an OR of MOE_DEV_* bits raised since the last
- * moe_fwd_dispatch / moe_routed_experts_fwd / moe_routing on that workspace. Synchronises
- * `stream` first; the only synchronising entry point.
+ * Layer norm over the last dimension of x [T,D]:
+ *   mean = sum_d x / D,  rstd = 1 / sqrt(sum_d (x - mean)^2 / D + eps)
+ *   y = (x - mean) rstd gamma + beta
+ *   x, y         device [T,D] of `dtype` (MOE_DTYPE_*); y may be x itself
+ *   gamma, beta  device [D] of `param_dtype`; NULL = 1 and 0
+ *   mean, rstd   device fp32 [T], kept for the backward pass
+ * eps >= 0, 1 <= D <= 2^24, T < 2^31; pointers aligned to their element type. Arithmetic in fp32, y
+ * rounded once. Rows whose length is a multiple of 16 bytes, on 16-byte-aligned pointers, use
+ * 16-byte accesses.
+ */
+moe_status_t moe_layernorm_fwd(const void *x, const void *gamma, const void *beta, int32_t dtype,
+                               int32_t param_dtype, void *y, float *mean, float *rstd, int64_t T, int32_t D,
+                               float eps, moe_stream_t stream);
+
+/* Bytes of workspace moe_layernorm_bwd needs (0 for T = 0 or sizes outside the limits). Pure arithmetic. */
+size_t moe_layernorm_bwd_workspace_bytes(int64_t T, int32_t D);
+
+/*
+ * Layer norm's backward pass. With xhat = (x - mean) rstd and g = dy gamma:
+ *   dx = rstd (g - mean_d(g) - xhat mean_d(g xhat)),  dgamma = sum_t dy xhat,  dbeta = sum_t dy
+ *   dy, x, dx      device [T,D] of `dtype`; dx may be dy or x itself
+ *   gamma          device [D] of `param_dtype`; NULL = 1
+ *   mean, rstd     device fp32 [T], from moe_layernorm_fwd
+ *   dgamma, dbeta  device [D] of `param_dtype`, written in full; either may be NULL (not computed)
+ *   workspace      device, moe_layernorm_bwd_workspace_bytes(T, D) bytes, 256-byte aligned; may be
+ *                  NULL when dgamma and dbeta both are. It holds no status word.
+ * Sums in fp32, in a fixed order. T = 0 writes zero parameter gradients.
+ */
+moe_status_t moe_layernorm_bwd(const void *dy, const void *x, const void *gamma, const float *mean,
+                               const float *rstd, int32_t dtype, int32_t param_dtype, void *dx, void *dgamma,
+                               void *dbeta, int64_t T, int32_t D, void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
+/*
+ * The router's choice: for each row of logits [T,E], the K largest, largest first and equal ones by
+ * the lowest expert id, and their scores -- the softmax over the chosen K (normalize != 0) or the
+ * softmax over all E, at the chosen ones (normalize = 0).
+ *   logits       device [T,E], fp32 or bf16 (MOE_DTYPE_F32, MOE_DTYPE_BF16), element-aligned
+ *   topk_ids     device int32 [T,K];  topk_scores  device fp32 [T,K]: as the layer takes them
+ * 1 <= K <= E <= 4096, T < 2^31. A logit of -inf masks its expert (score 0; chosen only when fewer
+ * than K are left); a row of nothing but -inf has scores of 0. A NaN sorts above all and makes the
+ * row's scores NaN.
+ */
+moe_status_t moe_router_topk_fwd(const void *logits, int32_t dtype, int32_t *topk_ids, float *topk_scores,
+                                 int64_t T, int32_t E, int32_t K, int32_t normalize, moe_stream_t stream);
+
+/*
+ * The way back from the scores' gradient (moe_routed_experts_bwd's dscores) to the logits':
+ *   normalize != 0:  dz_i = s_i (ds_i - sum_j s_j ds_j) at the chosen experts, 0 elsewhere
+ *   normalize  = 0:  dz_i = p_i ([i chosen] ds_i - sum_j s_j ds_j) at every expert
+ * logits, topk_ids (distinct in each row) and normalize as in the forward call; dlogits has the
+ * logits' type and shape, and is written in full. An id outside [0, E) is passed over. Rows of
+ * nothing but -inf get zeros.
+ */
+moe_status_t moe_router_topk_bwd(const void *logits, int32_t dtype, const int32_t *topk_ids,
+                                 const float *dscores, void *dlogits, int64_t T, int32_t E, int32_t K,
+                                 int32_t normalize, moe_stream_t stream);
+
+/*
+ * Bytes of workspace the moe_lm_* calls need: K is the number of teacher entries per row (1 for cross
+ * entropy). The same size serves the forward and the backward call. It does not hold the T V logits: the
+ * backward pass goes over pieces of the vocabulary of at most 512 MB (or 2048 columns). 0 for sizes
+ * outside the limits: T >= 1, D a multiple of 64, 1 <= V <= 2^30, 1 <= K <= 256. Pure arithmetic.
+ */
+size_t moe_lm_workspace_bytes(int64_t T, int32_t D, int32_t V, int32_t K);
+
+/*
+ * Softmax cross entropy of a linear head, without keeping its logits z = x w^T:
+ *   lse[t] = log sum_v exp(z_tv),  loss[t] = lse[t] - z_t,target
+ *   x            device bf16 [T,D], 16-byte aligned
+ *   w            device bf16 [V,D], 16-byte aligned
+ *   targets      device int32 [T]; rows of `ignore_index` have loss 0. Any other target outside [0, V) sets
+ *                MOE_DEV_BAD_TARGET, and its row counts as ignored
+ *   loss, lse    device fp32 [T] (lse also of ignored rows)
+ *   workspace    device, moe_lm_workspace_bytes(T, D, V, 1) bytes, 256-byte aligned; its first 4 bytes are
+ *                the status word (moe_get_status)
+ * bf16 products, fp32 accumulation; sums and exponentials in fp32.
+ */
+moe_status_t moe_lm_ce_fwd(const void *x, const void *w, const int32_t *targets, int32_t ignore_index,
+                           float *loss, float *lse, int64_t T, int32_t D, int32_t V, void *workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * Its backward pass: with dl = dloss (softmax(z) - onehot(target)), dx = dl w and dw = dl^T x.
+ *   lse          device fp32 [T], from moe_lm_ce_fwd
+ *   dloss        device fp32 [T]: the gradient of each row's loss (1 / rows for a mean); not read for
+ *                ignored rows, which contribute nothing
+ *   dx           device bf16 [T,D], written in full (zeros for ignored rows), or NULL (not computed)
+ *   dw           device bf16 [V,D], written in full, or NULL (not computed)
+ * The logits are computed again, piece by piece. dl is rounded to bf16; dx and dw are summed in fp32
+ * and rounded once. x must be finite in ignored rows too (they are multiplied by 0 in dw). T = 0
+ * writes a zero dw.
+ */
+moe_status_t moe_lm_ce_bwd(const void *x, const void *w, const int32_t *targets, int32_t ignore_index,
+                           const float *lse, const float *dloss, void *dx, void *dw, int64_t T, int32_t D,
+                           int32_t V, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * Distillation of a linear head from a teacher's top logits: with p = softmax(teacher_logits / tau) over
+ * a row's kept entries, z = x w^T and lse[t] = log sum_v exp(z_tv / tau) over the whole vocabulary,
+ *   loss[t] = tau^2 sum_j p_j (log p_j - (z_t,id_j / tau - lse[t]))
+ *   teacher_ids     device int32 [T,K]; a negative id is an entry that was not kept (its logit is not
+ *                   looked at), an id >= V sets MOE_DEV_BAD_TARGET and counts as not kept. Repeated ids count
+ *                   each for itself
+ *   teacher_logits  device fp32 [T,K]
+ *   temperature     tau > 0, finite
+ * A row without kept entries, or with nothing but -inf in them, has loss 0. The rest as for
+ * moe_lm_ce_fwd, with moe_lm_workspace_bytes(T, D, V, K) bytes of workspace.
+ */
+moe_status_t moe_lm_distill_fwd(const void *x, const void *w, const int32_t *teacher_ids,
+                                const float *teacher_logits, float temperature, float *loss, float *lse,
+                                int64_t T, int32_t D, int32_t V, int32_t K, void *workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * Its backward pass: dl = tau dloss (softmax(z / tau) - sum_j p_j onehot(id_j)), dx = dl w, dw = dl^T x.
+ * Arguments as for moe_lm_distill_fwd and moe_lm_ce_bwd.
+ */
+moe_status_t moe_lm_distill_bwd(const void *x, const void *w, const int32_t *teacher_ids,
+                                const float *teacher_logits, float temperature, const float *lse,
+                                const float *dloss, void *dx, void *dw, int64_t T, int32_t D, int32_t V,
+                                int32_t K, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * Reads the device status word at the start of `workspace` (a forward, backward, routing or
+ * vocabulary-loss workspace) into *device_bits (host memory): 0, or an OR of MOE_DEV_* bits raised
+ * since the last moe_fwd_dispatch / moe_routed_experts_fwd / moe_routing / moe_lm_* on that
+ * workspace. Synchronises `stream` first; the only synchronising entry point.
  */
 moe_status_t moe_get_status(const void *workspace, uint32_t *device_bits, moe_stream_t stream);
 

@@ -1,4 +1,5 @@
-"""Routed top-k mixture-of-experts expert layer (forward) for GB300 (sm_103a).
+"""Routed top-k mixture-of-experts expert layer for GB300 (sm_103a), and the operators around it in a
+training step: layer norm, the top-k router and the vocabulary losses.
 
 The compute path is the C-ABI library ``libmoe_gb300.so`` (hand-written CUDA kernels); the
 functions re-exported here are its thin ctypes binding. Importing this package does not load the
@@ -34,6 +35,16 @@ __all__ = [
     "moe_nvfp4_workspace_layout",
     "moe_routed_experts_fwd_nvfp4",
     "moe_fwd_nvfp4_stages",
+    "moe_layernorm_fwd",
+    "moe_layernorm_bwd_workspace_bytes",
+    "moe_layernorm_bwd",
+    "moe_router_topk_fwd",
+    "moe_router_topk_bwd",
+    "moe_lm_workspace_bytes",
+    "moe_lm_ce_fwd",
+    "moe_lm_ce_bwd",
+    "moe_lm_distill_fwd",
+    "moe_lm_distill_bwd",
     "MOE_WEIGHT_W13",
     "MOE_WEIGHT_W2",
     "moe_get_status",

@@ -22,6 +22,8 @@ MOE_SCORES_F32 = 0
 MOE_SCORES_BF16 = 1
 MOE_DEV_BAD_EXPERT_ID = 1
 MOE_DEV_TIMEOUT = 2
+MOE_DEV_BAD_TARGET = 4
+MOE_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 WS_REGIONS = (
     "status", "counts", "offsets", "tiles1", "tiles2", "block_counts", "block_bases",
@@ -108,6 +110,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  vp], ctypes.c_int),
             "moe_fwd_mxfp8_stages": (
                 [vp, vp, vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_layernorm_fwd": ([vp, vp, vp, i32, i32, vp, vp, vp, i64, i32, ctypes.c_float, vp], ctypes.c_int),
+            "moe_layernorm_bwd_workspace_bytes": ([i64, i32], sz),
+            "moe_layernorm_bwd": (
+                [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, i64, i32, vp, sz, vp], ctypes.c_int),
+            "moe_router_topk_fwd": ([vp, i32, vp, vp, i64, i32, i32, i32, vp], ctypes.c_int),
+            "moe_router_topk_bwd": ([vp, i32, vp, vp, vp, i64, i32, i32, i32, vp], ctypes.c_int),
+            "moe_lm_workspace_bytes": ([i64, i32, i32, i32], sz),
+            "moe_lm_ce_fwd": ([vp, vp, vp, i32, vp, vp, i64, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_lm_ce_bwd": ([vp, vp, vp, i32, vp, vp, vp, vp, i64, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_lm_distill_fwd": (
+                [vp, vp, vp, vp, ctypes.c_float, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_lm_distill_bwd": (
+                [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -588,3 +603,195 @@ def moe_fwd_nvfp4_stages(x, topk_ids, topk_scores, w13_nv, w2_nv, out, workspace
         _ptr(x), _ptr(topk_ids), _ptr(topk_scores), sd, _ptr(w13_nv[0]), _ptr(w13_nv[1]), _ptr(w2_nv[0]),
         _ptr(w2_nv[1]), float(x_scale), float(h_scale), _ptr(out), T, D, F, E, K, int(stage_begin),
         int(stage_end), _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+
+
+# ------------------------------------------------- layer norm, router and vocabulary losses
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _shape(t: torch.Tensor, name: str, shape: tuple) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _rows(x, name: str, dtypes) -> tuple:
+    _need(x, name, dtypes, 2)
+    return tuple(x.shape)
+
+
+def _norm_params(x, D: int, **params) -> int:
+    """Checks the given [D] parameters (None is allowed) and returns their common MOE_DTYPE."""
+    dtype = None
+    for name, p in params.items():
+        if p is None:
+            continue
+        _need(p, name, tuple(MOE_DTYPE), 1)
+        _shape(p, name, (D,))
+        if dtype is not None and p.dtype != dtype:
+            raise TypeError(f"{name} must have the dtype of the other parameters, {dtype}, got {p.dtype}")
+        dtype = p.dtype
+    return MOE_DTYPE[dtype if dtype is not None else x.dtype]
+
+
+def moe_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps: float = 1e-5, stream=None) -> None:
+    """Layer norm of the rows of x [T,D] (fp32, bf16 or fp16) into y; mean and rstd [T] fp32 are kept for
+    the backward pass. gamma and beta [D] may be None (1 and 0), and have one dtype of their own. y may be x."""
+    T, D = _rows(x, "x", tuple(MOE_DTYPE))
+    _need(y, "y", x.dtype, 2)
+    _shape(y, "y", (T, D))
+    pd = _norm_params(x, D, gamma=gamma, beta=beta)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _need(t, name, torch.float32, 1)
+        _shape(t, name, (T,))
+    _same_device(x, gamma=gamma, beta=beta, y=y, mean=mean, rstd=rstd)
+    _check("moe_layernorm_fwd", load().moe_layernorm_fwd(
+        _ptr(x), _ptr(gamma), _ptr(beta), MOE_DTYPE[x.dtype], pd, _ptr(y), _ptr(mean), _ptr(rstd), T, D, float(eps),
+        _stream_handle(stream)))
+
+
+def moe_layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
+    return int(load().moe_layernorm_bwd_workspace_bytes(T, D))
+
+
+def moe_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream=None) -> None:
+    """Layer norm's backward pass: dx, and dgamma and dbeta (either may be None) in the parameters' dtype.
+    The workspace is moe_layernorm_bwd_workspace_bytes(T, D) bytes (None when neither is wanted)."""
+    T, D = _rows(x, "x", tuple(MOE_DTYPE))
+    for name, t in (("dy", dy), ("dx", dx)):
+        _need(t, name, x.dtype, 2)
+        _shape(t, name, (T, D))
+    pd = _norm_params(x, D, gamma=gamma, dgamma=dgamma, dbeta=dbeta)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _need(t, name, torch.float32, 1)
+        _shape(t, name, (T,))
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _same_device(x, dy=dy, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
+    _check("moe_layernorm_bwd", load().moe_layernorm_bwd(
+        _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), MOE_DTYPE[x.dtype], pd, _ptr(dx), _ptr(dgamma),
+        _ptr(dbeta), T, D, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream_handle(stream)))
+
+
+def moe_router_topk_fwd(logits, topk_ids, topk_scores, normalize: bool = True, stream=None) -> None:
+    """The K largest of each row of logits [T,E] (fp32 or bf16) into topk_ids [T,K] int32 and their scores
+    into topk_scores [T,K] fp32: the softmax over the chosen (normalize) or over all E experts."""
+    T, E = _rows(logits, "logits", (torch.float32, torch.bfloat16))
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    K = topk_ids.shape[1]
+    _shape(topk_ids, "topk_ids", (T, K))
+    _need(topk_scores, "topk_scores", torch.float32, 2)
+    _shape(topk_scores, "topk_scores", (T, K))
+    _same_device(logits, topk_ids=topk_ids, topk_scores=topk_scores)
+    _check("moe_router_topk_fwd", load().moe_router_topk_fwd(
+        _ptr(logits), MOE_DTYPE[logits.dtype], _ptr(topk_ids), _ptr(topk_scores), T, E, K, int(bool(normalize)),
+        _stream_handle(stream)))
+
+
+def moe_router_topk_bwd(logits, topk_ids, dscores, dlogits, normalize: bool = True, stream=None) -> None:
+    """dlogits [T,E] from dscores [T,K] (as moe_routed_experts_bwd writes them), for the logits, ids and
+    normalize of moe_router_topk_fwd."""
+    T, E = _rows(logits, "logits", (torch.float32, torch.bfloat16))
+    _need(topk_ids, "topk_ids", torch.int32, 2)
+    K = topk_ids.shape[1]
+    _shape(topk_ids, "topk_ids", (T, K))
+    _need(dscores, "dscores", torch.float32, 2)
+    _shape(dscores, "dscores", (T, K))
+    _need(dlogits, "dlogits", logits.dtype, 2)
+    _shape(dlogits, "dlogits", (T, E))
+    _same_device(logits, topk_ids=topk_ids, dscores=dscores, dlogits=dlogits)
+    _check("moe_router_topk_bwd", load().moe_router_topk_bwd(
+        _ptr(logits), MOE_DTYPE[logits.dtype], _ptr(topk_ids), _ptr(dscores), _ptr(dlogits), T, E, K,
+        int(bool(normalize)), _stream_handle(stream)))
+
+
+def moe_lm_workspace_bytes(T: int, D: int, V: int, K: int = 1) -> int:
+    """Workspace of the moe_lm_* calls; K is the number of teacher entries per row (1 for cross entropy)."""
+    return int(load().moe_lm_workspace_bytes(T, D, V, K))
+
+
+def _head(x, w, workspace, **vectors) -> tuple:
+    """Checks the operands every vocabulary loss takes, and fp32 [T] vectors. Returns T, D, V."""
+    T, D = _rows(x, "x", torch.bfloat16)
+    _need(w, "w", torch.bfloat16, 2)
+    V = w.shape[0]
+    _shape(w, "w", (V, D))
+    _need(workspace, "workspace", torch.uint8)
+    for name, t in vectors.items():
+        _need(t, name, torch.float32, 1)
+        _shape(t, name, (T,))
+    _same_device(x, w=w, workspace=workspace, **vectors)
+    return T, D, V
+
+
+def _head_targets(x, targets) -> None:
+    _need(targets, "targets", torch.int32, 1)
+    _shape(targets, "targets", (x.shape[0],))
+    _same_device(x, targets=targets)
+
+
+def _head_teacher(x, teacher_ids, teacher_logits) -> int:
+    _need(teacher_ids, "teacher_ids", torch.int32, 2)
+    K = teacher_ids.shape[1]
+    _shape(teacher_ids, "teacher_ids", (x.shape[0], K))
+    _need(teacher_logits, "teacher_logits", torch.float32, 2)
+    _shape(teacher_logits, "teacher_logits", (x.shape[0], K))
+    _same_device(x, teacher_ids=teacher_ids, teacher_logits=teacher_logits)
+    return K
+
+
+def _head_grads(x, w, dx, dw) -> None:
+    for name, g, of in (("dx", dx, x), ("dw", dw, w)):
+        if g is not None:
+            _need(g, name, torch.bfloat16, 2)
+            _shape(g, name, tuple(of.shape))
+            _same_device(x, **{name: g})
+
+
+def moe_lm_ce_fwd(x, w, targets, loss, lse, workspace, ignore_index: int = -100, stream=None) -> None:
+    """Softmax cross entropy of the head z = x w^T without keeping z: loss and lse [T] fp32 for x [T,D] and
+    w [V,D] (bf16) and targets [T] int32. Rows of ignore_index have loss 0; a target outside [0, V) sets
+    MOE_DEV_BAD_TARGET in the workspace's status word and counts as ignored."""
+    T, D, V = _head(x, w, workspace, loss=loss, lse=lse)
+    _head_targets(x, targets)
+    _check("moe_lm_ce_fwd", load().moe_lm_ce_fwd(
+        _ptr(x), _ptr(w), _ptr(targets), int(ignore_index), _ptr(loss), _ptr(lse), T, D, V, _ptr(workspace),
+        workspace.numel(), _stream_handle(stream)))
+
+
+def moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, workspace, ignore_index: int = -100, stream=None) -> None:
+    """dx [T,D] and dw [V,D] (bf16; either may be None) for the losses' gradients dloss [T] and the lse of
+    moe_lm_ce_fwd."""
+    T, D, V = _head(x, w, workspace, lse=lse, dloss=dloss)
+    _head_targets(x, targets)
+    _head_grads(x, w, dx, dw)
+    _check("moe_lm_ce_bwd", load().moe_lm_ce_bwd(
+        _ptr(x), _ptr(w), _ptr(targets), int(ignore_index), _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dw), T, D, V,
+        _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+
+
+def moe_lm_distill_fwd(x, w, teacher_ids, teacher_logits, loss, lse, workspace, temperature: float = 1.0,
+                       stream=None) -> None:
+    """tau^2 KL(p || q) of the head z = x w^T without keeping z: p is the softmax of a row's teacher_logits
+    [T,K] fp32 at the temperature over the entries with teacher_ids [T,K] int32 >= 0, q the softmax of z at
+    the temperature over the whole vocabulary. Rows without entries have loss 0."""
+    T, D, V = _head(x, w, workspace, loss=loss, lse=lse)
+    K = _head_teacher(x, teacher_ids, teacher_logits)
+    _check("moe_lm_distill_fwd", load().moe_lm_distill_fwd(
+        _ptr(x), _ptr(w), _ptr(teacher_ids), _ptr(teacher_logits), float(temperature), _ptr(loss), _ptr(lse), T, D, V,
+        K, _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+
+
+def moe_lm_distill_bwd(x, w, teacher_ids, teacher_logits, lse, dloss, dx, dw, workspace, temperature: float = 1.0,
+                       stream=None) -> None:
+    """dx [T,D] and dw [V,D] (bf16; either may be None) for the losses' gradients dloss [T] and the lse of
+    moe_lm_distill_fwd."""
+    T, D, V = _head(x, w, workspace, lse=lse, dloss=dloss)
+    K = _head_teacher(x, teacher_ids, teacher_logits)
+    _head_grads(x, w, dx, dw)
+    _check("moe_lm_distill_bwd", load().moe_lm_distill_bwd(
+        _ptr(x), _ptr(w), _ptr(teacher_ids), _ptr(teacher_logits), float(temperature), _ptr(lse), _ptr(dloss), _ptr(dx),
+        _ptr(dw), T, D, V, K, _ptr(workspace), workspace.numel(), _stream_handle(stream)))

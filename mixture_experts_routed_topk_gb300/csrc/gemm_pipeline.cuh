@@ -41,6 +41,8 @@
 // when warps write them). ta and tb point into the
 // kernel's array of four tensor maps (tb == ta + 1); a policy with more operands reads ta[2], ta[3].
 // Optional:
+//   using Args = ...                                     a struct derived from GemmArgs, for a policy
+//        with arguments of its own (default: GemmArgs)
 //   __device__ static bool acquire(const Tile&, const GemmArgs&, volatile int* abort)
 //        run by the producer before a tile's first load: waits (bounded) until data that other
 //        CTAs of the same grid produce for this tile is visible to TMA; false aborts the CTA.
@@ -242,6 +244,16 @@ struct GemmArgs {
     float act_scale_out;     // NVFP4: tensor scale used to quantize the epilogue's output
 };
 
+// A policy with arguments of its own derives them from GemmArgs and names them P::Args.
+template <class P, class = void>
+struct ArgsOf {
+    using type = GemmArgs;
+};
+template <class P>
+struct ArgsOf<P, std::void_t<typename P::Args>> {
+    using type = typename P::Args;
+};
+
 template <class P, class = void>
 struct HasAcquire : std::false_type {};
 template <class P>
@@ -369,7 +381,7 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
 
 template <class P>
 __global__ void __launch_bounds__(gemm_threads<typename ShapeOf<P>::type>(), 1)
-    k_grouped_gemm(const __grid_constant__ GemmMaps maps, const GemmArgs args) {
+    k_grouped_gemm(const __grid_constant__ GemmMaps maps, const typename ArgsOf<P>::type args) {
     using S = typename ShapeOf<P>::type;
     const CUtensorMap* tmap_a = &maps.m[0];
     const CUtensorMap* tmap_b = &maps.m[1];
@@ -710,7 +722,7 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t r
 int sm_count_grid(int64_t max_tiles, int sm_count);
 
 template <class P>
-moe_status_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, int grid, cudaStream_t stream) {
+moe_status_t launch_gemm(const GemmMaps& maps, const typename ArgsOf<P>::type& a, int grid, cudaStream_t stream) {
     constexpr size_t kGemmSmemBytes = gemm_smem_bytes<typename ShapeOf<P>::type>();
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
@@ -730,7 +742,7 @@ moe_status_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, int grid, cuda
 }
 
 template <class P>
-moe_status_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs& a, int grid,
+moe_status_t launch_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const typename ArgsOf<P>::type& a, int grid,
                          cudaStream_t stream) {
     GemmMaps maps{};
     maps.m[0] = ta;

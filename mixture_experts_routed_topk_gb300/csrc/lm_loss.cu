@@ -1,0 +1,731 @@
+// lm_loss.cu -- losses of a linear head over a large vocabulary, without keeping its logits:
+// softmax cross entropy, and distillation from a teacher's top logits. Forward and backward.
+//
+// For hidden rows x [T, D] and head weights W [V, D], with u = 1 / temperature (1 for cross entropy):
+//   z = u x W^T                                     [T, V], never stored
+//   lse_t = log sum_v exp(z_tv),   q = exp(z - lse)
+//   a row's targets are K pairs (vocabulary id, probability p): the label with p = 1, or the softmax
+//   of the teacher's kept logits at the temperature
+//   cross entropy  loss_t = lse_t - z_t,target
+//   distillation   loss_t = tau^2 sum_j p_j (log p_j - (z_tj - lse_t))
+//   backward       dl = c_t (q - sum_j p_j onehot_j),  c_t = dloss_t (cross entropy), tau dloss_t
+//                  dx = dl W,  dW = dl^T x
+// A row whose label is ignored, or none of whose teacher entries is kept, has loss 0 and c_t = 0.
+//
+// All products run on the tcgen05 pipeline of gemm_pipeline.cuh (bf16 operands, fp32 accumulation):
+//   forward: the epilogue reduces a 128 x 256 logit tile to one (maximum, sum of exponentials) per
+//     row and picks the targets' logits out of it; k_lm_join joins a row's tiles.
+//   backward: over pieces of the vocabulary that fit the workspace, the epilogue of the recomputed
+//     logits writes dl in bf16; two more products turn the piece into its rows of dW and its share
+//     of dx. dx is summed over pieces and over slices of the contraction in fp32 and rounded once.
+// Rounding dl to bf16 costs each term of dx and dW at most half a bf16 step, as much as rounding
+// the results; it is what lets the two products use the bf16 tensor cores.
+//
+// A row's targets are first sorted by id (k_lm_teacher), so that a tile finds its own with one
+// search, and each thread picks them out of the 32 logits that it holds in registers. Ids that repeat
+// in a row count once each, in order.
+#include <algorithm>
+#include <climits>
+
+#include "gemm_pipeline.cuh"
+#include "train_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNoTarget = INT_MAX;
+constexpr int kLmMaxK = 256;
+
+// 2^x through the hardware (at most 2 units in the last place; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The same with subnormal results: a probability below 2^-126 still has a gradient where it meets
+// large hidden values.
+__device__ __forceinline__ float exp2_full(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------------------------------ targets
+
+// Cross entropy: sid[t] = the label, or kNoTarget; coef[t] = dloss[t], or 0 (backward only).
+__global__ void __launch_bounds__(256) k_lm_labels(const int32_t* __restrict__ targets, int32_t ignore_index,
+                                                   int64_t T, int32_t V, const float* __restrict__ dloss,
+                                                   int32_t* __restrict__ sid, float* __restrict__ coef,
+                                                   uint32_t* __restrict__ status) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (t >= T) return;
+    const int32_t id = targets[t];
+    const bool ignored = id == ignore_index, inside = id >= 0 && id < V;
+    if (!ignored && !inside) atomicOr(status, MOE_DEV_BAD_TARGET);
+    const bool ok = !ignored && inside;
+    sid[t] = ok ? id : kNoTarget;
+    if (coef) coef[t] = ok ? dloss[t] : 0.0f;
+}
+
+// Distillation: one warp per row. sid / sp: the kept ids in ascending order (equal ids in the order
+// given) with their probabilities, then kNoTarget / 0. ent[t] = sum_j p_j log p_j. coef as above.
+// An entry with a negative id is not kept (its logit is not looked at).
+__global__ void __launch_bounds__(128)
+    k_lm_teacher(const int32_t* __restrict__ ids, const float* __restrict__ logits, int64_t T, int32_t K, int32_t V,
+                 float inv_tau, float tau, const float* __restrict__ dloss, int32_t* __restrict__ sid,
+                 float* __restrict__ sp, float* __restrict__ ent, float* __restrict__ coef,
+                 uint32_t* __restrict__ status) {
+    __shared__ int32_t s_id[4][kLmMaxK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (t >= T) return;  // whole warps
+    int32_t* row_id = s_id[warp];
+    float a[kLmMaxK / 32];
+    float m = -INFINITY;
+    int kept = 0;
+    bool bad = false, nan = false;
+#pragma unroll
+    for (int i = 0; i < kLmMaxK / 32; ++i) {
+        const int j = i * 32 + lane;
+        a[i] = -INFINITY;
+        if (j < K) {
+            const int32_t id = __ldg(ids + t * K + j);
+            const bool ok = id >= 0 && id < V;
+            bad = bad || id >= V;
+            row_id[j] = ok ? id : kNoTarget;
+            if (ok) {
+                a[i] = __ldg(logits + t * K + j) * inv_tau;
+                nan = nan || a[i] != a[i];
+                m = fmaxf(m, a[i]);
+                ++kept;
+            }
+        }
+    }
+    if (bad) atomicOr(status, MOE_DEV_BAD_TARGET);
+    __syncwarp();
+    nan = __any_sync(0xffffffffu, nan);
+    kept = __reduce_add_sync(0xffffffffu, kept);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // kept entries of -inf only have no distribution: the row counts as one without entries
+    const bool none = kept == 0 || (m == -INFINITY && !nan);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLmMaxK / 32; ++i) s += none ? 0.0f : expf(a[i] - m);
+    s = warp_sum(s);
+    const float log_s = logf(s);
+    float e = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLmMaxK / 32; ++i) {
+        const int j = i * 32 + lane;
+        if (j < K) {
+            const int32_t id = none ? kNoTarget : row_id[j];
+            const bool ok = id != kNoTarget;
+            const float p = ok ? expf(a[i] - m) / s : 0.0f;
+            if (ok && p != 0.0f) e += p * (a[i] - m - log_s);
+            int rank = 0;
+            for (int l = 0; l < K; ++l) {
+                const int32_t other = none ? kNoTarget : row_id[l];
+                rank += (other < id || (other == id && l < j)) ? 1 : 0;
+            }
+            sid[t * K + rank] = id;
+            sp[t * K + rank] = p;
+        }
+    }
+    e = warp_sum(e);
+    if (lane == 0) {
+        ent[t] = e;
+        if (coef) coef[t] = none ? 0.0f : tau * dloss[t];
+    }
+}
+
+// ------------------------------------------------------------------------------- tile policies
+
+struct LmArgs : GemmArgs {
+    int64_t T;
+    int32_t V;           // vocabulary (columns at and past it do not exist)
+    int32_t v0;          // first column of the piece
+    int32_t group;       // row tiles walked together along the columns
+    int32_t K;           // targets per row
+    const int32_t* sid;  // [T, K] sorted target ids
+    const float* sp;     // [T, K] their probabilities; null: 1
+    float* zt;           // [T, K] out: the targets' logits
+    float2* part;        // [ntiles][T] out: (maximum, sum) of the tile's exponentials, base 2
+    float inv_tau;
+    const float* lse;    // [T]
+    const float* coef;   // [T]
+    int32_t pitch;       // row length of the dl piece
+    int32_t kb_slice;    // K steps per slice of the contraction (dx)
+    bool accumulate;     // dx: add to the slice's sums instead of starting them
+    bool direct;         // dx: one slice and one piece, so the tile is the result
+};
+
+struct LmTile {
+    int32_t m, n, kblocks, slice;
+};
+
+// Row tiles in groups of a.group; within a group columns outermost, so that a group's rows of A stay
+// in L2 while B streams by once per group.
+__device__ __forceinline__ void grouped_mn(int32_t tile, const LmArgs& a, int32_t* m, int32_t* n) {
+    const int32_t per_group = a.group * a.ntiles;
+    const int32_t g = tile / per_group;
+    const int32_t r = tile - g * per_group;
+    const int32_t rows = min(a.group, a.mtiles - g * a.group);
+    *n = r / rows;
+    *m = g * a.group + r - *n * rows;
+}
+
+// The row's first sorted target at or past vocabulary id `first`.
+__device__ __forceinline__ int first_target(const int32_t* sid, int32_t K, int32_t first) {
+    int lo = 0, hi = K;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(sid + mid) < first) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A = x rows, B = W rows, both K-major; K = D.
+struct LmLogits {
+    using Args = LmArgs;
+    using Tile = LmTile;
+    static constexpr bool kAMnMajor = false, kBMnMajor = false;
+    static constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBRows);
+
+    __device__ static int32_t num_tiles(const Args& a) { return a.mtiles * a.ntiles; }
+    __device__ static Tile decode(int32_t tile, const Args& a) {
+        Tile t;
+        grouped_mn(tile, a, &t.m, &t.n);
+        t.kblocks = a.kblocks;
+        t.slice = 0;
+        return t;
+    }
+    __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
+                                const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
+        tma_load_2d(sa, ta, bar, kb * kBK, t.m * kBM);
+        tma_load_2d(sb, tb, bar, kb * kBK, a.v0 + t.n * kBN2);
+    }
+};
+
+// Forward: a tile's share of the row's softmax sum, and the targets' logits.
+struct LmLse : LmLogits {
+    __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4*, const Args& a) {
+        const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
+        const bool live = row < a.T;
+        const int32_t n0 = t.n * kBN2;
+        const float scale2 = a.inv_tau * kLog2e;
+        int j = 0;
+        int32_t next = kNoTarget;
+        const int32_t* sid = a.sid + row * a.K;
+        if (live) {
+            j = first_target(sid, a.K, n0);
+            if (j < a.K) next = __ldg(sid + j);
+        }
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < kBN2 / 32; ++c) {
+            const int32_t c0 = n0 + 32 * c;
+            if (c0 >= a.V) break;  // warp-uniform
+            __syncwarp();
+            uint32_t w[32];
+            tmem_ld_32cols(taddr + 32 * c, w);
+            tmem_ld_wait(w);
+            if (c0 + 32 > a.V) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c0 + i >= a.V) w[i] = __float_as_uint(-INFINITY);
+            }
+            while (next < c0 + 32) {
+                uint32_t z = 0u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (next == c0 + i) z = w[i];
+                a.zt[row * a.K + j] = __uint_as_float(z) * a.inv_tau;
+                ++j;
+                next = j < a.K ? __ldg(sid + j) : kNoTarget;
+            }
+            float cm = __uint_as_float(w[0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) cm = fmaxf(cm, __uint_as_float(w[i]));
+            const float top = fmaxf(m, cm * scale2);
+            const float base = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: its terms are 0
+            s *= exp2_fast(m - base);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s += exp2_fast(fmaf(__uint_as_float(w[i]), scale2, -base));
+            m = top;
+        }
+        if (live) a.part[static_cast<int64_t>(t.n) * a.T + row] = make_float2(m, s);
+    }
+};
+
+// Backward: the tile's dl in bf16 into the piece [T, pitch]; columns past the vocabulary get zeros.
+struct LmDlogits : LmLogits {
+    __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
+        const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
+        const bool live = row < a.T;
+        const int32_t n0 = a.v0 + t.n * kBN2;
+        const float scale2 = a.inv_tau * kLog2e;
+        float coef = 0.0f, lse2 = 0.0f;
+        int j = 0;
+        int32_t next = kNoTarget;
+        const int32_t* sid = a.sid + row * a.K;
+        if (live) {
+            coef = __ldg(a.coef + row);
+            lse2 = __ldg(a.lse + row) * kLog2e;
+            j = first_target(sid, a.K, n0);
+            if (j < a.K) next = __ldg(sid + j);
+        }
+        const bool zero = coef == 0.0f;
+#pragma unroll 1
+        for (int cp = 0; cp < kBN2 / 64; ++cp) {
+            uint32_t words[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int32_t c0 = n0 + 64 * cp + 32 * half;
+                __syncwarp();
+                uint32_t w[32];
+                tmem_ld_32cols(taddr + 64 * cp + 32 * half, w);
+                tmem_ld_wait(w);
+                float d[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    d[i] = coef * exp2_full(fmaf(__uint_as_float(w[i]), scale2, -lse2));
+                    if (zero || c0 + i >= a.V) d[i] = 0.0f;
+                }
+                while (next < c0 + 32) {
+                    const float p = coef * (a.sp ? __ldg(a.sp + row * a.K + j) : 1.0f);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (next == c0 + i) d[i] -= p;
+                    ++j;
+                    next = j < a.K ? __ldg(sid + j) : kNoTarget;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) words[16 * half + i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
+            }
+            __syncwarp();
+            warp_store_row_segments(
+                stage, words, reinterpret_cast<char*>(a.out0 + row * a.pitch + t.n * kBN2 + 64 * cp), live);
+        }
+    }
+};
+
+// This warp's 64 accumulator columns at taddr as packed bf16.
+__device__ __forceinline__ void tmem_bf16_64(uint32_t taddr, uint32_t (&words)[32]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+        uint32_t w[32];
+        tmem_ld_32cols(taddr + 32 * half, w);
+        tmem_ld_wait(w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            words[16 * half + i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+}
+
+// dx: A = dl piece rows (K-major, K = the piece's columns), B = W read MN-major as B[n = d][k = v].
+struct LmDx {
+    using Args = LmArgs;
+    using Tile = LmTile;
+    static constexpr bool kAMnMajor = false, kBMnMajor = true;
+    static constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBRows, false, true);
+
+    __device__ static int32_t num_tiles(const Args& a) {
+        return a.mtiles * a.ntiles * ((a.kblocks + a.kb_slice - 1) / a.kb_slice);
+    }
+    __device__ static Tile decode(int32_t tile, const Args& a) {
+        Tile t;
+        const int32_t per_slice = a.mtiles * a.ntiles;
+        t.slice = tile / per_slice;
+        grouped_mn(tile - t.slice * per_slice, a, &t.m, &t.n);
+        t.kblocks = min(a.kb_slice, a.kblocks - t.slice * a.kb_slice);
+        return t;
+    }
+    __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
+                                const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
+        const int32_t k = (t.slice * a.kb_slice + kb) * kBK;
+        tma_load_2d(sa, ta, bar, k, t.m * kBM);
+#pragma unroll
+        for (int j = 0; j < kBRows / 64; ++j)
+            tma_load_2d(sb + j * kMnBoxBytes, tb, bar, t.n * kBN2 + 64 * j, a.v0 + k);
+    }
+    __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
+        const int lane = threadIdx.x & 31;
+        const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
+        const bool live = row < a.T;
+        if (a.direct) {
+#pragma unroll 1
+            for (int cp = 0; cp < kBN2 / 64; ++cp) {
+                uint32_t words[32];
+                tmem_bf16_64(taddr + 64 * cp, words);
+                const int32_t d0 = t.n * kBN2 + 64 * cp;
+                warp_store_row_segments(stage, words, reinterpret_cast<char*>(a.out0 + row * a.D + d0),
+                                        live && d0 < a.D);
+            }
+            return;
+        }
+        float* sums = a.fout + static_cast<int64_t>(t.slice) * a.T * a.D;
+#pragma unroll 1
+        for (int c = 0; c < kBN2 / 32; ++c) {
+            const int32_t d0 = t.n * kBN2 + 32 * c;
+            if (d0 >= a.D) break;  // warp-uniform
+            uint32_t before[32];
+            if (a.accumulate) {  // this warp's 32 rows of 32 sums, in whole 128-byte row segments
+                const int64_t row0 = row - lane;
+                uint4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int64_t r = row0 + 4 * q + (lane >> 3);
+                    v[q] = r < a.T ? __ldcg(reinterpret_cast<const uint4*>(sums + r * a.D + d0) + (lane & 7))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) stage[(4 * q + (lane >> 3)) * kStageRowU4 + (lane & 7)] = v[q];
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint4 x = stage[lane * kStageRowU4 + q];
+                    before[4 * q] = x.x, before[4 * q + 1] = x.y, before[4 * q + 2] = x.z, before[4 * q + 3] = x.w;
+                }
+            }
+            __syncwarp();
+            uint32_t w[32];
+            tmem_ld_32cols(taddr + 32 * c, w);
+            tmem_ld_wait(w);
+            if (a.accumulate) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(before[i]));
+            }
+            warp_store_row_segments(stage, w, reinterpret_cast<char*>(sums + row * a.D + d0), live);
+        }
+    }
+};
+
+// dW: A = dl^T (MN-major: vocabulary contiguous), B = x (MN-major: d contiguous); K = T. TMA returns
+// zeros for rows past T, so the contraction needs no padding.
+struct LmDw {
+    using Args = LmArgs;
+    using Tile = LmTile;
+    static constexpr bool kAMnMajor = true, kBMnMajor = true;
+    static constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBRows, true, true);
+
+    __device__ static int32_t num_tiles(const Args& a) { return a.mtiles * a.ntiles; }
+    __device__ static Tile decode(int32_t tile, const Args& a) { return LmLogits::decode(tile, a); }
+    __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
+                                const CUtensorMap* ta, const CUtensorMap* tb, const Args&) {
+#pragma unroll
+        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * kMnBoxBytes, ta, bar, t.m * kBM + 64 * j, kb * kBK);
+#pragma unroll
+        for (int j = 0; j < kBRows / 64; ++j)
+            tma_load_2d(sb + j * kMnBoxBytes, tb, bar, t.n * kBN2 + 64 * j, kb * kBK);
+    }
+    __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
+        const int64_t v = static_cast<int64_t>(a.v0) + t.m * kBM + row_in_tile;
+#pragma unroll 1
+        for (int cp = 0; cp < kBN2 / 64; ++cp) {
+            uint32_t words[32];
+            tmem_bf16_64(taddr + 64 * cp, words);
+            const int32_t d0 = t.n * kBN2 + 64 * cp;
+            warp_store_row_segments(stage, words, reinterpret_cast<char*>(a.out0 + v * a.D + d0),
+                                    v < a.V && d0 < a.D);
+        }
+    }
+};
+
+// --------------------------------------------------------------------------------- reductions
+
+// Joins a row's tiles and forms its loss. A block owns 32 rows, one per lane; its warps take the
+// tiles in turn and meet in shared memory in warp order.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    k_lm_join(const float2* __restrict__ part, int32_t ntiles, int64_t T, int32_t K, const int32_t* __restrict__ sid,
+              const float* __restrict__ sp, const float* __restrict__ zt, const float* __restrict__ ent, float tau,
+              float* __restrict__ loss, float* __restrict__ lse_out) {
+    __shared__ float2 acc[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    griddep_wait();
+    griddep_launch_dependents();
+    float m = -INFINITY, s = 0.0f;
+    if (row < T) {
+        for (int n = warp; n < ntiles; n += kJoinWarps) {
+            const float2 p = part[static_cast<int64_t>(n) * T + row];
+            const float top = fmaxf(m, p.x);
+            s = (s == 0.0f ? 0.0f : s * exp2_fast(m - top)) + (p.y == 0.0f ? 0.0f : p.y * exp2_fast(p.x - top));
+            m = top;
+        }
+    }
+    acc[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0 || row >= T) return;
+    float top = acc[0][lane].x;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, acc[w][lane].x);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+        if (acc[w][lane].y != 0.0f) s += acc[w][lane].y * exp2_fast(acc[w][lane].x - top);
+    const float lse = kLn2 * top + logf(s);
+    lse_out[row] = lse;
+    const int32_t* my_sid = sid + row * K;
+    if (sp == nullptr) {
+        loss[row] = my_sid[0] == kNoTarget ? 0.0f : lse - zt[row];
+        return;
+    }
+    float l = 0.0f;
+    bool any = false;
+    for (int j = 0; j < K; ++j) {
+        if (my_sid[j] == kNoTarget) break;
+        any = true;
+        const float p = sp[row * K + j];
+        if (p != 0.0f) l += p * (lse - zt[row * K + j]);
+    }
+    loss[row] = any ? tau * tau * (ent[row] + l) : 0.0f;
+}
+
+// dx = bf16( sum over slices in slice order ).
+__global__ void __launch_bounds__(256) k_lm_sum_slices(const float4* __restrict__ sums, int32_t slices, int64_t n4,
+                                                       uint2* __restrict__ dx) {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        float4 a = sums[i];
+        for (int s = 1; s < slices; ++s) {
+            const float4 b = sums[s * n4 + i];
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+        }
+        dx[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    }
+}
+
+// ---------------------------------------------------------------------------------------- plan
+
+constexpr size_t kRegionAlign = 256;
+constexpr int kPlanSms = 152;                 // SMs of the GB300, for sizes that must not depend on the device
+constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of one dl piece
+constexpr int32_t kMinPiece = 2048;           // but at least this many columns
+
+struct LmPlan {
+    int32_t mtiles, ntiles;  // of the logits
+    int32_t piece;           // columns per piece of the backward (a multiple of 256)
+    int32_t dx_ntiles;
+    int32_t slices, kb_slice;
+    bool direct;
+    size_t off_sid, off_sp, off_zt, off_ent, off_coef, off_part, off_dl, off_sums, total;
+};
+
+// Slices of dx's contraction: a grid of few tiles leaves SMs idle, and each slice costs a round of
+// fp32 sums. The time of s slices is taken as the K steps of the busiest SM (0.35 us each) plus
+// the sums' traffic at 6 TB/s.
+int32_t pick_slices(int64_t tiles, int32_t kblocks, double sum_bytes) {
+    int32_t best = 1;
+    double best_t = 1e30;
+    for (int32_t s = 1; s <= 64 && s <= kblocks; ++s) {
+        const int32_t kb = (kblocks + s - 1) / s;
+        if ((kblocks + kb - 1) / kb != s) continue;
+        const double t =
+            0.35 * static_cast<double>(ceil_div(tiles * s, kPlanSms)) * kb + (s > 1 ? s * sum_bytes / 6e6 : 0.0);
+        if (t < best_t) best_t = t, best = s;
+    }
+    return best;
+}
+
+void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
+    p->mtiles = static_cast<int32_t>(ceil_div(T, kBM));
+    p->ntiles = static_cast<int32_t>(ceil_div(V, kBN2));
+    int64_t piece = kPieceBytes / (2 * T) / kBN2 * kBN2;
+    piece = std::max<int64_t>(piece, kMinPiece);
+    piece = std::min<int64_t>(piece, static_cast<int64_t>(p->ntiles) * kBN2);
+    const int64_t pieces = ceil_div(static_cast<int64_t>(p->ntiles) * kBN2, piece);
+    piece = ceil_div(p->ntiles, pieces) * kBN2;  // pieces of equal size
+    p->piece = static_cast<int32_t>(piece);
+    p->dx_ntiles = static_cast<int32_t>(ceil_div(D, kBN2));
+    const int32_t kblocks = p->piece / kBK;
+    p->slices = pick_slices(static_cast<int64_t>(p->mtiles) * p->dx_ntiles, kblocks, 8.0 * T * D);
+    p->kb_slice = (kblocks + p->slices - 1) / p->slices;
+    p->direct = p->slices == 1 && p->piece >= V;
+    size_t off = kRegionAlign;  // the status word
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + kRegionAlign - 1) / kRegionAlign * kRegionAlign;
+        return at;
+    };
+    const size_t t = static_cast<size_t>(T), tk = t * K;
+    p->off_sid = take(4 * tk);
+    p->off_sp = take(4 * tk);
+    p->off_zt = take(4 * tk);
+    p->off_ent = take(4 * t);
+    p->off_coef = take(4 * t);
+    // the forward's partials and the backward's buffers are never alive at once
+    const size_t shared = off;
+    p->off_part = take(8 * t * p->ntiles);
+    const size_t fwd_end = off;
+    off = shared;
+    p->off_dl = take(2 * t * p->piece);
+    p->off_sums = off;
+    if (!p->direct) p->off_sums = take(4 * t * D * p->slices);
+    p->total = std::max(off, fwd_end);
+}
+
+bool sizes_ok(int64_t T, int32_t D, int32_t V, int32_t K) {
+    if (T <= 0 || D <= 0 || V <= 0 || K <= 0 || K > kLmMaxK || D % 64 != 0) return false;
+    if (T >= (int64_t{1} << 31) || V > (1 << 30)) return false;
+    // tile indices are 32-bit
+    const int64_t mt = ceil_div(T, kBM), nt = ceil_div(V, kBN2), dt = ceil_div(D, kBN2);
+    return mt * nt < (int64_t{1} << 31) && mt * dt * 64 < (int64_t{1} << 31) && 2 * nt * dt < (int64_t{1} << 31);
+}
+
+template <typename P>
+P* at(const LmProblem& p, size_t off) {
+    return reinterpret_cast<P*>(p.ws + off);
+}
+
+// Row tiles walked together: their rows of x (or dl) should take about a quarter of the 129 MB L2.
+int32_t row_group(int64_t row_bytes, int32_t mtiles) {
+    const int64_t g = (32ll << 20) / (row_bytes * kBM);
+    return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(g, mtiles)));
+}
+
+moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward, cudaStream_t stream) {
+    uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
+    if (cudaMemsetAsync(status, 0, sizeof(uint32_t), stream) != cudaSuccess) return MOE_ERR_CUDA;
+    float* coef = backward ? at<float>(p, pl.off_coef) : nullptr;
+    cudaError_t e;
+    if (p.teacher_ids == nullptr)
+        e = launch_pdl(k_lm_labels, dim3(static_cast<unsigned>(ceil_div(p.T, 256))), dim3(256), 0, stream, p.targets,
+                       p.ignore_index, p.T, p.V, p.dloss, at<int32_t>(p, pl.off_sid), coef, status);
+    else
+        e = launch_pdl(k_lm_teacher, dim3(static_cast<unsigned>(ceil_div(p.T, 4))), dim3(128), 0, stream,
+                       p.teacher_ids, p.teacher_logits, p.T, p.K, p.V, 1.0f / p.temperature, p.temperature, p.dloss,
+                       at<int32_t>(p, pl.off_sid), at<float>(p, pl.off_sp), at<float>(p, pl.off_ent), coef, status);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
+    LmArgs a{};
+    a.T = p.T;
+    a.D = p.D;
+    a.V = p.V;
+    a.K = p.K;
+    a.sid = at<int32_t>(p, pl.off_sid);
+    a.sp = p.teacher_ids ? at<float>(p, pl.off_sp) : nullptr;
+    a.inv_tau = 1.0f / p.temperature;
+    a.status = reinterpret_cast<uint32_t*>(p.ws);
+    return a;
+}
+
+}  // namespace
+
+size_t lm_workspace_bytes(int64_t T, int32_t D, int32_t V, int32_t K) {
+    if (!sizes_ok(T, D, V, K)) return 0;
+    LmPlan pl{};
+    make_plan(T, D, V, K, &pl);
+    return pl.total;
+}
+
+moe_status_t launch_lm_fwd(const LmProblem& p, cudaStream_t stream) {
+    LmPlan pl{};
+    make_plan(p.T, p.D, p.V, p.K, &pl);
+    CUtensorMap tx, tw;
+    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2)) return MOE_ERR_CUDA;
+    moe_status_t st = prepare_targets(p, pl, false, stream);
+    if (st != MOE_OK) return st;
+    LmArgs a = common_args(p, pl);
+    a.mtiles = pl.mtiles;
+    a.ntiles = pl.ntiles;
+    a.kblocks = p.D / kBK;
+    a.group = row_group(2ll * p.D, pl.mtiles);
+    a.zt = at<float>(p, pl.off_zt);
+    a.part = at<float2>(p, pl.off_part);
+    st = launch_gemm<LmLse>(tx, tw, a, sm_count_grid(static_cast<int64_t>(pl.mtiles) * pl.ntiles, p.sm_count), stream);
+    if (st != MOE_OK) return st;
+    return launch_pdl(k_lm_join, dim3(static_cast<unsigned>(ceil_div(p.T, 32))), dim3(32 * kJoinWarps), 0, stream,
+                      static_cast<const float2*>(a.part), pl.ntiles, p.T, p.K, a.sid, a.sp,
+                      static_cast<const float*>(a.zt), static_cast<const float*>(at<float>(p, pl.off_ent)),
+                      p.temperature, p.loss, p.lse) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
+    LmPlan pl{};
+    make_plan(p.T, p.D, p.V, p.K, &pl);
+    __nv_bfloat16* dl = at<__nv_bfloat16>(p, pl.off_dl);
+    float* sums = at<float>(p, pl.off_sums);
+    CUtensorMap tx, tw, tdl, tw_mn, tdl_mn, tx_mn;
+    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2) ||
+        !make_tmap(&tdl, dl, pl.piece, p.T, kBK, kBM) || !make_tmap(&tw_mn, p.w, p.D, p.V, 64, kBK) ||
+        !make_tmap(&tdl_mn, dl, pl.piece, p.T, 64, kBK) || !make_tmap(&tx_mn, p.x, p.D, p.T, 64, kBK))
+        return MOE_ERR_CUDA;
+    moe_status_t st = prepare_targets(p, pl, true, stream);
+    if (st != MOE_OK) return st;
+    int32_t slices_used = 0;
+    for (int64_t at_v = 0; at_v < p.V; at_v += pl.piece) {
+        const int32_t v0 = static_cast<int32_t>(at_v);
+        const int32_t cols =
+            static_cast<int32_t>(std::min<int64_t>(pl.piece, ceil_div(p.V - at_v, kBN2) * kBN2));
+        LmArgs a = common_args(p, pl);
+        a.v0 = v0;
+        a.pitch = pl.piece;
+        a.lse = p.lse_in;
+        a.coef = at<float>(p, pl.off_coef);
+        a.mtiles = pl.mtiles;
+        a.ntiles = cols / kBN2;
+        a.kblocks = p.D / kBK;
+        a.group = row_group(2ll * p.D, pl.mtiles);
+        a.out0 = dl;
+        st = launch_gemm<LmDlogits>(tx, tw, a, sm_count_grid(static_cast<int64_t>(a.mtiles) * a.ntiles, p.sm_count),
+                                    stream);
+        if (st != MOE_OK) return st;
+        if (p.dx) {
+            LmArgs b = a;
+            b.ntiles = pl.dx_ntiles;
+            b.kblocks = cols / kBK;
+            b.kb_slice = pl.kb_slice;
+            b.group = row_group(2ll * pl.kb_slice * kBK, pl.mtiles);
+            b.direct = pl.direct;
+            b.accumulate = v0 > 0;
+            b.out0 = static_cast<__nv_bfloat16*>(p.dx);
+            b.fout = sums;
+            // the first piece is a whole one and starts every slice's sums; a shorter last piece adds to fewer
+            const int32_t slices = static_cast<int32_t>(ceil_div(b.kblocks, b.kb_slice));
+            slices_used = std::max(slices_used, slices);
+            st = launch_gemm<LmDx>(tdl, tw_mn, b,
+                                   sm_count_grid(static_cast<int64_t>(b.mtiles) * b.ntiles * slices, p.sm_count),
+                                   stream);
+            if (st != MOE_OK) return st;
+        }
+        if (p.dw) {
+            LmArgs c = a;
+            c.mtiles = cols / kBM;
+            c.ntiles = pl.dx_ntiles;
+            c.kblocks = static_cast<int32_t>(ceil_div(p.T, kBK));
+            c.group = row_group(2ll * p.T, c.mtiles);
+            c.out0 = static_cast<__nv_bfloat16*>(p.dw);
+            st = launch_gemm<LmDw>(tdl_mn, tx_mn, c,
+                                   sm_count_grid(static_cast<int64_t>(c.mtiles) * c.ntiles, p.sm_count), stream);
+            if (st != MOE_OK) return st;
+        }
+    }
+    if (p.dx && !pl.direct) {
+        const int64_t n4 = p.T * p.D / 4;
+        const int64_t grid = std::min<int64_t>(ceil_div(n4, 256), 16ll * p.sm_count);
+        if (launch_pdl(k_lm_sum_slices, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream,
+                       reinterpret_cast<const float4*>(sums), slices_used, n4, static_cast<uint2*>(p.dx)) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+}  // namespace moe
