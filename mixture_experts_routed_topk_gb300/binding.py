@@ -53,6 +53,8 @@ def library_path() -> str:
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the library (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -606,51 +608,76 @@ def moe_fwd_nvfp4_stages(x, topk_ids, topk_scores, w13_nv, w2_nv, out, workspace
 
 
 # ------------------------------------------------- layer norm, router and vocabulary losses
+#
+# These calls are short on the GPU (a few microseconds at the smallest sizes), so their checks are too:
+# one comparison per property and tensor, and the words for a refusal only once it is one.
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+def _refuse(t, name: str, dtype, shape, device: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != len(shape):
+        raise ValueError(f"{name} must have {len(shape)} dims, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _shape(t: torch.Tensor, name: str, shape: tuple) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _operand(t, name: str, dtype, shape, device: int) -> int:
+    """The device pointer of a contiguous tensor of this dtype, shape and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
 
 
-def _rows(x, name: str, dtypes) -> tuple:
-    _need(x, name, dtypes, 2)
-    return tuple(x.shape)
+def _rows(x, name: str, dtypes):
+    """T, D, device and pointer of a contiguous [T, D] tensor of one of the dtypes."""
+    if isinstance(x, torch.Tensor) and x.dtype in dtypes and x.dim() == 2 and x.is_cuda and x.is_contiguous():
+        T, D = x.shape
+        return T, D, x.get_device(), x.data_ptr()
+    _need(x, name, tuple(dtypes), 2)
 
 
-def _norm_params(x, D: int, **params) -> int:
-    """Checks the given [D] parameters (None is allowed) and returns their common MOE_DTYPE."""
-    dtype = None
-    for name, p in params.items():
+def _workspace(t, device: int) -> int:
+    return _operand(t, "workspace", torch.uint8, (t.numel(),) if isinstance(t, torch.Tensor) else (0,), device)
+
+
+def _current_stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _norm_params(x, D: int, device: int, *params):
+    """The common MOE_DTYPE of the (name, [D] tensor or None) pairs, and their pointers (0 for None)."""
+    dtype, ptrs = None, []
+    for name, p in params:
         if p is None:
+            ptrs.append(0)
             continue
-        _need(p, name, tuple(MOE_DTYPE), 1)
-        _shape(p, name, (D,))
-        if dtype is not None and p.dtype != dtype:
-            raise TypeError(f"{name} must have the dtype of the other parameters, {dtype}, got {p.dtype}")
-        dtype = p.dtype
-    return MOE_DTYPE[dtype if dtype is not None else x.dtype]
+        if dtype is None:
+            if not isinstance(p, torch.Tensor) or p.dtype not in MOE_DTYPE:
+                _need(p, name, tuple(MOE_DTYPE), 1)
+            dtype = p.dtype
+        ptrs.append(_operand(p, name, dtype, (D,), device))
+    return MOE_DTYPE[dtype if dtype is not None else x.dtype], ptrs
 
 
 def moe_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps: float = 1e-5, stream=None) -> None:
     """Layer norm of the rows of x [T,D] (fp32, bf16 or fp16) into y; mean and rstd [T] fp32 are kept for
     the backward pass. gamma and beta [D] may be None (1 and 0), and have one dtype of their own. y may be x."""
-    T, D = _rows(x, "x", tuple(MOE_DTYPE))
-    _need(y, "y", x.dtype, 2)
-    _shape(y, "y", (T, D))
-    pd = _norm_params(x, D, gamma=gamma, beta=beta)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _need(t, name, torch.float32, 1)
-        _shape(t, name, (T,))
-    _same_device(x, gamma=gamma, beta=beta, y=y, mean=mean, rstd=rstd)
+    T, D, dev, px = _rows(x, "x", MOE_DTYPE)
+    pd, (pg, pb) = _norm_params(x, D, dev, ("gamma", gamma), ("beta", beta))
     _check("moe_layernorm_fwd", load().moe_layernorm_fwd(
-        _ptr(x), _ptr(gamma), _ptr(beta), MOE_DTYPE[x.dtype], pd, _ptr(y), _ptr(mean), _ptr(rstd), T, D, float(eps),
-        _stream_handle(stream)))
+        px, pg, pb, MOE_DTYPE[x.dtype], pd, _operand(y, "y", x.dtype, (T, D), dev),
+        _operand(mean, "mean", torch.float32, (T,), dev), _operand(rstd, "rstd", torch.float32, (T,), dev), T, D,
+        float(eps), _current_stream(stream)))
 
 
 def moe_layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
@@ -659,53 +686,44 @@ def moe_layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
 
 def moe_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream=None) -> None:
     """Layer norm's backward pass: dx, and dgamma and dbeta (either may be None) in the parameters' dtype.
-    The workspace is moe_layernorm_bwd_workspace_bytes(T, D) bytes (None when neither is wanted)."""
-    T, D = _rows(x, "x", tuple(MOE_DTYPE))
-    for name, t in (("dy", dy), ("dx", dx)):
-        _need(t, name, x.dtype, 2)
-        _shape(t, name, (T, D))
-    pd = _norm_params(x, D, gamma=gamma, dgamma=dgamma, dbeta=dbeta)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _need(t, name, torch.float32, 1)
-        _shape(t, name, (T,))
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8)
-    _same_device(x, dy=dy, gamma=gamma, mean=mean, rstd=rstd, dx=dx, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
+    The workspace is moe_layernorm_bwd_workspace_bytes(T, D) bytes (None when neither is wanted). dx may be dy or x."""
+    T, D, dev, px = _rows(x, "x", MOE_DTYPE)
+    pd, (pg, pdg, pdb) = _norm_params(x, D, dev, ("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta))
     _check("moe_layernorm_bwd", load().moe_layernorm_bwd(
-        _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), MOE_DTYPE[x.dtype], pd, _ptr(dx), _ptr(dgamma),
-        _ptr(dbeta), T, D, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream_handle(stream)))
+        _operand(dy, "dy", x.dtype, (T, D), dev), px, pg, _operand(mean, "mean", torch.float32, (T,), dev),
+        _operand(rstd, "rstd", torch.float32, (T,), dev), MOE_DTYPE[x.dtype], pd,
+        _operand(dx, "dx", x.dtype, (T, D), dev), pdg, pdb, T, D, 0 if workspace is None else _workspace(workspace, dev),
+        0 if workspace is None else workspace.numel(), _current_stream(stream)))
+
+
+_LOGIT_DTYPES = (torch.float32, torch.bfloat16)
+
+
+def _choices(topk_ids, T: int, dev: int):
+    """K and the pointer of topk_ids [T, K]."""
+    K = topk_ids.shape[1] if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
+    return K, _operand(topk_ids, "topk_ids", torch.int32, (T, K), dev)
 
 
 def moe_router_topk_fwd(logits, topk_ids, topk_scores, normalize: bool = True, stream=None) -> None:
     """The K largest of each row of logits [T,E] (fp32 or bf16) into topk_ids [T,K] int32 and their scores
     into topk_scores [T,K] fp32: the softmax over the chosen (normalize) or over all E experts."""
-    T, E = _rows(logits, "logits", (torch.float32, torch.bfloat16))
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    K = topk_ids.shape[1]
-    _shape(topk_ids, "topk_ids", (T, K))
-    _need(topk_scores, "topk_scores", torch.float32, 2)
-    _shape(topk_scores, "topk_scores", (T, K))
-    _same_device(logits, topk_ids=topk_ids, topk_scores=topk_scores)
+    T, E, dev, pz = _rows(logits, "logits", _LOGIT_DTYPES)
+    K, pi = _choices(topk_ids, T, dev)
     _check("moe_router_topk_fwd", load().moe_router_topk_fwd(
-        _ptr(logits), MOE_DTYPE[logits.dtype], _ptr(topk_ids), _ptr(topk_scores), T, E, K, int(bool(normalize)),
-        _stream_handle(stream)))
+        pz, MOE_DTYPE[logits.dtype], pi, _operand(topk_scores, "topk_scores", torch.float32, (T, K), dev), T, E, K,
+        1 if normalize else 0, _current_stream(stream)))
 
 
 def moe_router_topk_bwd(logits, topk_ids, dscores, dlogits, normalize: bool = True, stream=None) -> None:
     """dlogits [T,E] from dscores [T,K] (as moe_routed_experts_bwd writes them), for the logits, ids and
     normalize of moe_router_topk_fwd."""
-    T, E = _rows(logits, "logits", (torch.float32, torch.bfloat16))
-    _need(topk_ids, "topk_ids", torch.int32, 2)
-    K = topk_ids.shape[1]
-    _shape(topk_ids, "topk_ids", (T, K))
-    _need(dscores, "dscores", torch.float32, 2)
-    _shape(dscores, "dscores", (T, K))
-    _need(dlogits, "dlogits", logits.dtype, 2)
-    _shape(dlogits, "dlogits", (T, E))
-    _same_device(logits, topk_ids=topk_ids, dscores=dscores, dlogits=dlogits)
+    T, E, dev, pz = _rows(logits, "logits", _LOGIT_DTYPES)
+    K, pi = _choices(topk_ids, T, dev)
     _check("moe_router_topk_bwd", load().moe_router_topk_bwd(
-        _ptr(logits), MOE_DTYPE[logits.dtype], _ptr(topk_ids), _ptr(dscores), _ptr(dlogits), T, E, K,
-        int(bool(normalize)), _stream_handle(stream)))
+        pz, MOE_DTYPE[logits.dtype], pi, _operand(dscores, "dscores", torch.float32, (T, K), dev),
+        _operand(dlogits, "dlogits", logits.dtype, (T, E), dev), T, E, K, 1 if normalize else 0,
+        _current_stream(stream)))
 
 
 def moe_lm_workspace_bytes(T: int, D: int, V: int, K: int = 1) -> int:
@@ -713,64 +731,49 @@ def moe_lm_workspace_bytes(T: int, D: int, V: int, K: int = 1) -> int:
     return int(load().moe_lm_workspace_bytes(T, D, V, K))
 
 
-def _head(x, w, workspace, **vectors) -> tuple:
-    """Checks the operands every vocabulary loss takes, and fp32 [T] vectors. Returns T, D, V."""
-    T, D = _rows(x, "x", torch.bfloat16)
-    _need(w, "w", torch.bfloat16, 2)
-    V = w.shape[0]
-    _shape(w, "w", (V, D))
-    _need(workspace, "workspace", torch.uint8)
-    for name, t in vectors.items():
-        _need(t, name, torch.float32, 1)
-        _shape(t, name, (T,))
-    _same_device(x, w=w, workspace=workspace, **vectors)
-    return T, D, V
+_BF16 = (torch.bfloat16,)
 
 
-def _head_targets(x, targets) -> None:
-    _need(targets, "targets", torch.int32, 1)
-    _shape(targets, "targets", (x.shape[0],))
-    _same_device(x, targets=targets)
+def _head(x, w):
+    """T, D, V, device and the pointers of x [T, D] and w [V, D]."""
+    T, D, dev, px = _rows(x, "x", _BF16)
+    V = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else 0
+    return T, D, V, dev, px, _operand(w, "w", torch.bfloat16, (V, D), dev)
 
 
-def _head_teacher(x, teacher_ids, teacher_logits) -> int:
-    _need(teacher_ids, "teacher_ids", torch.int32, 2)
-    K = teacher_ids.shape[1]
-    _shape(teacher_ids, "teacher_ids", (x.shape[0], K))
-    _need(teacher_logits, "teacher_logits", torch.float32, 2)
-    _shape(teacher_logits, "teacher_logits", (x.shape[0], K))
-    _same_device(x, teacher_ids=teacher_ids, teacher_logits=teacher_logits)
-    return K
+def _teacher(teacher_ids, teacher_logits, T: int, dev: int):
+    """K and the pointers of teacher_ids and teacher_logits [T, K]."""
+    K = teacher_ids.shape[1] if isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2 else 0
+    return (K, _operand(teacher_ids, "teacher_ids", torch.int32, (T, K), dev),
+            _operand(teacher_logits, "teacher_logits", torch.float32, (T, K), dev))
 
 
-def _head_grads(x, w, dx, dw) -> None:
-    for name, g, of in (("dx", dx, x), ("dw", dw, w)):
-        if g is not None:
-            _need(g, name, torch.bfloat16, 2)
-            _shape(g, name, tuple(of.shape))
-            _same_device(x, **{name: g})
+def _vector(t, name: str, T: int, dev: int) -> int:
+    return _operand(t, name, torch.float32, (T,), dev)
+
+
+def _grad(t, name: str, shape, dev: int) -> int:
+    return 0 if t is None else _operand(t, name, torch.bfloat16, shape, dev)
 
 
 def moe_lm_ce_fwd(x, w, targets, loss, lse, workspace, ignore_index: int = -100, stream=None) -> None:
     """Softmax cross entropy of the head z = x w^T without keeping z: loss and lse [T] fp32 for x [T,D] and
     w [V,D] (bf16) and targets [T] int32. Rows of ignore_index have loss 0; a target outside [0, V) sets
     MOE_DEV_BAD_TARGET in the workspace's status word and counts as ignored."""
-    T, D, V = _head(x, w, workspace, loss=loss, lse=lse)
-    _head_targets(x, targets)
+    T, D, V, dev, px, pw = _head(x, w)
     _check("moe_lm_ce_fwd", load().moe_lm_ce_fwd(
-        _ptr(x), _ptr(w), _ptr(targets), int(ignore_index), _ptr(loss), _ptr(lse), T, D, V, _ptr(workspace),
-        workspace.numel(), _stream_handle(stream)))
+        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(loss, "loss", T, dev),
+        _vector(lse, "lse", T, dev), T, D, V, _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
 
 
 def moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, workspace, ignore_index: int = -100, stream=None) -> None:
     """dx [T,D] and dw [V,D] (bf16; either may be None) for the losses' gradients dloss [T] and the lse of
     moe_lm_ce_fwd."""
-    T, D, V = _head(x, w, workspace, lse=lse, dloss=dloss)
-    _head_targets(x, targets)
-    _head_grads(x, w, dx, dw)
+    T, D, V, dev, px, pw = _head(x, w)
     _check("moe_lm_ce_bwd", load().moe_lm_ce_bwd(
-        _ptr(x), _ptr(w), _ptr(targets), int(ignore_index), _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dw), T, D, V,
-        _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(lse, "lse", T, dev),
+        _vector(dloss, "dloss", T, dev), _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V,
+        _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
 
 
 def moe_lm_distill_fwd(x, w, teacher_ids, teacher_logits, loss, lse, workspace, temperature: float = 1.0,
@@ -778,20 +781,20 @@ def moe_lm_distill_fwd(x, w, teacher_ids, teacher_logits, loss, lse, workspace, 
     """tau^2 KL(p || q) of the head z = x w^T without keeping z: p is the softmax of a row's teacher_logits
     [T,K] fp32 at the temperature over the entries with teacher_ids [T,K] int32 >= 0, q the softmax of z at
     the temperature over the whole vocabulary. Rows without entries have loss 0."""
-    T, D, V = _head(x, w, workspace, loss=loss, lse=lse)
-    K = _head_teacher(x, teacher_ids, teacher_logits)
+    T, D, V, dev, px, pw = _head(x, w)
+    K, pi, pl = _teacher(teacher_ids, teacher_logits, T, dev)
     _check("moe_lm_distill_fwd", load().moe_lm_distill_fwd(
-        _ptr(x), _ptr(w), _ptr(teacher_ids), _ptr(teacher_logits), float(temperature), _ptr(loss), _ptr(lse), T, D, V,
-        K, _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+        px, pw, pi, pl, float(temperature), _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev), T, D, V, K,
+        _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
 
 
 def moe_lm_distill_bwd(x, w, teacher_ids, teacher_logits, lse, dloss, dx, dw, workspace, temperature: float = 1.0,
                        stream=None) -> None:
     """dx [T,D] and dw [V,D] (bf16; either may be None) for the losses' gradients dloss [T] and the lse of
     moe_lm_distill_fwd."""
-    T, D, V = _head(x, w, workspace, lse=lse, dloss=dloss)
-    K = _head_teacher(x, teacher_ids, teacher_logits)
-    _head_grads(x, w, dx, dw)
+    T, D, V, dev, px, pw = _head(x, w)
+    K, pi, pl = _teacher(teacher_ids, teacher_logits, T, dev)
     _check("moe_lm_distill_bwd", load().moe_lm_distill_bwd(
-        _ptr(x), _ptr(w), _ptr(teacher_ids), _ptr(teacher_logits), float(temperature), _ptr(lse), _ptr(dloss), _ptr(dx),
-        _ptr(dw), T, D, V, K, _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+        px, pw, pi, pl, float(temperature), _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev),
+        _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V, K, _workspace(workspace, dev),
+        workspace.numel(), _current_stream(stream)))

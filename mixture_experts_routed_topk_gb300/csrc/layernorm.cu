@@ -6,15 +6,22 @@
 //   dgamma = sum_t dy xhat,  dbeta = sum_t dy
 //
 // Both directions are bound by memory: forward T D read and written once, backward 2 T D read and
-// T D written. A row is read once and stays in registers (rows up to 8192 elements; longer ones
-// are read again, mostly from L2). All arithmetic is fp32; the variance is taken from the centred
-// values, so a large mean does not cancel it away.
+// T D written. All arithmetic is fp32; the variance is taken from the centred values, so a large mean
+// does not cancel it away.
 //
-// The backward grid is persistent: a block walks rows b, b + grid, ... and keeps its column sums of
-// dy xhat and dy in registers, so dgamma and dbeta cost no extra pass over x and dy. Each block
-// writes one row of partial sums, and a second kernel adds the rows in block order: the result
-// does not depend on the order in which blocks finish.
+// Rows up to 8192 elements: persistent blocks of 512 threads, in groups of 32 to 512 threads that own
+// one row at a time (16 elements per thread). A group asynchronously copies the rows it will need
+// next into a ring in shared memory, so that loads are in flight while it waits in the two row sums.
+// Where rows start on 16-byte boundaries a thread copies and reads only its own elements; otherwise the
+// group copies the aligned 16-byte pieces that cover the row, and each thread picks out its elements.
+//
+// The backward blocks keep their column sums of dy xhat and dy in registers, so dgamma and dbeta cost
+// no extra pass over x and dy. Each block writes one row of partial sums, and a second kernel adds the
+// rows in block order: the result does not depend on the order in which blocks finish.
+//
+// Longer rows are read two or three times, mostly from L2.
 #include <algorithm>
+#include <atomic>
 
 #include "ptx_sm103.cuh"
 #include "train_internal.cuh"
@@ -22,9 +29,6 @@
 namespace moe {
 namespace {
 
-// One thread's piece of a row: kN / kVec vectors of kVec elements, vector i at element
-// (i * kGroup + lane) * kVec of the row. kVec elements fill 16 bytes, or kVec is 1 where the rows
-// do not all start on 16-byte boundaries.
 template <typename T, int kVec>
 struct alignas(sizeof(T) * kVec) Pack {
     T v[kVec];
@@ -74,106 +78,203 @@ __device__ __forceinline__ void store_param(void* p, int32_t dtype, int64_t j, f
     else static_cast<__half*>(p)[j] = __float2half_rn(v);
 }
 
-// Sum over the kGroup threads of a row; every thread of the group gets it. kGroup is 32 (one warp)
-// or the whole block. The two buffers alternate, so that one barrier per sum is enough: a warp
-// writes buffer b again only after the barrier of the sum in between, which every reader has passed.
+constexpr int kLnThreads = 512;
+constexpr int kLnN = 16;  // elements of a row per thread
+
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Sums of two values over the kGroup threads of a row; every thread of the group gets them. Each group
+// has a named barrier. The two buffers alternate, so that one barrier per sum is enough: a warp writes
+// buffer b again only after the barrier of the sum in between, which every reader has passed.
 template <int kGroup>
 struct GroupSum {
-    float (*buf)[32];
+    float2 (*buf)[kLnThreads / 32];
     int turn = 0;
-    __device__ float operator()(float v) {
-        v = warp_sum(v);
+    __device__ float2 operator()(float2 v) {
+        v.x = warp_sum(v.x);
+        v.y = warp_sum(v.y);
         if constexpr (kGroup > 32) {
-            float* b = buf[turn];
+            const int group = threadIdx.x / kGroup, first = group * (kGroup / 32);
+            float2* b = buf[turn];
             turn ^= 1;
             if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-            __syncthreads();
-            v = 0.0f;
+            group_barrier(1 + group, kGroup);
+            v = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kGroup / 32; ++w) v += b[w];
+            for (int w = 0; w < kGroup / 32; ++w) v.x += b[first + w].x, v.y += b[first + w].y;
         }
         return v;
     }
 };
 
-constexpr int kWarpBlock = 128;  // threads of a block whose warps own a row each
-template <int kGroup>
-constexpr int kBlockThreads = kGroup == 32 ? kWarpBlock : kGroup;
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 
-// x and y are not declared restrict: y may be x itself (a row is in registers before it is written).
-template <typename T, int kGroup, int kN, int kVec>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>)
-    k_ln_fwd(const T* x, const Param gamma, const Param beta, T* y, float* __restrict__ mean_out,
-             float* __restrict__ rstd_out, int64_t rows, int32_t D, float eps) {
-    constexpr int kRows = kBlockThreads<kGroup> / kGroup;
-    constexpr int kVecs = kN / kVec;
-    using P = Pack<T, kVec>;
-    __shared__ float buf[2][32];
-    GroupSum<kGroup> sum{buf};
-    const int lane = threadIdx.x % kGroup;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
-    griddep_wait();
-    griddep_launch_dependents();
-    if (row >= rows) return;  // whole warps; a block that is one group always has its row
-    const T* xr = x + row * D;
-    float v[kN];
-    float s = 0.0f;
+// One tensor's share of a ring stage: kLnThreads x kLnN elements, and 16 bytes more for each of up to 16
+// rows, whose covering pieces may begin before and end after them.
+template <typename T>
+constexpr int kTensorBytes = kLnThreads * kLnN * static_cast<int>(sizeof(T)) + 256;
+// Stages: enough bytes in flight (some 50 KB per SM hide the memory's latency at full rate) with two
+// blocks per SM; the backward pass in fp32 holds twice the bytes and runs one block per SM.
+template <typename T, bool kBackward>
+constexpr int kLnStages = kBackward ? 3 : (sizeof(T) == 4 ? 3 : 4);
+template <typename T, bool kBackward>
+constexpr int kLnBlocksPerSm = kBackward && sizeof(T) == 4 ? 1 : 2;
+template <typename T, bool kBackward>
+constexpr int kLnSmemBytes = kLnStages<T, kBackward> * (kBackward ? 2 : 1) * kTensorBytes<T>;
+
+// The covering pieces of one group's row.
+template <typename T, int kGroup>
+constexpr int kPiecesBytes = kGroup * kLnN * static_cast<int>(sizeof(T)) + 16;
+
+// A row as a group's threads see it in shared memory: element (i, e) of thread `lane` is element
+// index(i, e) of the row.
+template <typename T, int kGroup, bool kAligned>
+struct Row {
+    static constexpr int kVec = kAligned ? 16 / static_cast<int>(sizeof(T)) : 1;
+    static constexpr int kVecs = kLnN / kVec;
+
+    __device__ static int index(int i, int lane) { return (i * kGroup + lane) * kVec; }
+
+    // Starts the copies of row `row` of the tensor [rows, D] at base into this tensor's part of a stage.
+    __device__ static void fetch(uint8_t* part, const T* base, int64_t row, int64_t rows, int32_t D, int lane) {
+        if constexpr (kAligned) {
+            const T* src = base + row * D;
+            uint8_t* dst = part + 16 * static_cast<int>(threadIdx.x);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int j = (i * kGroup + lane) * kVec;
-        if (j < D) {
-            const P p = *reinterpret_cast<const P*>(xr + j);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[i * kVec + e] = to_float(p.v[e]);
+            for (int i = 0; i < kVecs; ++i)
+                if (index(i, lane) < D) copy_async16(dst + i * kLnThreads * 16, src + index(i, lane));
         } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[i * kVec + e] = 0.0f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kN; ++i) s += v[i];
-    const float inv_d = 1.0f / static_cast<float>(D);
-    const float mean = sum(s) * inv_d;
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        if ((i * kGroup + lane) * kVec < D) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const float c = v[i * kVec + e] - mean;
-                v[i * kVec + e] = c;
-                q += c * c;
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
+            const uintptr_t hi = lo + static_cast<uintptr_t>(rows) * D * sizeof(T);
+            const uintptr_t begin = lo + static_cast<uintptr_t>(row) * D * sizeof(T);
+            const uintptr_t first = begin & ~static_cast<uintptr_t>(15);
+            const int pieces = static_cast<int>((begin + D * sizeof(T) + 15 - first) / 16);
+            uint8_t* dst = part + (threadIdx.x / kGroup) * kPiecesBytes<T, kGroup>;
+            for (int c = lane; c < pieces; c += kGroup) {
+                const uintptr_t at = first + 16 * static_cast<uintptr_t>(c);
+                if (at >= lo && at + 16 <= hi) {
+                    copy_async16(dst + 16 * c, reinterpret_cast<const void*>(at));
+                } else {  // the tensor's own first and last piece: only the elements inside it
+                    for (uintptr_t a = at < lo ? lo : at; a < at + 16 && a < hi; a += sizeof(T))
+                        *reinterpret_cast<T*>(dst + 16 * c + (a - at)) = *reinterpret_cast<const T*>(a);
+                }
             }
         }
     }
-    const float rstd = 1.0f / sqrtf(sum(q) * inv_d + eps);
-    T* yr = y + row * D;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int j = (i * kGroup + lane) * kVec;
-        if (j < D) {
-            float g[kVec], b[kVec];
-            load_param<kVec>(gamma, j, 1.0f, g);
-            load_param<kVec>(beta, j, 0.0f, b);
-            P p;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) p.v[e] = from_float<T>(fmaf(v[i * kVec + e] * rstd, g[e], b[e]));
-            *reinterpret_cast<P*>(yr + j) = p;
+
+    // Vector i of this thread's part of the row (index(i, lane) < D).
+    __device__ static Pack<T, kVec> get(const uint8_t* part, const T* base, int64_t row, int32_t D, int i, int lane) {
+        if constexpr (kAligned) {
+            return *reinterpret_cast<const Pack<T, kVec>*>(part + 16 * (i * kLnThreads + static_cast<int>(threadIdx.x)));
+        } else {
+            const uintptr_t begin = reinterpret_cast<uintptr_t>(base) + static_cast<uintptr_t>(row) * D * sizeof(T);
+            const uint8_t* r = part + (threadIdx.x / kGroup) * kPiecesBytes<T, kGroup> + (begin & 15);
+            return *reinterpret_cast<const Pack<T, kVec>*>(r + index(i, lane) * sizeof(T));
         }
     }
-    if (lane == 0) {
-        mean_out[row] = mean;
-        rstd_out[row] = rstd;
+};
+
+// x and y are not declared restrict: y may be x itself. A group has its row in registers before it writes
+// it, and of the neighbouring rows that its pieces touch it uses nothing.
+template <typename T, int kGroup, bool kAligned>
+__global__ void __launch_bounds__(kLnThreads, (kLnBlocksPerSm<T, false>))
+    k_ln_fwd(const T* x, const Param gamma, const Param beta, T* y, float* __restrict__ mean_out,
+             float* __restrict__ rstd_out, int64_t rows, int32_t D, float eps) {
+    using R = Row<T, kGroup, kAligned>;
+    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, false>;
+    constexpr int kRows = kLnThreads / kGroup;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 buf[2][kLnThreads / 32];
+    GroupSum<kGroup> sum{buf};
+    const int lane = threadIdx.x % kGroup;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
+    griddep_wait();
+    griddep_launch_dependents();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (row + s * stride < rows) R::fetch(ring + s * kTensorBytes<T>, x, row + s * stride, rows, D, lane);
+        copy_commit();
+    }
+    const float inv_d = 1.0f / static_cast<float>(D);
+    int slot = 0;
+    for (; row < rows; row += stride, slot = slot + 1 == kStages ? 0 : slot + 1) {
+        copy_wait<kStages - 2>();
+        if constexpr (!kAligned) {  // the row was copied by the whole group
+            if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
+            else __syncwarp();
+        }
+        {   // the slot that was read in the previous round
+            const int next = slot == 0 ? kStages - 1 : slot - 1;
+            const int64_t r = row + (kStages - 1) * stride;
+            if (r < rows) R::fetch(ring + next * kTensorBytes<T>, x, r, rows, D, lane);
+            copy_commit();
+        }
+        float v[kLnN];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (R::index(i, lane) < D) {
+                const auto p = R::get(ring + slot * kTensorBytes<T>, x, row, D, i, lane);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[i * kVec + e] = to_float(p.v[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[i * kVec + e] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLnN; ++i) s += v[i];
+        const float mean = sum(make_float2(s, 0.0f)).x * inv_d;
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (R::index(i, lane) < D) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float c = v[i * kVec + e] - mean;
+                    v[i * kVec + e] = c;
+                    q += c * c;
+                }
+            }
+        }
+        const float rstd = 1.0f / sqrtf(sum(make_float2(q, 0.0f)).x * inv_d + eps);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int j = R::index(i, lane);
+            if (j < D) {
+                float g[kVec], b[kVec];
+                load_param<kVec>(gamma, j, 1.0f, g);
+                load_param<kVec>(beta, j, 0.0f, b);
+                Pack<T, kVec> p;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) p.v[e] = from_float<T>(fmaf(v[i * kVec + e] * rstd, g[e], b[e]));
+                *reinterpret_cast<Pack<T, kVec>*>(y + row * D + j) = p;
+            }
+        }
+        if (lane == 0) {
+            mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
     }
 }
 
 // Rows longer than the registers hold: three passes over the row, the second and third from L2.
-constexpr int kLongThreads = 512;
+constexpr int kLongThreads = kLnThreads;
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads)
     k_ln_fwd_long(const T* x, const Param gamma, const Param beta, T* y, float* __restrict__ mean_out,
                   float* __restrict__ rstd_out, int32_t D, float eps) {
-    __shared__ float buf[2][32];
+    __shared__ float2 buf[2][kLnThreads / 32];
     GroupSum<kLongThreads> sum{buf};
     griddep_wait();
     griddep_launch_dependents();
@@ -182,13 +283,13 @@ __global__ void __launch_bounds__(kLongThreads)
     const float inv_d = 1.0f / static_cast<float>(D);
     float s = 0.0f;
     for (int j = threadIdx.x; j < D; j += kLongThreads) s += to_float(xr[j]);
-    const float mean = sum(s) * inv_d;
+    const float mean = sum(make_float2(s, 0.0f)).x * inv_d;
     float q = 0.0f;
     for (int j = threadIdx.x; j < D; j += kLongThreads) {
         const float c = to_float(xr[j]) - mean;
         q += c * c;
     }
-    const float rstd = 1.0f / sqrtf(sum(q) * inv_d + eps);
+    const float rstd = 1.0f / sqrtf(sum(make_float2(q, 0.0f)).x * inv_d + eps);
     for (int j = threadIdx.x; j < D; j += kLongThreads) {
         float g[1], b[1];
         load_param<1>(gamma, j, 1.0f, g);
@@ -202,109 +303,111 @@ __global__ void __launch_bounds__(kLongThreads)
 }
 
 // partial: [grid][2][D], or null where neither parameter gradient is wanted. dx may be dy or x.
-template <typename T, int kGroup, int kN, int kVec>
-__global__ void __launch_bounds__(kBlockThreads<kGroup>)
+template <typename T, int kGroup, bool kAligned>
+__global__ void __launch_bounds__(kLnThreads, (kLnBlocksPerSm<T, true>))
     k_ln_bwd(const T* dy, const T* x, const Param gamma, const float* __restrict__ mean_in,
              const float* __restrict__ rstd_in, T* dx, int64_t rows, int32_t D, float* __restrict__ partial) {
-    constexpr int kRows = kBlockThreads<kGroup> / kGroup;
-    constexpr int kVecs = kN / kVec;
-    using P = Pack<T, kVec>;
-    __shared__ float buf[2][32];
+    using R = Row<T, kGroup, kAligned>;
+    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, true>;
+    constexpr int kRows = kLnThreads / kGroup;
+    constexpr int kStage = 2 * kTensorBytes<T>;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 buf[2][kLnThreads / 32];
     GroupSum<kGroup> sum{buf};
     const int lane = threadIdx.x % kGroup;
-    float dg[kN], db[kN];
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
+    float dg[kLnN], db[kLnN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) dg[i] = 0.0f, db[i] = 0.0f;
+    for (int i = 0; i < kLnN; ++i) dg[i] = 0.0f, db[i] = 0.0f;
+    auto fetch = [&](int slot, int64_t r) {
+        if (r < rows) {
+            R::fetch(ring + slot * kStage, x, r, rows, D, lane);
+            R::fetch(ring + slot * kStage + kTensorBytes<T>, dy, r, rows, D, lane);
+        }
+        copy_commit();
+    };
     griddep_wait();
     griddep_launch_dependents();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(s, row + s * stride);
     const float inv_d = 1.0f / static_cast<float>(D);
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup; row < rows;
-         row += static_cast<int64_t>(gridDim.x) * kRows) {
-        P px[kVecs], pd[kVecs];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = (i * kGroup + lane) * kVec;
-            if (j < D) {
-                px[i] = *reinterpret_cast<const P*>(x + row * D + j);
-                pd[i] = *reinterpret_cast<const P*>(dy + row * D + j);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) px[i].v[e] = from_float<T>(0.0f), pd[i].v[e] = from_float<T>(0.0f);
-            }
+    int slot = 0;
+    for (; row < rows; row += stride, slot = slot + 1 == kStages ? 0 : slot + 1) {
+        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
+        copy_wait<kStages - 2>();
+        if constexpr (!kAligned) {  // the row was copied by the whole group
+            if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
+            else __syncwarp();
         }
-        const float mean = mean_in[row], rstd = rstd_in[row];
-        float sg = 0.0f, sgx = 0.0f;
+        fetch(slot == 0 ? kStages - 1 : slot - 1, row + (kStages - 1) * stride);  // read in the previous round
+        const uint8_t* xs = ring + slot * kStage;
+        const uint8_t* ds = xs + kTensorBytes<T>;
+        float2 s = make_float2(0.0f, 0.0f);  // sums of g and of g xhat
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int j = (i * kGroup + lane) * kVec;
+            const int j = R::index(i, lane);
             if (j < D) {
                 float g[kVec];
                 load_param<kVec>(gamma, j, 1.0f, g);
+                const auto px = R::get(xs, x, row, D, i, lane);
+                const auto pd = R::get(ds, dy, row, D, i, lane);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float d = to_float(pd[i].v[e]);
-                    const float xhat = (to_float(px[i].v[e]) - mean) * rstd;
+                    const float d = to_float(pd.v[e]);
+                    const float xhat = (to_float(px.v[e]) - mean) * rstd;
                     dg[i * kVec + e] += d * xhat;
                     db[i * kVec + e] += d;
-                    sg += d * g[e];
-                    sgx += d * g[e] * xhat;
+                    s.x += d * g[e];
+                    s.y += d * g[e] * xhat;
                 }
             }
         }
-        sg = sum(sg) * inv_d;
-        sgx = sum(sgx) * inv_d;
+        s = sum(s);
+        s.x *= inv_d;
+        s.y *= inv_d;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            const int j = (i * kGroup + lane) * kVec;
+            const int j = R::index(i, lane);
             if (j < D) {
                 float g[kVec];
                 load_param<kVec>(gamma, j, 1.0f, g);
-                P p;
+                const auto px = R::get(xs, x, row, D, i, lane);
+                const auto pd = R::get(ds, dy, row, D, i, lane);
+                Pack<T, kVec> p;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float xhat = (to_float(px[i].v[e]) - mean) * rstd;
-                    p.v[e] = from_float<T>(rstd * (to_float(pd[i].v[e]) * g[e] - sg - xhat * sgx));
+                    const float xhat = (to_float(px.v[e]) - mean) * rstd;
+                    p.v[e] = from_float<T>(rstd * (to_float(pd.v[e]) * g[e] - s.x - xhat * s.y));
                 }
-                *reinterpret_cast<P*>(dx + row * D + j) = p;
+                *reinterpret_cast<Pack<T, kVec>*>(dx + row * D + j) = p;
             }
         }
     }
     if (partial == nullptr) return;
+    // the block's row of partial sums: its groups own the same columns, and meet in the ring in group order
     float* mine = partial + static_cast<int64_t>(blockIdx.x) * 2 * D;
-    if constexpr (kRows > 1) {
-        // the block's warps own the same columns: add them in warp order
-        __shared__ float acc[2][kGroup * kN];
-        for (int w = 0; w < kRows; ++w) {
-            __syncthreads();
-            if (static_cast<int>(threadIdx.x) / kGroup == w) {
+    copy_wait<0>();
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(ring);  // [kRows][2][kGroup * kLnN]
+    static_assert(kLnSmemBytes<T, true> >= 2 * kLnThreads * kLnN * 4, "the sums fit the ring");
+    constexpr int kCols = kGroup * kLnN;
+    float* own = acc + (threadIdx.x / kGroup) * 2 * kCols;
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        const int j = (i * kGroup + lane) * kVec + e;
-                        acc[0][j] = (w ? acc[0][j] : 0.0f) + dg[i * kVec + e];
-                        acc[1][j] = (w ? acc[1][j] : 0.0f) + db[i * kVec + e];
-                    }
-                }
-            }
+        for (int e = 0; e < kVec; ++e) {
+            own[R::index(i, lane) + e] = dg[i * kVec + e];
+            own[kCols + R::index(i, lane) + e] = db[i * kVec + e];
         }
-        __syncthreads();
-        for (int j = threadIdx.x; j < D; j += blockDim.x) {
-            mine[j] = acc[0][j];
-            mine[D + j] = acc[1][j];
-        }
-    } else {
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < D; j += kLnThreads) {
+        float a = 0.0f, b = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const int j = (i * kGroup + lane) * kVec + e;
-                if (j < D) {
-                    mine[j] = dg[i * kVec + e];
-                    mine[D + j] = db[i * kVec + e];
-                }
-            }
-        }
+        for (int r = 0; r < kRows; ++r) a += acc[2 * r * kCols + j], b += acc[(2 * r + 1) * kCols + j];
+        mine[j] = a;
+        mine[D + j] = b;
     }
 }
 
@@ -315,7 +418,7 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads)
     k_ln_bwd_long(const T* dy, const T* x, const Param gamma, const float* __restrict__ mean_in,
                   const float* __restrict__ rstd_in, T* dx, int64_t rows, int32_t D, float* __restrict__ partial) {
-    __shared__ float buf[2][32];
+    __shared__ float2 buf[2][kLnThreads / 32];
     GroupSum<kLongThreads> sum{buf};
     griddep_wait();
     griddep_launch_dependents();
@@ -325,21 +428,22 @@ __global__ void __launch_bounds__(kLongThreads)
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, first = false) {
         const float mean = mean_in[row], rstd = rstd_in[row];
         const T *xr = x + row * D, *dr = dy + row * D;
-        float sg = 0.0f, sgx = 0.0f;
+        float2 s = make_float2(0.0f, 0.0f);
         for (int j = threadIdx.x; j < D; j += kLongThreads) {
             float g[1];
             load_param<1>(gamma, j, 1.0f, g);
             const float d = to_float(dr[j]), xhat = (to_float(xr[j]) - mean) * rstd;
-            sg += d * g[0];
-            sgx += d * g[0] * xhat;
+            s.x += d * g[0];
+            s.y += d * g[0] * xhat;
         }
-        sg = sum(sg) * inv_d;
-        sgx = sum(sgx) * inv_d;
+        s = sum(s);
+        s.x *= inv_d;
+        s.y *= inv_d;
         for (int j = threadIdx.x; j < D; j += kLongThreads) {
             float g[1];
             load_param<1>(gamma, j, 1.0f, g);
             const float d = to_float(dr[j]), xhat = (to_float(xr[j]) - mean) * rstd;
-            dx[row * D + j] = from_float<T>(rstd * (d * g[0] - sg - xhat * sgx));
+            dx[row * D + j] = from_float<T>(rstd * (d * g[0] - s.x - xhat * s.y));
             if (mine) {
                 mine[j] = (first ? 0.0f : mine[j]) + d * xhat;
                 mine[D + j] = (first ? 0.0f : mine[D + j]) + d;
@@ -350,7 +454,7 @@ __global__ void __launch_bounds__(kLongThreads)
 
 // dgamma[j] = sum over the blocks' partial rows in block order; dbeta likewise. A block owns 32
 // columns of one of the two sums; its warps take the rows in turn and meet in shared memory.
-constexpr int kGradWarps = 8;
+constexpr int kGradWarps = 16;
 __global__ void __launch_bounds__(32 * kGradWarps)
     k_ln_param_grads(const float* __restrict__ partial, int32_t blocks, int32_t D, int32_t param_dtype,
                      void* __restrict__ dgamma, void* __restrict__ dbeta) {
@@ -381,70 +485,88 @@ bool rows_aligned16(const void* p, int64_t row_bytes) {
 
 Param param(const void* p, int32_t dtype) { return Param{p, dtype, reinterpret_cast<uintptr_t>(p) % 16 == 0}; }
 
-template <typename T, int kGroup, int kN, int kVec>
-cudaError_t run_fwd(const LayerNormProblem& p, cudaStream_t stream) {
-    constexpr int kRows = kBlockThreads<kGroup> / kGroup;
-    return launch_pdl(k_ln_fwd<T, kGroup, kN, kVec>, dim3(static_cast<unsigned>(ceil_div(p.T, kRows))),
-                      dim3(kBlockThreads<kGroup>), 0, stream, static_cast<const T*>(p.x),
-                      param(p.gamma, p.param_dtype), param(p.beta, p.param_dtype), static_cast<T*>(p.y), p.mean, p.rstd,
-                      p.T, p.D, p.eps);
+// Allows the kernel its dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
-template <typename T, int kVec>
+int ln_grid(const LayerNormProblem& p, int rows_per_block, int blocks_per_sm) {
+    const int64_t want = ceil_div(p.T, rows_per_block);
+    return static_cast<int>(std::min<int64_t>({want, static_cast<int64_t>(blocks_per_sm) * p.sm_count,
+                                               static_cast<int64_t>(kLnMaxBlocks)}));
+}
+
+template <typename T, int kGroup, bool kAligned>
+cudaError_t run_fwd(const LayerNormProblem& p, cudaStream_t stream) {
+    constexpr int kBytes = kLnSmemBytes<T, false>;
+    const cudaError_t e = allow_smem<&k_ln_fwd<T, kGroup, kAligned>>(kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_ln_fwd<T, kGroup, kAligned>, dim3(ln_grid(p, kLnThreads / kGroup, kLnBlocksPerSm<T, false>)),
+                      dim3(kLnThreads), kBytes, stream, static_cast<const T*>(p.x), param(p.gamma, p.param_dtype),
+                      param(p.beta, p.param_dtype), static_cast<T*>(p.y), p.mean, p.rstd, p.T, p.D, p.eps);
+}
+
+template <typename T, bool kAligned>
 cudaError_t dispatch_fwd(const LayerNormProblem& p, cudaStream_t stream) {
-    if (p.D <= 256) return run_fwd<T, 32, 8, kVec>(p, stream);
-    if (p.D <= 512) return run_fwd<T, 32, 16, kVec>(p, stream);
-    if (p.D <= 1024) return run_fwd<T, 32, 32, kVec>(p, stream);
-    if (p.D <= 2048) return run_fwd<T, 128, 16, kVec>(p, stream);
-    if (p.D <= 4096) return run_fwd<T, 256, 16, kVec>(p, stream);
-    if (p.D <= 8192) return run_fwd<T, 512, 16, kVec>(p, stream);
-    return launch_pdl(k_ln_fwd_long<T>, dim3(static_cast<unsigned>(p.T)), dim3(kLongThreads), 0, stream,
-                      static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), param(p.beta, p.param_dtype),
-                      static_cast<T*>(p.y), p.mean, p.rstd, p.D, p.eps);
+    if (p.D <= 512) return run_fwd<T, 32, kAligned>(p, stream);
+    if (p.D <= 1024) return run_fwd<T, 64, kAligned>(p, stream);
+    if (p.D <= 2048) return run_fwd<T, 128, kAligned>(p, stream);
+    if (p.D <= 4096) return run_fwd<T, 256, kAligned>(p, stream);
+    return run_fwd<T, 512, kAligned>(p, stream);
 }
 
 template <typename T>
 cudaError_t fwd_of(const LayerNormProblem& p, cudaStream_t stream) {
-    constexpr int kVec = 16 / sizeof(T);
+    if (p.D > kLnThreads * kLnN)
+        return launch_pdl(k_ln_fwd_long<T>, dim3(static_cast<unsigned>(p.T)), dim3(kLongThreads), 0, stream,
+                          static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), param(p.beta, p.param_dtype),
+                          static_cast<T*>(p.y), p.mean, p.rstd, p.D, p.eps);
     const int64_t bytes = static_cast<int64_t>(p.D) * sizeof(T);
-    return rows_aligned16(p.x, bytes) && rows_aligned16(p.y, bytes) ? dispatch_fwd<T, kVec>(p, stream)
-                                                                   : dispatch_fwd<T, 1>(p, stream);
+    return rows_aligned16(p.x, bytes) && rows_aligned16(p.y, bytes) ? dispatch_fwd<T, true>(p, stream)
+                                                                   : dispatch_fwd<T, false>(p, stream);
 }
 
-int bwd_grid(const LayerNormProblem& p, int rows_per_block, int threads) {
-    const int64_t want = ceil_div(p.T, rows_per_block);
-    const int64_t per_sm = threads <= 256 ? 2 : 1;
-    return static_cast<int>(std::min<int64_t>({want, per_sm * p.sm_count, static_cast<int64_t>(kLnMaxBlocks)}));
-}
-
-template <typename T, int kGroup, int kN, int kVec>
+template <typename T, int kGroup, bool kAligned>
 cudaError_t run_bwd(const LayerNormProblem& p, int* blocks, cudaStream_t stream) {
-    *blocks = bwd_grid(p, kBlockThreads<kGroup> / kGroup, kBlockThreads<kGroup>);
-    return launch_pdl(k_ln_bwd<T, kGroup, kN, kVec>, dim3(*blocks), dim3(kBlockThreads<kGroup>), 0, stream,
+    constexpr int kBytes = kLnSmemBytes<T, true>;
+    const cudaError_t e = allow_smem<&k_ln_bwd<T, kGroup, kAligned>>(kBytes);
+    if (e != cudaSuccess) return e;
+    *blocks = ln_grid(p, kLnThreads / kGroup, kLnBlocksPerSm<T, true>);
+    return launch_pdl(k_ln_bwd<T, kGroup, kAligned>, dim3(*blocks), dim3(kLnThreads), kBytes, stream,
                       static_cast<const T*>(p.dy), static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), p.mean_in,
                       p.rstd_in, static_cast<T*>(p.dx), p.T, p.D, p.partial);
 }
 
-template <typename T, int kVec>
+template <typename T, bool kAligned>
 cudaError_t dispatch_bwd(const LayerNormProblem& p, int* blocks, cudaStream_t stream) {
-    if (p.D <= 256) return run_bwd<T, 32, 8, kVec>(p, blocks, stream);
-    if (p.D <= 512) return run_bwd<T, 32, 16, kVec>(p, blocks, stream);
-    if (p.D <= 2048) return run_bwd<T, 128, 16, kVec>(p, blocks, stream);
-    if (p.D <= 4096) return run_bwd<T, 256, 16, kVec>(p, blocks, stream);
-    if (p.D <= 8192) return run_bwd<T, 512, 16, kVec>(p, blocks, stream);
-    *blocks = bwd_grid(p, 1, kLongThreads);
-    return launch_pdl(k_ln_bwd_long<T>, dim3(*blocks), dim3(kLongThreads), 0, stream, static_cast<const T*>(p.dy),
-                      static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), p.mean_in, p.rstd_in,
-                      static_cast<T*>(p.dx), p.T, p.D, p.partial);
+    if (p.D <= 512) return run_bwd<T, 32, kAligned>(p, blocks, stream);
+    if (p.D <= 1024) return run_bwd<T, 64, kAligned>(p, blocks, stream);
+    if (p.D <= 2048) return run_bwd<T, 128, kAligned>(p, blocks, stream);
+    if (p.D <= 4096) return run_bwd<T, 256, kAligned>(p, blocks, stream);
+    return run_bwd<T, 512, kAligned>(p, blocks, stream);
 }
 
 template <typename T>
 cudaError_t bwd_of(const LayerNormProblem& p, int* blocks, cudaStream_t stream) {
-    constexpr int kVec = 16 / sizeof(T);
+    if (p.D > kLnThreads * kLnN) {
+        *blocks = ln_grid(p, 1, 2);
+        return launch_pdl(k_ln_bwd_long<T>, dim3(*blocks), dim3(kLongThreads), 0, stream, static_cast<const T*>(p.dy),
+                          static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), p.mean_in, p.rstd_in,
+                          static_cast<T*>(p.dx), p.T, p.D, p.partial);
+    }
     const int64_t bytes = static_cast<int64_t>(p.D) * sizeof(T);
     return rows_aligned16(p.x, bytes) && rows_aligned16(p.dy, bytes) && rows_aligned16(p.dx, bytes)
-               ? dispatch_bwd<T, kVec>(p, blocks, stream)
-               : dispatch_bwd<T, 1>(p, blocks, stream);
+               ? dispatch_bwd<T, true>(p, blocks, stream)
+               : dispatch_bwd<T, false>(p, blocks, stream);
 }
 
 }  // namespace

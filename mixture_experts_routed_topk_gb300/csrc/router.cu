@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kRouterThreads)
     float m = 0.0f, total = 0.0f;
     int32_t* my_ids = ids + row * K;
     float* my_scores = scores + row * K;
+    int32_t id_k = 0;  // lane k % 32 keeps choice k until 32 of them are stored at once
+    float e_k = 0.0f;
     for (int k = 0; k < K; ++k) {
         uint32_t best = 0u;
         int at = 0;
@@ -130,17 +132,27 @@ __global__ void __launch_bounds__(kRouterThreads)
         const float e = expf(v - m);
         if (normalize) total += e;
         if (t == (k & 31)) {
-            my_ids[k] = static_cast<int32_t>(top.y);
-            my_scores[k] = e;
+            id_k = static_cast<int32_t>(top.y);
+            e_k = e;
+        }
+        if ((k & 31) == 31 && K > 32 && t < 32) {  // more than a warp's worth: scaled below
+            my_ids[k - 31 + t] = id_k;
+            my_scores[k - 31 + t] = e_k;
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i)
             if (expert_of<kThreads, kVec>(i, t) == static_cast<int>(top.y)) key[i] = 0u;
     }
-    // the thread that wrote a score scales it; a row with nothing but -inf has scores of 0
+    // a row with nothing but -inf has scores of 0
     const bool none = m == -INFINITY;
-    if (t < 32)
-        for (int k = t; k < K; k += 32) my_scores[k] = none ? 0.0f : my_scores[k] / total;
+    const float inv = 1.0f / total;
+    if (t >= 32) return;
+    const int rest = K > 32 ? K & ~31 : 0;  // choices [rest, K) are still in registers
+    if (rest + t < K) {
+        my_ids[rest + t] = id_k;
+        my_scores[rest + t] = none ? 0.0f : e_k * inv;
+    }
+    for (int k = t; k < rest; k += 32) my_scores[k] = none ? 0.0f : my_scores[k] * inv;  // as this thread wrote it
 }
 
 template <typename T, int kThreads, int kN, int kVec>
