@@ -11,8 +11,8 @@
 //
 // Rows up to 8192 elements: persistent blocks of 512 threads, in groups of 32 to 512 threads that own
 // one row at a time (16 elements per thread). A group asynchronously copies the rows it will need
-// next into a ring in shared memory, so that loads are in flight while it waits in the two row sums.
-// Where rows start on 16-byte boundaries a thread copies and reads only its own elements; otherwise the
+// next into a ring in shared memory, so that loads are in flight while it waits in the two row sums; it
+// takes two rows through those sums at a time, and keeps the parameters in registers. Where rows start on 16-byte boundaries a thread copies and reads only its own elements; otherwise the
 // group copies the aligned 16-byte pieces that cover the row, and each thread picks out its elements.
 //
 // The backward blocks keep their column sums of dy xhat and dy in registers, so dgamma and dbeta cost
@@ -85,27 +85,53 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sums of two values over the kGroup threads of a row; every thread of the group gets them. Each group
-// has a named barrier. The two buffers alternate, so that one barrier per sum is enough: a warp writes
-// buffer b again only after the barrier of the sum in between, which every reader has passed.
-template <int kGroup>
+// Sums of kN (2 or 4) values over the kGroup threads of a row; every thread of the group gets them.
+// Lanes trade halves of the values as they add, so that after log2(kN) steps a lane carries one value:
+// 5 or 6 shuffles for what would take 10 or 20. Each group has a named barrier; the two buffers
+// alternate, so that one barrier per sum is enough: a warp writes buffer b again only after the barrier
+// of the sum in between, which every reader has passed.
+template <int kGroup, int kN>
 struct GroupSum {
-    float2 (*buf)[kLnThreads / 32];
+    static_assert(kN == 2 || kN == 4, "values");
+    static constexpr int kSpan = 32 / kN;  // lanes that end up with the same value
+    float (*buf)[kN][kLnThreads / 32];
     int turn = 0;
-    __device__ float2 operator()(float2 v) {
-        v.x = warp_sum(v.x);
-        v.y = warp_sum(v.y);
-        if constexpr (kGroup > 32) {
-            const int group = threadIdx.x / kGroup, first = group * (kGroup / 32);
-            float2* b = buf[turn];
-            turn ^= 1;
-            if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-            group_barrier(1 + group, kGroup);
-            v = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kGroup / 32; ++w) v.x += b[first + w].x, v.y += b[first + w].y;
+
+    __device__ void operator()(float (&v)[kN]) {
+        const int lane = threadIdx.x & 31;
+        float t;
+        {
+            const bool up = lane & 16;
+            if constexpr (kN == 4) {
+                float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+                a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+                b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+                const bool second = lane & 8;
+                t = (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, 8);
+            } else {
+                t = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+            }
         }
-        return v;
+#pragma unroll
+        for (int o = kSpan / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if constexpr (kGroup > 32) {
+            constexpr int kWarps = kGroup / 32;
+            const int group = threadIdx.x / kGroup, first = group * kWarps;
+            float(&b)[kN][kLnThreads / 32] = buf[turn];
+            turn ^= 1;
+            if (lane % kSpan == 0) b[lane / kSpan][threadIdx.x >> 5] = t;
+            group_barrier(1 + group, kGroup);
+            // lane l adds value l / kSpan over the warps l % kSpan, l % kSpan + kSpan, ...
+            t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w += kSpan)
+                if (w + lane % kSpan < kWarps) t += b[lane / kSpan][first + w + lane % kSpan];
+#pragma unroll
+            for (int o = kSpan / 2; o > 0; o >>= 1)
+                if (o < kWarps) t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * kSpan);
     }
 };
 
@@ -122,12 +148,14 @@ __device__ __forceinline__ void copy_wait() {
 // rows, whose covering pieces may begin before and end after them.
 template <typename T>
 constexpr int kTensorBytes = kLnThreads * kLnN * static_cast<int>(sizeof(T)) + 256;
-// Stages: enough bytes in flight (some 50 KB per SM hide the memory's latency at full rate) with two
-// blocks per SM; the backward pass in fp32 holds twice the bytes and runs one block per SM.
+// Rows a group takes through its sums together, and rows in the ring: with two at a time, those two, the
+// two being fetched into the places of the last two, and the ones in between. Some 50 KB in flight hide
+// the memory's latency at full rate; the ring takes up to 200 KB of an SM's shared memory. fp32 rows of
+// the backward pass are so long that three single ones fill it.
 template <typename T, bool kBackward>
-constexpr int kLnStages = kBackward ? 3 : (sizeof(T) == 4 ? 3 : 4);
+constexpr int kLnBatch = kBackward && sizeof(T) == 4 ? 1 : 2;
 template <typename T, bool kBackward>
-constexpr int kLnBlocksPerSm = kBackward && sizeof(T) == 4 ? 1 : 2;
+constexpr int kLnStages = kBackward ? (sizeof(T) == 4 ? 3 : 6) : (sizeof(T) == 4 ? 6 : 10);
 template <typename T, bool kBackward>
 constexpr int kLnSmemBytes = kLnStages<T, kBackward> * (kBackward ? 2 : 1) * kTensorBytes<T>;
 
@@ -183,88 +211,121 @@ struct Row {
     }
 };
 
+// This thread's parameters, in the order of its elements.
+template <class R, typename P = Param>
+__device__ __forceinline__ void load_params(const P& a, int32_t D, int lane, float none, float (&out)[kLnN]) {
+#pragma unroll
+    for (int i = 0; i < R::kVecs; ++i) {
+        float t[R::kVec];
+#pragma unroll
+        for (int e = 0; e < R::kVec; ++e) t[e] = none;
+        if (R::index(i, lane) < D) load_param<R::kVec>(a, R::index(i, lane), none, t);
+#pragma unroll
+        for (int e = 0; e < R::kVec; ++e) out[i * R::kVec + e] = t[e];
+    }
+}
+
 // x and y are not declared restrict: y may be x itself. A group has its row in registers before it writes
 // it, and of the neighbouring rows that its pieces touch it uses nothing.
 template <typename T, int kGroup, bool kAligned>
-__global__ void __launch_bounds__(kLnThreads, (kLnBlocksPerSm<T, false>))
+__global__ void __launch_bounds__(kLnThreads, 1)
     k_ln_fwd(const T* x, const Param gamma, const Param beta, T* y, float* __restrict__ mean_out,
              float* __restrict__ rstd_out, int64_t rows, int32_t D, float eps) {
     using R = Row<T, kGroup, kAligned>;
-    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, false>;
+    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, false>, kBatch = kLnBatch<T, false>;
+    static_assert(kBatch == 2, "two rows share a sum");
     constexpr int kRows = kLnThreads / kGroup;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 buf[2][kLnThreads / 32];
-    GroupSum<kGroup> sum{buf};
+    __shared__ float buf[2][2][kLnThreads / 32];
+    GroupSum<kGroup, 2> sum{buf};
     const int lane = threadIdx.x % kGroup;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
     griddep_wait();
     griddep_launch_dependents();
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (row + s * stride < rows) R::fetch(ring + s * kTensorBytes<T>, x, row + s * stride, rows, D, lane);
+    auto fetch = [&](int slot, int64_t r) {
+        if (r < rows) R::fetch(ring + slot * kTensorBytes<T>, x, r, rows, D, lane);
         copy_commit();
-    }
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - kBatch; ++s) fetch(s, row + s * stride);
+    float g[kLnN], b[kLnN];
+    load_params<R>(gamma, D, lane, 1.0f, g);
+    load_params<R>(beta, D, lane, 0.0f, b);
     const float inv_d = 1.0f / static_cast<float>(D);
+    // slots go round in pairs: this round's pair, and the last round's, which is filled again
     int slot = 0;
-    for (; row < rows; row += stride, slot = slot + 1 == kStages ? 0 : slot + 1) {
-        copy_wait<kStages - 2>();
-        if constexpr (!kAligned) {  // the row was copied by the whole group
+    for (; row < rows; row += kBatch * stride) {
+        copy_wait<kStages - 2 * kBatch>();
+        if constexpr (!kAligned) {  // the rows were copied by the whole group
             if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
             else __syncwarp();
         }
-        {   // the slot that was read in the previous round
-            const int next = slot == 0 ? kStages - 1 : slot - 1;
-            const int64_t r = row + (kStages - 1) * stride;
-            if (r < rows) R::fetch(ring + next * kTensorBytes<T>, x, r, rows, D, lane);
-            copy_commit();
-        }
-        float v[kLnN];
-        float s = 0.0f;
+        const int last = slot == 0 ? kStages - kBatch : slot - kBatch;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (R::index(i, lane) < D) {
-                const auto p = R::get(ring + slot * kTensorBytes<T>, x, row, D, i, lane);
+        for (int k = 0; k < kBatch; ++k) fetch(last + k, row + (kStages - kBatch + k) * stride);
+        float v[kBatch][kLnN], s[kBatch];
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) v[i * kVec + e] = to_float(p.v[e]);
-            } else {
+        for (int k = 0; k < kBatch; ++k) {
+            const bool live = row + k * stride < rows;
+            s[k] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) v[i * kVec + e] = 0.0f;
+            for (int i = 0; i < kVecs; ++i) {
+                if (live && R::index(i, lane) < D) {
+                    const auto p = R::get(ring + (slot + k) * kTensorBytes<T>, x, row + k * stride, D, i, lane);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) v[k][i * kVec + e] = to_float(p.v[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) v[k][i * kVec + e] = 0.0f;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kLnN; ++i) s[k] += v[k][i];
         }
+        sum(s);
+        float mean[kBatch];
 #pragma unroll
-        for (int i = 0; i < kLnN; ++i) s += v[i];
-        const float mean = sum(make_float2(s, 0.0f)).x * inv_d;
-        float q = 0.0f;
+        for (int k = 0; k < kBatch; ++k) {
+            mean[k] = s[k] * inv_d;
+            s[k] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (R::index(i, lane) < D) {
+            for (int i = 0; i < kVecs; ++i) {
+                if (R::index(i, lane) < D) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float c = v[i * kVec + e] - mean;
-                    v[i * kVec + e] = c;
-                    q += c * c;
+                    for (int e = 0; e < kVec; ++e) {
+                        const float c = v[k][i * kVec + e] - mean[k];
+                        v[k][i * kVec + e] = c;
+                        s[k] += c * c;
+                    }
                 }
             }
         }
-        const float rstd = 1.0f / sqrtf(sum(make_float2(q, 0.0f)).x * inv_d + eps);
+        sum(s);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = R::index(i, lane);
-            if (j < D) {
-                float g[kVec], b[kVec];
-                load_param<kVec>(gamma, j, 1.0f, g);
-                load_param<kVec>(beta, j, 0.0f, b);
-                Pack<T, kVec> p;
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t r = row + k * stride;
+            if (r >= rows) break;
+            const float rstd = 1.0f / sqrtf(s[k] * inv_d + eps);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) p.v[e] = from_float<T>(fmaf(v[i * kVec + e] * rstd, g[e], b[e]));
-                *reinterpret_cast<Pack<T, kVec>*>(y + row * D + j) = p;
+            for (int i = 0; i < kVecs; ++i) {
+                const int j = R::index(i, lane);
+                if (j < D) {
+                    Pack<T, kVec> p;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const int n = i * kVec + e;
+                        p.v[e] = from_float<T>(fmaf(v[k][n] * rstd, g[n], b[n]));
+                    }
+                    *reinterpret_cast<Pack<T, kVec>*>(y + r * D + j) = p;
+                }
+            }
+            if (lane == 0) {
+                mean_out[r] = mean[k];
+                rstd_out[r] = rstd;
             }
         }
-        if (lane == 0) {
-            mean_out[row] = mean;
-            rstd_out[row] = rstd;
-        }
+        slot = slot + kBatch == kStages ? 0 : slot + kBatch;
     }
 }
 
@@ -274,22 +335,24 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads)
     k_ln_fwd_long(const T* x, const Param gamma, const Param beta, T* y, float* __restrict__ mean_out,
                   float* __restrict__ rstd_out, int32_t D, float eps) {
-    __shared__ float2 buf[2][kLnThreads / 32];
-    GroupSum<kLongThreads> sum{buf};
+    __shared__ float buf[2][2][kLnThreads / 32];
+    GroupSum<kLongThreads, 2> sum{buf};
     griddep_wait();
     griddep_launch_dependents();
     const int64_t row = blockIdx.x;
     const T* xr = x + row * D;
     const float inv_d = 1.0f / static_cast<float>(D);
-    float s = 0.0f;
-    for (int j = threadIdx.x; j < D; j += kLongThreads) s += to_float(xr[j]);
-    const float mean = sum(make_float2(s, 0.0f)).x * inv_d;
-    float q = 0.0f;
+    float s[2] = {0.0f, 0.0f};
+    for (int j = threadIdx.x; j < D; j += kLongThreads) s[0] += to_float(xr[j]);
+    sum(s);
+    const float mean = s[0] * inv_d;
+    s[0] = 0.0f;
     for (int j = threadIdx.x; j < D; j += kLongThreads) {
         const float c = to_float(xr[j]) - mean;
-        q += c * c;
+        s[0] += c * c;
     }
-    const float rstd = 1.0f / sqrtf(sum(make_float2(q, 0.0f)).x * inv_d + eps);
+    sum(s);
+    const float rstd = 1.0f / sqrtf(s[0] * inv_d + eps);
     for (int j = threadIdx.x; j < D; j += kLongThreads) {
         float g[1], b[1];
         load_param<1>(gamma, j, 1.0f, g);
@@ -304,22 +367,19 @@ __global__ void __launch_bounds__(kLongThreads)
 
 // partial: [grid][2][D], or null where neither parameter gradient is wanted. dx may be dy or x.
 template <typename T, int kGroup, bool kAligned>
-__global__ void __launch_bounds__(kLnThreads, (kLnBlocksPerSm<T, true>))
+__global__ void __launch_bounds__(kLnThreads, 1)
     k_ln_bwd(const T* dy, const T* x, const Param gamma, const float* __restrict__ mean_in,
              const float* __restrict__ rstd_in, T* dx, int64_t rows, int32_t D, float* __restrict__ partial) {
     using R = Row<T, kGroup, kAligned>;
-    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, true>;
+    constexpr int kVec = R::kVec, kVecs = R::kVecs, kStages = kLnStages<T, true>, kBatch = kLnBatch<T, true>;
     constexpr int kRows = kLnThreads / kGroup;
     constexpr int kStage = 2 * kTensorBytes<T>;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float2 buf[2][kLnThreads / 32];
-    GroupSum<kGroup> sum{buf};
+    __shared__ float buf[2][2 * kBatch][kLnThreads / 32];
+    GroupSum<kGroup, 2 * kBatch> sum{buf};
     const int lane = threadIdx.x % kGroup;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
-    float dg[kLnN], db[kLnN];
-#pragma unroll
-    for (int i = 0; i < kLnN; ++i) dg[i] = 0.0f, db[i] = 0.0f;
     auto fetch = [&](int slot, int64_t r) {
         if (r < rows) {
             R::fetch(ring + slot * kStage, x, r, rows, D, lane);
@@ -330,59 +390,82 @@ __global__ void __launch_bounds__(kLnThreads, (kLnBlocksPerSm<T, true>))
     griddep_wait();
     griddep_launch_dependents();
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(s, row + s * stride);
+    for (int s = 0; s < kStages - kBatch; ++s) fetch(s, row + s * stride);
+    float g[kLnN], dg[kLnN], db[kLnN];
+    load_params<R>(gamma, D, lane, 1.0f, g);
+#pragma unroll
+    for (int i = 0; i < kLnN; ++i) dg[i] = 0.0f, db[i] = 0.0f;
     const float inv_d = 1.0f / static_cast<float>(D);
     int slot = 0;
-    for (; row < rows; row += stride, slot = slot + 1 == kStages ? 0 : slot + 1) {
-        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
-        copy_wait<kStages - 2>();
-        if constexpr (!kAligned) {  // the row was copied by the whole group
+    for (; row < rows; row += kBatch * stride) {
+        float mean[kBatch], rstd[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool live = row + k * stride < rows;
+            mean[k] = live ? __ldg(mean_in + row + k * stride) : 0.0f;
+            rstd[k] = live ? __ldg(rstd_in + row + k * stride) : 0.0f;
+        }
+        copy_wait<kStages - 2 * kBatch>();
+        if constexpr (!kAligned) {  // the rows were copied by the whole group
             if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
             else __syncwarp();
         }
-        fetch(slot == 0 ? kStages - 1 : slot - 1, row + (kStages - 1) * stride);  // read in the previous round
-        const uint8_t* xs = ring + slot * kStage;
-        const uint8_t* ds = xs + kTensorBytes<T>;
-        float2 s = make_float2(0.0f, 0.0f);  // sums of g and of g xhat
+        const int last = slot == 0 ? kStages - kBatch : slot - kBatch;  // read in the last round
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = R::index(i, lane);
-            if (j < D) {
-                float g[kVec];
-                load_param<kVec>(gamma, j, 1.0f, g);
-                const auto px = R::get(xs, x, row, D, i, lane);
-                const auto pd = R::get(ds, dy, row, D, i, lane);
+        for (int k = 0; k < kBatch; ++k) fetch(last + k, row + (kStages - kBatch + k) * stride);
+        float s[2 * kBatch];  // per row, the sums of g dy and of g dy xhat
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float d = to_float(pd.v[e]);
-                    const float xhat = (to_float(px.v[e]) - mean) * rstd;
-                    dg[i * kVec + e] += d * xhat;
-                    db[i * kVec + e] += d;
-                    s.x += d * g[e];
-                    s.y += d * g[e] * xhat;
+        for (int k = 0; k < kBatch; ++k) {
+            const bool live = row + k * stride < rows;
+            const uint8_t* xs = ring + (slot + k) * kStage;
+            const uint8_t* ds = xs + kTensorBytes<T>;
+            s[2 * k] = 0.0f;
+            s[2 * k + 1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                if (live && R::index(i, lane) < D) {
+                    const auto px = R::get(xs, x, row + k * stride, D, i, lane);
+                    const auto pd = R::get(ds, dy, row + k * stride, D, i, lane);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const int n = i * kVec + e;
+                        const float d = to_float(pd.v[e]);
+                        const float xhat = (to_float(px.v[e]) - mean[k]) * rstd[k];
+                        const float dgx = d * g[n];
+                        dg[n] = fmaf(d, xhat, dg[n]);
+                        db[n] += d;
+                        s[2 * k] += dgx;
+                        s[2 * k + 1] = fmaf(dgx, xhat, s[2 * k + 1]);
+                    }
                 }
             }
         }
-        s = sum(s);
-        s.x *= inv_d;
-        s.y *= inv_d;
+        sum(s);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = R::index(i, lane);
-            if (j < D) {
-                float g[kVec];
-                load_param<kVec>(gamma, j, 1.0f, g);
-                const auto px = R::get(xs, x, row, D, i, lane);
-                const auto pd = R::get(ds, dy, row, D, i, lane);
-                Pack<T, kVec> p;
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t r = row + k * stride;
+            if (r >= rows) break;
+            const uint8_t* xs = ring + (slot + k) * kStage;
+            const uint8_t* ds = xs + kTensorBytes<T>;
+            const float sg = s[2 * k] * inv_d, sgx = s[2 * k + 1] * inv_d;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float xhat = (to_float(px.v[e]) - mean) * rstd;
-                    p.v[e] = from_float<T>(rstd * (to_float(pd.v[e]) * g[e] - s.x - xhat * s.y));
+            for (int i = 0; i < kVecs; ++i) {
+                const int j = R::index(i, lane);
+                if (j < D) {
+                    const auto px = R::get(xs, x, r, D, i, lane);
+                    const auto pd = R::get(ds, dy, r, D, i, lane);
+                    Pack<T, kVec> p;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const float xhat = (to_float(px.v[e]) - mean[k]) * rstd[k];
+                        const float t = fmaf(to_float(pd.v[e]), g[i * kVec + e], -sg);
+                        p.v[e] = from_float<T>(rstd[k] * fmaf(-xhat, sgx, t));
+                    }
+                    *reinterpret_cast<Pack<T, kVec>*>(dx + r * D + j) = p;
                 }
-                *reinterpret_cast<Pack<T, kVec>*>(dx + row * D + j) = p;
             }
         }
+        slot = slot + kBatch == kStages ? 0 : slot + kBatch;
     }
     if (partial == nullptr) return;
     // the block's row of partial sums: its groups own the same columns, and meet in the ring in group order
@@ -418,8 +501,8 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads)
     k_ln_bwd_long(const T* dy, const T* x, const Param gamma, const float* __restrict__ mean_in,
                   const float* __restrict__ rstd_in, T* dx, int64_t rows, int32_t D, float* __restrict__ partial) {
-    __shared__ float2 buf[2][kLnThreads / 32];
-    GroupSum<kLongThreads> sum{buf};
+    __shared__ float buf[2][2][kLnThreads / 32];
+    GroupSum<kLongThreads, 2> sum{buf};
     griddep_wait();
     griddep_launch_dependents();
     const float inv_d = 1.0f / static_cast<float>(D);
@@ -428,22 +511,22 @@ __global__ void __launch_bounds__(kLongThreads)
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, first = false) {
         const float mean = mean_in[row], rstd = rstd_in[row];
         const T *xr = x + row * D, *dr = dy + row * D;
-        float2 s = make_float2(0.0f, 0.0f);
+        float s[2] = {0.0f, 0.0f};
         for (int j = threadIdx.x; j < D; j += kLongThreads) {
             float g[1];
             load_param<1>(gamma, j, 1.0f, g);
             const float d = to_float(dr[j]), xhat = (to_float(xr[j]) - mean) * rstd;
-            s.x += d * g[0];
-            s.y += d * g[0] * xhat;
+            s[0] += d * g[0];
+            s[1] += d * g[0] * xhat;
         }
-        s = sum(s);
-        s.x *= inv_d;
-        s.y *= inv_d;
+        sum(s);
+        s[0] *= inv_d;
+        s[1] *= inv_d;
         for (int j = threadIdx.x; j < D; j += kLongThreads) {
             float g[1];
             load_param<1>(gamma, j, 1.0f, g);
             const float d = to_float(dr[j]), xhat = (to_float(xr[j]) - mean) * rstd;
-            dx[row * D + j] = from_float<T>(rstd * (d * g[0] - s.x - xhat * s.y));
+            dx[row * D + j] = from_float<T>(rstd * (d * g[0] - s[0] - xhat * s[1]));
             if (mine) {
                 mine[j] = (first ? 0.0f : mine[j]) + d * xhat;
                 mine[D + j] = (first ? 0.0f : mine[D + j]) + d;
@@ -499,10 +582,10 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
-int ln_grid(const LayerNormProblem& p, int rows_per_block, int blocks_per_sm) {
-    const int64_t want = ceil_div(p.T, rows_per_block);
-    return static_cast<int>(std::min<int64_t>({want, static_cast<int64_t>(blocks_per_sm) * p.sm_count,
-                                               static_cast<int64_t>(kLnMaxBlocks)}));
+// One block per SM, fewer for few rows.
+int ln_grid(const LayerNormProblem& p, int rows_per_block) {
+    return static_cast<int>(std::min<int64_t>(
+        {ceil_div(p.T, rows_per_block), static_cast<int64_t>(p.sm_count), static_cast<int64_t>(kLnMaxBlocks)}));
 }
 
 template <typename T, int kGroup, bool kAligned>
@@ -510,7 +593,7 @@ cudaError_t run_fwd(const LayerNormProblem& p, cudaStream_t stream) {
     constexpr int kBytes = kLnSmemBytes<T, false>;
     const cudaError_t e = allow_smem<&k_ln_fwd<T, kGroup, kAligned>>(kBytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_ln_fwd<T, kGroup, kAligned>, dim3(ln_grid(p, kLnThreads / kGroup, kLnBlocksPerSm<T, false>)),
+    return launch_pdl(k_ln_fwd<T, kGroup, kAligned>, dim3(ln_grid(p, kLnThreads / kGroup)),
                       dim3(kLnThreads), kBytes, stream, static_cast<const T*>(p.x), param(p.gamma, p.param_dtype),
                       param(p.beta, p.param_dtype), static_cast<T*>(p.y), p.mean, p.rstd, p.T, p.D, p.eps);
 }
@@ -540,7 +623,7 @@ cudaError_t run_bwd(const LayerNormProblem& p, int* blocks, cudaStream_t stream)
     constexpr int kBytes = kLnSmemBytes<T, true>;
     const cudaError_t e = allow_smem<&k_ln_bwd<T, kGroup, kAligned>>(kBytes);
     if (e != cudaSuccess) return e;
-    *blocks = ln_grid(p, kLnThreads / kGroup, kLnBlocksPerSm<T, true>);
+    *blocks = ln_grid(p, kLnThreads / kGroup);
     return launch_pdl(k_ln_bwd<T, kGroup, kAligned>, dim3(*blocks), dim3(kLnThreads), kBytes, stream,
                       static_cast<const T*>(p.dy), static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), p.mean_in,
                       p.rstd_in, static_cast<T*>(p.dx), p.T, p.D, p.partial);
@@ -558,7 +641,7 @@ cudaError_t dispatch_bwd(const LayerNormProblem& p, int* blocks, cudaStream_t st
 template <typename T>
 cudaError_t bwd_of(const LayerNormProblem& p, int* blocks, cudaStream_t stream) {
     if (p.D > kLnThreads * kLnN) {
-        *blocks = ln_grid(p, 1, 2);
+        *blocks = ln_grid(p, 1);
         return launch_pdl(k_ln_bwd_long<T>, dim3(*blocks), dim3(kLongThreads), 0, stream, static_cast<const T*>(p.dy),
                           static_cast<const T*>(p.x), param(p.gamma, p.param_dtype), p.mean_in, p.rstd_in,
                           static_cast<T*>(p.dx), p.T, p.D, p.partial);

@@ -57,7 +57,7 @@ struct LayerNormProblem {
 };
 // Rows of the parameter-gradient partials: the backward grid has at most this many blocks, which
 // the workspace size is computed from without asking the device.
-constexpr int kLnMaxBlocks = 304;
+constexpr int kLnMaxBlocks = 152;
 constexpr int32_t kLnMaxD = 1 << 24;
 
 moe_status_t launch_layernorm_fwd(const LayerNormProblem& p, cudaStream_t stream);
