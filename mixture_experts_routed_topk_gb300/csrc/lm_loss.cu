@@ -55,7 +55,7 @@ __device__ __forceinline__ float exp2_full(float x) {
 
 // ------------------------------------------------------------------------------------ targets
 
-// Cross entropy: sid[t] = the label, or kNoTarget; coef[t] = dloss[t], or 0 (backward only).
+// Cross entropy's backward: sid[t] = the label, or kNoTarget; coef[t] = dloss[t], or 0.
 __global__ void __launch_bounds__(256) k_lm_labels(const int32_t* __restrict__ targets, int32_t ignore_index,
                                                    int64_t T, int32_t V, const float* __restrict__ dloss,
                                                    int32_t* __restrict__ sid, float* __restrict__ coef,
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) k_lm_labels(const int32_t* __restrict__ t
     if (!ignored && !inside) atomicOr(status, MOE_DEV_BAD_TARGET);
     const bool ok = !ignored && inside;
     sid[t] = ok ? id : kNoTarget;
-    if (coef) coef[t] = ok ? dloss[t] : 0.0f;
+    coef[t] = ok ? dloss[t] : 0.0f;
 }
 
 // Distillation: one warp per row. sid / sp: the kept ids in ascending order (equal ids in the order
@@ -153,6 +153,7 @@ struct LmArgs : GemmArgs {
     int32_t V;           // vocabulary (columns at and past it do not exist)
     int32_t v0;          // first column of the piece
     int32_t group;       // row tiles walked together along the columns
+    int32_t bn;          // columns per logit tile (a multiple of 32, at most 256)
     int32_t K;           // targets per row
     const int32_t* sid;  // [T, K] sorted target ids
     const float* sp;     // [T, K] their probabilities; null: 1
@@ -168,7 +169,7 @@ struct LmArgs : GemmArgs {
 };
 
 struct LmTile {
-    int32_t m, n, kblocks, slice;
+    int32_t m, n, kblocks, slice, bn;
 };
 
 // Row tiles in groups of a.group; within a group columns outermost, so that a group's rows of A stay
@@ -206,21 +207,27 @@ struct LmLogits {
         grouped_mn(tile, a, &t.m, &t.n);
         t.kblocks = a.kblocks;
         t.slice = 0;
+        t.bn = a.bn;
         return t;
     }
     __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
                                 const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
         tma_load_2d(sa, ta, bar, kb * kBK, t.m * kBM);
-        tma_load_2d(sb, tb, bar, kb * kBK, a.v0 + t.n * kBN2);
+        tma_load_2d(sb, tb, bar, kb * kBK, a.v0 + t.n * a.bn);
     }
 };
 
 // Forward: a tile's share of the row's softmax sum, and the targets' logits.
 struct LmLse : LmLogits {
+    __device__ static uint32_t idesc(const Tile& t) {
+        return (kIdesc & ~(63u << 17)) | (static_cast<uint32_t>(t.bn >> 3) << 17);
+    }
+    __device__ static uint32_t tx_bytes(const Tile& t) { return kABytes + t.bn * kBK * 2; }
+
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4*, const Args& a) {
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
         const bool live = row < a.T;
-        const int32_t n0 = t.n * kBN2;
+        const int32_t n0 = t.n * t.bn;
         const float scale2 = a.inv_tau * kLog2e;
         int j = 0;
         int32_t next = kNoTarget;
@@ -231,7 +238,7 @@ struct LmLse : LmLogits {
         }
         float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kBN2 / 32; ++c) {
+        for (int c = 0; c < t.bn / 32; ++c) {
             const int32_t c0 = n0 + 32 * c;
             if (c0 >= a.V) break;  // warp-uniform
             __syncwarp();
@@ -445,52 +452,76 @@ struct LmDw {
 // --------------------------------------------------------------------------------- reductions
 
 // Joins a row's tiles and forms its loss. A block owns 32 rows, one per lane; its warps take the
-// tiles in turn and meet in shared memory in warp order.
+// tiles in turn and meet in shared memory in warp order. Then (distillation) each warp sums the targets
+// of two rows. sp null: cross entropy, where sid holds the labels as the caller gave them.
 constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     k_lm_join(const float2* __restrict__ part, int32_t ntiles, int64_t T, int32_t K, const int32_t* __restrict__ sid,
               const float* __restrict__ sp, const float* __restrict__ zt, const float* __restrict__ ent, float tau,
-              float* __restrict__ loss, float* __restrict__ lse_out) {
+              int32_t ignore_index, int32_t V, float* __restrict__ loss, float* __restrict__ lse_out,
+              uint32_t* __restrict__ status) {
     __shared__ float2 acc[kJoinWarps][32];
+    __shared__ float s_lse[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     griddep_wait();
     griddep_launch_dependents();
     float m = -INFINITY, s = 0.0f;
     if (row < T) {
-        for (int n = warp; n < ntiles; n += kJoinWarps) {
-            const float2 p = part[static_cast<int64_t>(n) * T + row];
+        auto add = [&](const float2& p) {
             const float top = fmaxf(m, p.x);
             s = (s == 0.0f ? 0.0f : s * exp2_fast(m - top)) + (p.y == 0.0f ? 0.0f : p.y * exp2_fast(p.x - top));
             m = top;
+        };
+        int n = warp;
+        for (; n + 3 * kJoinWarps < ntiles; n += 4 * kJoinWarps) {
+            float2 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) p[u] = part[static_cast<int64_t>(n + u * kJoinWarps) * T + row];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(p[u]);
         }
+        for (; n < ntiles; n += kJoinWarps) add(part[static_cast<int64_t>(n) * T + row]);
     }
     acc[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (warp != 0 || row >= T) return;
-    float top = acc[0][lane].x;
+    if (warp == 0 && row < T) {
+        float top = acc[0][lane].x;
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, acc[w][lane].x);
-    s = 0.0f;
+        for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, acc[w][lane].x);
+        s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w)
-        if (acc[w][lane].y != 0.0f) s += acc[w][lane].y * exp2_fast(acc[w][lane].x - top);
-    const float lse = kLn2 * top + logf(s);
-    lse_out[row] = lse;
-    const int32_t* my_sid = sid + row * K;
-    if (sp == nullptr) {
-        loss[row] = my_sid[0] == kNoTarget ? 0.0f : lse - zt[row];
-        return;
+        for (int w = 0; w < kJoinWarps; ++w)
+            if (acc[w][lane].y != 0.0f) s += acc[w][lane].y * exp2_fast(acc[w][lane].x - top);
+        const float lse = kLn2 * top + logf(s);
+        lse_out[row] = lse;
+        s_lse[lane] = lse;
+        if (sp == nullptr) {
+            const int32_t id = sid[row];
+            const bool inside = id >= 0 && id < V, ignored = id == ignore_index;
+            if (!inside && !ignored) atomicOr(status, MOE_DEV_BAD_TARGET);
+            loss[row] = inside && !ignored ? lse - zt[row] : 0.0f;
+        }
     }
-    float l = 0.0f;
-    bool any = false;
-    for (int j = 0; j < K; ++j) {
-        if (my_sid[j] == kNoTarget) break;
-        any = true;
-        const float p = sp[row * K + j];
-        if (p != 0.0f) l += p * (lse - zt[row * K + j]);
+    if (sp == nullptr) return;
+    __syncthreads();
+    for (int r = warp; r < 32; r += kJoinWarps) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + r;
+        if (t >= T) break;
+        const float lse = s_lse[r];
+        float l = 0.0f;
+        bool any = false;
+        for (int j = lane; j < K; j += 32) {
+            if (sid[t * K + j] == kNoTarget) break;  // sorted: nothing after it
+            any = true;
+            const float p = sp[t * K + j];
+            if (p != 0.0f) l += p * (lse - zt[t * K + j]);
+        }
+        __syncwarp();
+        l = warp_sum(l);
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) loss[t] = any ? tau * tau * (ent[t] + l) : 0.0f;
     }
-    loss[row] = any ? tau * tau * (ent[row] + l) : 0.0f;
 }
 
 // dx = bf16( sum over slices in slice order ).
@@ -517,7 +548,8 @@ constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of one dl piece
 constexpr int32_t kMinPiece = 2048;           // but at least this many columns
 
 struct LmPlan {
-    int32_t mtiles, ntiles;  // of the logits
+    int32_t mtiles, ntiles;  // of the logits, in 128 x 256 tiles
+    int32_t fwd_bn, fwd_ntiles;  // the forward's tiles
     int32_t piece;           // columns per piece of the backward (a multiple of 256)
     int32_t dx_ntiles;
     int32_t slices, kb_slice;
@@ -544,6 +576,15 @@ int32_t pick_slices(int64_t tiles, int32_t kblocks, double sum_bytes) {
 void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
     p->mtiles = static_cast<int32_t>(ceil_div(T, kBM));
     p->ntiles = static_cast<int32_t>(ceil_div(V, kBN2));
+    // With one row tile the weights' bytes decide, and every SM should stream as many of them: tiles of
+    // 224 columns instead of 256 for 32000 columns, 143 instead of 125 of the 152 SMs. With more row
+    // tiles the products decide, and 256 columns are the cheapest ones.
+    p->fwd_bn = kBN2;
+    if (p->mtiles == 1) {
+        const int64_t rounds = ceil_div(p->ntiles, kPlanSms);
+        p->fwd_bn = static_cast<int32_t>(std::min<int64_t>(kBN2, ceil_div(ceil_div(V, rounds * kPlanSms), 32) * 32));
+    }
+    p->fwd_ntiles = static_cast<int32_t>(ceil_div(V, p->fwd_bn));
     int64_t piece = kPieceBytes / (2 * T) / kBN2 * kBN2;
     piece = std::max<int64_t>(piece, kMinPiece);
     piece = std::min<int64_t>(piece, static_cast<int64_t>(p->ntiles) * kBN2);
@@ -569,7 +610,7 @@ void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
     p->off_coef = take(4 * t);
     // the forward's partials and the backward's buffers are never alive at once
     const size_t shared = off;
-    p->off_part = take(8 * t * p->ntiles);
+    p->off_part = take(8 * t * p->fwd_ntiles);
     const size_t fwd_end = off;
     off = shared;
     p->off_dl = take(2 * t * p->piece);
@@ -602,6 +643,7 @@ moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward
     if (cudaMemsetAsync(status, 0, sizeof(uint32_t), stream) != cudaSuccess) return MOE_ERR_CUDA;
     float* coef = backward ? at<float>(p, pl.off_coef) : nullptr;
     cudaError_t e;
+    if (p.teacher_ids == nullptr && !backward) return MOE_OK;  // the forward takes the labels as they are
     if (p.teacher_ids == nullptr)
         e = launch_pdl(k_lm_labels, dim3(static_cast<unsigned>(ceil_div(p.T, 256))), dim3(256), 0, stream, p.targets,
                        p.ignore_index, p.T, p.V, p.dloss, at<int32_t>(p, pl.off_sid), coef, status);
@@ -638,22 +680,26 @@ moe_status_t launch_lm_fwd(const LmProblem& p, cudaStream_t stream) {
     LmPlan pl{};
     make_plan(p.T, p.D, p.V, p.K, &pl);
     CUtensorMap tx, tw;
-    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2)) return MOE_ERR_CUDA;
+    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, pl.fwd_bn)) return MOE_ERR_CUDA;
     moe_status_t st = prepare_targets(p, pl, false, stream);
     if (st != MOE_OK) return st;
     LmArgs a = common_args(p, pl);
+    // a label outside the vocabulary finds no tile; the join tells ignored labels from wrong ones
+    if (p.targets) a.sid = p.targets;
     a.mtiles = pl.mtiles;
-    a.ntiles = pl.ntiles;
+    a.ntiles = pl.fwd_ntiles;
+    a.bn = pl.fwd_bn;
     a.kblocks = p.D / kBK;
     a.group = row_group(2ll * p.D, pl.mtiles);
     a.zt = at<float>(p, pl.off_zt);
     a.part = at<float2>(p, pl.off_part);
-    st = launch_gemm<LmLse>(tx, tw, a, sm_count_grid(static_cast<int64_t>(pl.mtiles) * pl.ntiles, p.sm_count), stream);
+    st = launch_gemm<LmLse>(tx, tw, a, sm_count_grid(static_cast<int64_t>(pl.mtiles) * pl.fwd_ntiles, p.sm_count),
+                            stream);
     if (st != MOE_OK) return st;
     return launch_pdl(k_lm_join, dim3(static_cast<unsigned>(ceil_div(p.T, 32))), dim3(32 * kJoinWarps), 0, stream,
-                      static_cast<const float2*>(a.part), pl.ntiles, p.T, p.K, a.sid, a.sp,
+                      static_cast<const float2*>(a.part), pl.fwd_ntiles, p.T, p.K, a.sid, a.sp,
                       static_cast<const float*>(a.zt), static_cast<const float*>(at<float>(p, pl.off_ent)),
-                      p.temperature, p.loss, p.lse) == cudaSuccess
+                      p.temperature, p.ignore_index, p.V, p.loss, p.lse, a.status) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -682,6 +728,7 @@ moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
         a.coef = at<float>(p, pl.off_coef);
         a.mtiles = pl.mtiles;
         a.ntiles = cols / kBN2;
+        a.bn = kBN2;
         a.kblocks = p.D / kBK;
         a.group = row_group(2ll * p.D, pl.mtiles);
         a.out0 = dl;

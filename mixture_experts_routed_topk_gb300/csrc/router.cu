@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kRouterThreads)
     int32_t* my_ids = ids + row * K;
     float* my_scores = scores + row * K;
     int32_t id_k = 0;  // lane k % 32 keeps choice k until 32 of them are stored at once
-    float e_k = 0.0f;
+    float v_k = 0.0f, e_k = 0.0f, part = 0.0f;
     for (int k = 0; k < K; ++k) {
         uint32_t best = 0u;
         int at = 0;
@@ -118,9 +118,8 @@ __global__ void __launch_bounds__(kRouterThreads)
         for (int i = 0; i < kN; ++i)
             if (key[i] > best) best = key[i], at = i;
         const uint2 top = red.argmax(best, expert_of<kThreads, kVec>(at, t));
-        const float v = key_value(top.x);
         if (k == 0) {
-            m = v;
+            m = key_value(top.x);
             if (!normalize) {
                 float s = 0.0f;
 #pragma unroll
@@ -129,26 +128,32 @@ __global__ void __launch_bounds__(kRouterThreads)
                 total = red.sum(s);
             }
         }
-        const float e = expf(v - m);
-        if (normalize) total += e;
         if (t == (k & 31)) {
             id_k = static_cast<int32_t>(top.y);
-            e_k = e;
+            v_k = key_value(top.x);
         }
-        if ((k & 31) == 31 && K > 32 && t < 32) {  // more than a warp's worth: scaled below
+        const int own = static_cast<int>(top.y) - t * kVec;  // its place among this thread's, if it is one
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (own == expert_of<kThreads, kVec>(i, 0)) key[i] = 0u;
+        if ((k & 31) == 31 && t < 32) {  // a warp's worth of choices; scaled below
+            e_k = expf(v_k - m);
+            part += e_k;
             my_ids[k - 31 + t] = id_k;
             my_scores[k - 31 + t] = e_k;
         }
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (expert_of<kThreads, kVec>(i, t) == static_cast<int>(top.y)) key[i] = 0u;
     }
-    // a row with nothing but -inf has scores of 0
-    const bool none = m == -INFINITY;
-    const float inv = 1.0f / total;
     if (t >= 32) return;
-    const int rest = K > 32 ? K & ~31 : 0;  // choices [rest, K) are still in registers
-    if (rest + t < K) {
+    const int rest = K & ~31;  // choices [rest, K) are still in registers
+    const bool mine = rest + t < K;
+    if (mine) {
+        e_k = expf(v_k - m);
+        part += e_k;
+    }
+    if (normalize) total = warp_sum(part);
+    const bool none = m == -INFINITY;  // a row with nothing but -inf has scores of 0
+    const float inv = 1.0f / total;
+    if (mine) {
         my_ids[rest + t] = id_k;
         my_scores[rest + t] = none ? 0.0f : e_k * inv;
     }
