@@ -396,15 +396,23 @@ __global__ void __launch_bounds__(kLnThreads, 1)
 #pragma unroll
     for (int i = 0; i < kLnN; ++i) dg[i] = 0.0f, db[i] = 0.0f;
     const float inv_d = 1.0f / static_cast<float>(D);
+    // the rows' statistics, loaded a round ahead
+    float next_mean[kBatch], next_rstd[kBatch];
+    auto load_stats = [&](int64_t first) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool live = first + k * stride < rows;
+            next_mean[k] = live ? __ldg(mean_in + first + k * stride) : 0.0f;
+            next_rstd[k] = live ? __ldg(rstd_in + first + k * stride) : 0.0f;
+        }
+    };
+    load_stats(row);
     int slot = 0;
     for (; row < rows; row += kBatch * stride) {
         float mean[kBatch], rstd[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const bool live = row + k * stride < rows;
-            mean[k] = live ? __ldg(mean_in + row + k * stride) : 0.0f;
-            rstd[k] = live ? __ldg(rstd_in + row + k * stride) : 0.0f;
-        }
+        for (int k = 0; k < kBatch; ++k) mean[k] = next_mean[k], rstd[k] = next_rstd[k];
+        load_stats(row + kBatch * stride);
         copy_wait<kStages - 2 * kBatch>();
         if constexpr (!kAligned) {  // the rows were copied by the whole group
             if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
