@@ -159,7 +159,8 @@ struct LmArgs : GemmArgs {
     const float* sp;     // [T, K] their probabilities; null: 1
     float* zt;           // [T, K] out: the targets' logits
     float2* part;        // [ntiles][T] out: (maximum, sum) of the tile's exponentials, base 2
-    float inv_tau;
+    float zscale;        // accumulator to scaled logit (logit_scale)
+    float scale2;        // the same in units of log 2, for base-2 exponentials
     const float* lse;    // [T]
     const float* coef;   // [T]
     int32_t pitch;       // row length of the dl piece
@@ -228,7 +229,7 @@ struct LmLse : LmLogits {
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
         const bool live = row < a.T;
         const int32_t n0 = t.n * t.bn;
-        const float scale2 = a.inv_tau * kLog2e;
+        const float scale2 = a.scale2;
         int j = 0;
         int32_t next = kNoTarget;
         const int32_t* sid = a.sid + row * a.K;
@@ -255,7 +256,7 @@ struct LmLse : LmLogits {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (next == c0 + i) z = w[i];
-                a.zt[row * a.K + j] = __uint_as_float(z) * a.inv_tau;
+                a.zt[row * a.K + j] = __uint_as_float(z) * a.zscale;
                 ++j;
                 next = j < a.K ? __ldg(sid + j) : kNoTarget;
             }
@@ -279,7 +280,7 @@ struct LmDlogits : LmLogits {
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
         const bool live = row < a.T;
         const int32_t n0 = a.v0 + t.n * kBN2;
-        const float scale2 = a.inv_tau * kLog2e;
+        const float scale2 = a.scale2;
         float coef = 0.0f, lse2 = 0.0f;
         int j = 0;
         int32_t next = kNoTarget;
@@ -654,6 +655,14 @@ moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// 1 / temperature, and what the tensor cores' accumulation takes off. They cut the fp32 accumulator's low
+// bits off after each 16 products, towards zero: a logit comes out too small by 1.5e-8 to 1.6e-8 of itself
+// per such step (measured for D = 256 to 7168 on rows that lean towards their target). 2^-26 per step is
+// given back. Relative error of the loss at D = 4096, before and after: rows that lean towards their target
+// 1.2e-5 and 1.5e-6, normal rows 6.1e-7 and 2.5e-7, rows with two thirds of their weight in a few columns
+// 7.4e-7 and 3.0e-7; rows with 2 % of their elements, which lose nothing, 5e-8 and 5e-7.
+double logit_scale(int32_t D, float temperature) { return (1.0 + D * 0x1p-30) / static_cast<double>(temperature); }
+
 LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     LmArgs a{};
     a.T = p.T;
@@ -662,7 +671,9 @@ LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     a.K = p.K;
     a.sid = at<int32_t>(p, pl.off_sid);
     a.sp = p.teacher_ids ? at<float>(p, pl.off_sp) : nullptr;
-    a.inv_tau = 1.0f / p.temperature;
+    const double scale = logit_scale(p.D, p.temperature);
+    a.zscale = static_cast<float>(scale);
+    a.scale2 = static_cast<float>(scale * 1.4426950408889634);
     a.status = reinterpret_cast<uint32_t*>(p.ws);
     return a;
 }
