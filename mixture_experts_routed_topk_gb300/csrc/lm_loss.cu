@@ -154,6 +154,7 @@ struct LmArgs : GemmArgs {
     int32_t v0;          // first column of the piece
     int32_t group;       // row tiles walked together along the columns
     int32_t bn;          // columns per logit tile (a multiple of 32, at most 256)
+    int32_t bm;          // rows of x (or dl) that a tile loads (box_rows)
     int32_t K;           // targets per row
     const int32_t* sid;  // [T, K] sorted target ids
     const float* sp;     // [T, K] their probabilities; null: 1
@@ -170,7 +171,7 @@ struct LmArgs : GemmArgs {
 };
 
 struct LmTile {
-    int32_t m, n, kblocks, slice, bn;
+    int32_t m, n, kblocks, slice, bn, bm;
 };
 
 // Row tiles in groups of a.group; within a group columns outermost, so that a group's rows of A stay
@@ -209,8 +210,13 @@ struct LmLogits {
         t.kblocks = a.kblocks;
         t.slice = 0;
         t.bn = a.bn;
+        t.bm = a.bm;
         return t;
     }
+    __device__ static uint32_t idesc(const Tile& t) {
+        return (kIdesc & ~(63u << 17)) | (static_cast<uint32_t>(t.bn >> 3) << 17);
+    }
+    __device__ static uint32_t tx_bytes(const Tile& t) { return (t.bm + t.bn) * kBK * 2; }
     __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
                                 const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
         tma_load_2d(sa, ta, bar, kb * kBK, t.m * kBM);
@@ -220,11 +226,6 @@ struct LmLogits {
 
 // Forward: a tile's share of the row's softmax sum, and the targets' logits.
 struct LmLse : LmLogits {
-    __device__ static uint32_t idesc(const Tile& t) {
-        return (kIdesc & ~(63u << 17)) | (static_cast<uint32_t>(t.bn >> 3) << 17);
-    }
-    __device__ static uint32_t tx_bytes(const Tile& t) { return kABytes + t.bn * kBK * 2; }
-
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4*, const Args& a) {
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
         const bool live = row < a.T;
@@ -356,8 +357,12 @@ struct LmDx {
         t.slice = tile / per_slice;
         grouped_mn(tile - t.slice * per_slice, a, &t.m, &t.n);
         t.kblocks = min(a.kb_slice, a.kblocks - t.slice * a.kb_slice);
+        t.bn = kBN2;
+        t.bm = a.bm;
         return t;
     }
+    __device__ static uint32_t idesc(const Tile&) { return kIdesc; }
+    __device__ static uint32_t tx_bytes(const Tile& t) { return (t.bm + kBN2) * kBK * 2; }
     __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
                                 const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
         const int32_t k = (t.slice * a.kb_slice + kb) * kBK;
@@ -533,7 +538,15 @@ __global__ void __launch_bounds__(256) k_lm_sum_slices(const float4* __restrict_
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4;
          i += static_cast<int64_t>(gridDim.x) * 256) {
         float4 a = sums[i];
-        for (int s = 1; s < slices; ++s) {
+        int s = 1;
+        for (; s + 7 < slices; s += 8) {  // eight loads at a time, added in slice order
+            float4 b[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) b[u] = sums[(s + u) * n4 + i];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) a.x += b[u].x, a.y += b[u].y, a.z += b[u].z, a.w += b[u].w;
+        }
+        for (; s < slices; ++s) {
             const float4 b = sums[s * n4 + i];
             a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
         }
@@ -574,17 +587,23 @@ int32_t pick_slices(int64_t tiles, int32_t kblocks, double sum_bytes) {
     return best;
 }
 
+// Columns of the forward's tiles: a grid whose last round is nearly empty is worse than one of narrower
+// tiles (one row tile and 32000 columns: 143 tiles of 224 for the 152 SMs instead of 125 of 256), and
+// each tile costs what some 32 columns do besides its own.
+int32_t pick_columns(int64_t mtiles, int32_t V) {
+    int32_t best = kBN2;
+    int64_t best_cost = INT64_MAX;
+    for (int32_t bn = kBN2; bn >= 32; bn -= 32) {
+        const int64_t cost = ceil_div(mtiles * ceil_div(V, bn), kPlanSms) * (bn + 32);
+        if (cost < best_cost) best_cost = cost, best = bn;
+    }
+    return best;
+}
+
 void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
     p->mtiles = static_cast<int32_t>(ceil_div(T, kBM));
     p->ntiles = static_cast<int32_t>(ceil_div(V, kBN2));
-    // With one row tile the weights' bytes decide, and every SM should stream as many of them: tiles of
-    // 224 columns instead of 256 for 32000 columns, 143 instead of 125 of the 152 SMs. With more row
-    // tiles the products decide, and 256 columns are the cheapest ones.
-    p->fwd_bn = kBN2;
-    if (p->mtiles == 1) {
-        const int64_t rounds = ceil_div(p->ntiles, kPlanSms);
-        p->fwd_bn = static_cast<int32_t>(std::min<int64_t>(kBN2, ceil_div(ceil_div(V, rounds * kPlanSms), 32) * 32));
-    }
+    p->fwd_bn = pick_columns(p->mtiles, V);
     p->fwd_ntiles = static_cast<int32_t>(ceil_div(V, p->fwd_bn));
     int64_t piece = kPieceBytes / (2 * T) / kBN2 * kBN2;
     piece = std::max<int64_t>(piece, kMinPiece);
@@ -639,6 +658,10 @@ int32_t row_group(int64_t row_bytes, int32_t mtiles) {
     return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(g, mtiles)));
 }
 
+// Rows of the A box. A single row tile loads only the rows there are: the rest of the stage keeps what it
+// held, and the products' rows that come of it are not looked at (rows do not mix in a product).
+uint32_t box_rows(int64_t T) { return static_cast<uint32_t>(T >= kBM ? kBM : ceil_div(T, 8) * 8); }
+
 moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward, cudaStream_t stream) {
     uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
     if (cudaMemsetAsync(status, 0, sizeof(uint32_t), stream) != cudaSuccess) return MOE_ERR_CUDA;
@@ -669,6 +692,7 @@ LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     a.D = p.D;
     a.V = p.V;
     a.K = p.K;
+    a.bm = static_cast<int32_t>(box_rows(p.T));
     a.sid = at<int32_t>(p, pl.off_sid);
     a.sp = p.teacher_ids ? at<float>(p, pl.off_sp) : nullptr;
     const double scale = logit_scale(p.D, p.temperature);
@@ -691,7 +715,7 @@ moe_status_t launch_lm_fwd(const LmProblem& p, cudaStream_t stream) {
     LmPlan pl{};
     make_plan(p.T, p.D, p.V, p.K, &pl);
     CUtensorMap tx, tw;
-    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, pl.fwd_bn)) return MOE_ERR_CUDA;
+    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, box_rows(p.T)) || !make_tmap(&tw, p.w, p.D, p.V, kBK, pl.fwd_bn)) return MOE_ERR_CUDA;
     moe_status_t st = prepare_targets(p, pl, false, stream);
     if (st != MOE_OK) return st;
     LmArgs a = common_args(p, pl);
@@ -721,8 +745,8 @@ moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
     __nv_bfloat16* dl = at<__nv_bfloat16>(p, pl.off_dl);
     float* sums = at<float>(p, pl.off_sums);
     CUtensorMap tx, tw, tdl, tw_mn, tdl_mn, tx_mn;
-    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, kBM) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2) ||
-        !make_tmap(&tdl, dl, pl.piece, p.T, kBK, kBM) || !make_tmap(&tw_mn, p.w, p.D, p.V, 64, kBK) ||
+    if (!make_tmap(&tx, p.x, p.D, p.T, kBK, box_rows(p.T)) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2) ||
+        !make_tmap(&tdl, dl, pl.piece, p.T, kBK, box_rows(p.T)) || !make_tmap(&tw_mn, p.w, p.D, p.V, 64, kBK) ||
         !make_tmap(&tdl_mn, dl, pl.piece, p.T, 64, kBK) || !make_tmap(&tx_mn, p.x, p.D, p.T, 64, kBK))
         return MOE_ERR_CUDA;
     moe_status_t st = prepare_targets(p, pl, true, stream);
