@@ -604,7 +604,7 @@ moe_status_t moe_router_topk_fwd(const void *logits, int32_t dtype, int32_t *top
  *   normalize  = 0:  dz_i = p_i ([i chosen] ds_i - sum_j s_j ds_j) at every expert
  * logits, topk_ids (distinct in each row) and normalize as in the forward call; dlogits has the
  * logits' type and shape, and is written in full. An id outside [0, E) is passed over. Rows of
- * nothing but -inf get zeros.
+ * nothing but -inf get zeros. dlogits may not alias logits.
  */
 moe_status_t moe_router_topk_bwd(const void *logits, int32_t dtype, const int32_t *topk_ids,
                                  const float *dscores, void *dlogits, int64_t T, int32_t E, int32_t K,

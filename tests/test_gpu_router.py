@@ -88,6 +88,29 @@ def test_a_broken_row_shows_and_stays_alone():
     assert torch.equal(ids[keep], want[0][keep]) and torch.equal(scores[keep], want[1][keep])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_a_nan_of_either_sign_sorts_above_all(dtype):
+    z = rand(3, 64, seed=16, dtype=dtype)
+    z[0, 9] = torch.inf
+    z[0, 20] = float("nan")
+    z[1, 30] = -torch.tensor(float("nan"), dtype=dtype)
+    z[1, 31] = torch.copysign(torch.tensor(float("nan"), dtype=dtype), torch.tensor(-1.0, dtype=dtype))
+    for normalize in (True, False):
+        ids, scores = fwd(z, 3, normalize)
+        assert ids[0].tolist()[:2] == [20, 9] and ids[1].tolist()[:2] == [30, 31]
+        assert torch.isnan(scores[:2]).all() and not torch.isnan(scores[2]).any()
+
+
+@pytest.mark.parametrize("E,K", [(256, 8), (200, 40), (64, 1)])
+def test_logits_that_differ_only_in_their_last_bits(E, K):
+    # closer than the upper 24 bits tell, in and at the edge of the choice, in ascending and mixed order
+    near = 1.0 + torch.arange(E, dtype=torch.float64) * 2.0 ** -23
+    z = torch.stack([near, near.flip(0), near[torch.randperm(E, generator=torch.Generator().manual_seed(1))],
+                     torch.cat([4 + torch.arange(K, dtype=torch.float64), near[K:]])]).float()
+    for normalize in (True, False):
+        compare(z, K, normalize, seed=17)
+
+
 def test_ids_outside_are_passed_over():
     z, ds = rand(2, 16, seed=7), torch.ones(2, 3)
     ids = torch.tensor([[4, -1, 16], [2, 1 << 30, 5]], dtype=torch.int32)
