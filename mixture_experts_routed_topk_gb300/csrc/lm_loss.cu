@@ -196,6 +196,56 @@ __device__ __forceinline__ int first_target(const int32_t* sid, int32_t K, int32
     return lo;
 }
 
+// Stores 128 bytes of each of the warp's 32 rows, `pitch` bytes apart from base on (the first `live` of
+// them): through the staging rows, so that each store instruction writes four whole 128-byte segments.
+__device__ __forceinline__ void store_rows(uint4* stage, const uint32_t (&words)[32], char* base, int64_t pitch,
+                                           int live) {
+    const int lane = threadIdx.x & 31;
+    uint4* mine = stage + lane * kStageRowU4;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        mine[c] = make_uint4(words[4 * c], words[4 * c + 1], words[4 * c + 2], words[4 * c + 3]);
+    __syncwarp();
+    char* dst = base + (lane >> 3) * pitch + 16 * (lane & 7);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (4 * j + (lane >> 3) < live)
+            *reinterpret_cast<uint4*>(dst + 4 * j * pitch) = stage[(4 * j + (lane >> 3)) * kStageRowU4 + (lane & 7)];
+    __syncwarp();
+}
+
+// The warp's 32 rows of a 128 x 256 accumulator as bf16: columns [0, cols) (cols a multiple of 64) to rows
+// `pitch` elements apart from base on. The next 64 columns leave tensor memory while these are stored.
+__device__ __forceinline__ void store_tile_bf16(uint32_t taddr, uint4* stage, __nv_bfloat16* base, int64_t pitch,
+                                                int32_t cols, int live) {
+    uint32_t v0[32], v1[32];
+    __syncwarp();
+    tmem_ld_32cols(taddr, v0);
+    tmem_ld_32cols(taddr + 32, v1);
+#pragma unroll 1
+    for (int32_t c = 0; c < cols; c += 64) {
+        tmem_ld_wait(v0);
+        tmem_ld_tie(v1);
+        uint32_t words[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            words[i] = pack_bf16x2(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1]));
+            words[16 + i] = pack_bf16x2(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1]));
+        }
+        if (c + 64 < cols) {
+            tmem_ld_32cols(taddr + c + 64, v0);
+            tmem_ld_32cols(taddr + c + 96, v1);
+        }
+        store_rows(stage, words, reinterpret_cast<char*>(base + c), 2 * pitch, live);
+    }
+}
+
+// Rows of the warp's 32, from `first` on, that lie below `limit`.
+__device__ __forceinline__ int live_rows(int64_t first, int64_t limit) {
+    const int64_t n = limit - first;
+    return n >= 32 ? 32 : n > 0 ? static_cast<int>(n) : 0;
+}
+
 // A = x rows, B = W rows, both K-major; K = D.
 struct LmLogits {
     using Args = LmArgs;
@@ -278,6 +328,7 @@ struct LmLse : LmLogits {
 // Backward: the tile's dl in bf16 into the piece [T, pitch]; columns past the vocabulary get zeros.
 struct LmDlogits : LmLogits {
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
+        const int lane = threadIdx.x & 31;
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
         const bool live = row < a.T;
         const int32_t n0 = a.v0 + t.n * kBN2;
@@ -321,25 +372,11 @@ struct LmDlogits : LmLogits {
                 for (int i = 0; i < 16; ++i) words[16 * half + i] = pack_bf16x2(d[2 * i], d[2 * i + 1]);
             }
             __syncwarp();
-            warp_store_row_segments(
-                stage, words, reinterpret_cast<char*>(a.out0 + row * a.pitch + t.n * kBN2 + 64 * cp), live);
+            store_rows(stage, words, reinterpret_cast<char*>(a.out0 + (row - lane) * a.pitch + t.n * kBN2 + 64 * cp),
+                       2ll * a.pitch, live_rows(row - lane, a.T));
         }
     }
 };
-
-// This warp's 64 accumulator columns at taddr as packed bf16.
-__device__ __forceinline__ void tmem_bf16_64(uint32_t taddr, uint32_t (&words)[32]) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        __syncwarp();
-        uint32_t w[32];
-        tmem_ld_32cols(taddr + 32 * half, w);
-        tmem_ld_wait(w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            words[16 * half + i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    }
-}
 
 // dx: A = dl piece rows (K-major, K = the piece's columns), B = W read MN-major as B[n = d][k = v].
 struct LmDx {
@@ -373,27 +410,20 @@ struct LmDx {
     }
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
         const int lane = threadIdx.x & 31;
-        const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
-        const bool live = row < a.T;
+        const int64_t row0 = static_cast<int64_t>(t.m) * kBM + row_in_tile - lane;  // the warp's first
+        const int live = live_rows(row0, a.T);
+        const int32_t d_tile = t.n * kBN2;
         if (a.direct) {
-#pragma unroll 1
-            for (int cp = 0; cp < kBN2 / 64; ++cp) {
-                uint32_t words[32];
-                tmem_bf16_64(taddr + 64 * cp, words);
-                const int32_t d0 = t.n * kBN2 + 64 * cp;
-                warp_store_row_segments(stage, words, reinterpret_cast<char*>(a.out0 + row * a.D + d0),
-                                        live && d0 < a.D);
-            }
+            store_tile_bf16(taddr, stage, a.out0 + row0 * a.D + d_tile, a.D, min(kBN2, a.D - d_tile), live);
             return;
         }
         float* sums = a.fout + static_cast<int64_t>(t.slice) * a.T * a.D;
 #pragma unroll 1
         for (int c = 0; c < kBN2 / 32; ++c) {
-            const int32_t d0 = t.n * kBN2 + 32 * c;
+            const int32_t d0 = d_tile + 32 * c;
             if (d0 >= a.D) break;  // warp-uniform
             uint32_t before[32];
             if (a.accumulate) {  // this warp's 32 rows of 32 sums, in whole 128-byte row segments
-                const int64_t row0 = row - lane;
                 uint4 v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -419,7 +449,7 @@ struct LmDx {
                 for (int i = 0; i < 32; ++i)
                     w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(before[i]));
             }
-            warp_store_row_segments(stage, w, reinterpret_cast<char*>(sums + row * a.D + d0), live);
+            store_rows(stage, w, reinterpret_cast<char*>(sums + row0 * a.D + d0), 4ll * a.D, live);
         }
     }
 };
@@ -443,15 +473,9 @@ struct LmDw {
             tma_load_2d(sb + j * kMnBoxBytes, tb, bar, t.n * kBN2 + 64 * j, kb * kBK);
     }
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
-        const int64_t v = static_cast<int64_t>(a.v0) + t.m * kBM + row_in_tile;
-#pragma unroll 1
-        for (int cp = 0; cp < kBN2 / 64; ++cp) {
-            uint32_t words[32];
-            tmem_bf16_64(taddr + 64 * cp, words);
-            const int32_t d0 = t.n * kBN2 + 64 * cp;
-            warp_store_row_segments(stage, words, reinterpret_cast<char*>(a.out0 + v * a.D + d0),
-                                    v < a.V && d0 < a.D);
-        }
+        const int64_t v = static_cast<int64_t>(a.v0) + t.m * kBM + row_in_tile - (threadIdx.x & 31);
+        const int32_t d0 = t.n * kBN2;
+        store_tile_bf16(taddr, stage, a.out0 + v * a.D + d0, a.D, min(kBN2, a.D - d0), live_rows(v, a.V));
     }
 };
 
@@ -793,7 +817,7 @@ moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
             c.mtiles = cols / kBM;
             c.ntiles = pl.dx_ntiles;
             c.kblocks = static_cast<int32_t>(ceil_div(p.T, kBK));
-            c.group = row_group(2ll * p.T, c.mtiles);
+            c.group = std::max(1, std::min(kPlanSms / c.ntiles, c.mtiles));
             c.out0 = static_cast<__nv_bfloat16*>(p.dw);
             st = launch_gemm<LmDw>(tdl_mn, tx_mn, c,
                                    sm_count_grid(static_cast<int64_t>(c.mtiles) * c.ntiles, p.sm_count), stream);
