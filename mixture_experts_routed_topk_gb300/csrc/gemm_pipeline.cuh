@@ -51,6 +51,9 @@
 //   __device__ static uint32_t idesc(const Tile&), tx_bytes(const Tile&)
 //        per-tile instruction descriptor and stage transaction bytes, for policies whose tiles
 //        differ in N (default: kIdesc and the shape's kTxBytes)
+//   __device__ static bool a_mn_major(const Tile&)
+//        per-tile layout of A in shared memory, for policies whose tiles differ in it (default:
+//        kAMnMajor); their idesc(t) has to say the same
 //   static constexpr bool kDynamicSchedule = true
 //        CTAs take tiles in list order from the global counter args.ticket (zero on entry)
 //        instead of the fixed c, c + grid, ...: the producer takes a tile, decodes it and hands it
@@ -266,6 +269,12 @@ struct HasTileShape : std::false_type {};
 template <class P>
 struct HasTileShape<P, std::void_t<decltype(P::idesc(std::declval<const typename P::Tile&>())),
                                    decltype(P::tx_bytes(std::declval<const typename P::Tile&>()))>>
+    : std::true_type {};
+
+template <class P, class = void>
+struct HasTileMajor : std::false_type {};
+template <class P>
+struct HasTileMajor<P, std::void_t<decltype(P::a_mn_major(std::declval<const typename P::Tile&>()))>>
     : std::true_type {};
 
 template <class P, class = void>
@@ -592,9 +601,15 @@ __global__ void __launch_bounds__(gemm_threads<typename ShapeOf<P>::type>(), 1)
                                    idesc, slot, kk, (kb | kk) != 0 ? 1u : 0u);
                     } else {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            mma_bf16_ss(d_tmem, operand_desc<P::kAMnMajor>(a0, kk),
-                                        operand_desc<P::kBMnMajor>(b0, kk), idesc, (kb | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            uint64_t a_desc;
+                            if constexpr (HasTileMajor<P>::value)
+                                a_desc = P::a_mn_major(t) ? operand_desc<true>(a0, kk) : operand_desc<false>(a0, kk);
+                            else
+                                a_desc = operand_desc<P::kAMnMajor>(a0, kk);
+                            mma_bf16_ss(d_tmem, a_desc, operand_desc<P::kBMnMajor>(b0, kk), idesc,
+                                        (kb | kk) != 0 ? 1u : 0u);
+                        }
                     }
                     mma_commit(&ps->empty[s]);  // frees the stage once these MMAs have read it
                     if (!decoded) {

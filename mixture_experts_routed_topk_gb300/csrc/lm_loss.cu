@@ -16,8 +16,8 @@
 //   forward: the epilogue reduces a 128 x 256 logit tile to one (maximum, sum of exponentials) per
 //     row and picks the targets' logits out of it; k_lm_join joins a row's tiles.
 //   backward: over pieces of the vocabulary that fit the workspace, the epilogue of the recomputed
-//     logits writes dl in bf16; two more products turn the piece into its rows of dW and its share
-//     of dx. dx is summed over pieces and over slices of the contraction in fp32 and rounded once.
+//     logits writes dl in bf16; one more grid turns the piece into its rows of dW and its share of
+//     dx. dx is summed over pieces and over slices of the contraction in fp32 and rounded once.
 // Rounding dl to bf16 costs each term of dx and dW at most half a bf16 step, as much as rounding
 // the results; it is what lets the two products use the bf16 tensor cores.
 //
@@ -168,21 +168,25 @@ struct LmArgs : GemmArgs {
     int32_t kb_slice;    // K steps per slice of the contraction (dx)
     bool accumulate;     // dx: add to the slice's sums instead of starting them
     bool direct;         // dx: one slice and one piece, so the tile is the result
+    // the gradients' grid: dx tiles (all slices), then dW's tiles with their own counts
+    int32_t dx_tiles, dw_tiles;
+    int32_t dw_mtiles, dw_kblocks, dw_group;
 };
 
 struct LmTile {
     int32_t m, n, kblocks, slice, bn, bm;
+    bool dw;
 };
 
-// Row tiles in groups of a.group; within a group columns outermost, so that a group's rows of A stay
+// Row tiles in groups; within a group columns outermost, so that a group's rows of A stay
 // in L2 while B streams by once per group.
-__device__ __forceinline__ void grouped_mn(int32_t tile, const LmArgs& a, int32_t* m, int32_t* n) {
-    const int32_t per_group = a.group * a.ntiles;
+__device__ __forceinline__ void grouped_mn(int32_t tile, int32_t group, int32_t mtiles, int32_t ntiles, LmTile* t) {
+    const int32_t per_group = group * ntiles;
     const int32_t g = tile / per_group;
     const int32_t r = tile - g * per_group;
-    const int32_t rows = min(a.group, a.mtiles - g * a.group);
-    *n = r / rows;
-    *m = g * a.group + r - *n * rows;
+    const int32_t rows = min(group, mtiles - g * group);
+    t->n = r / rows;
+    t->m = g * group + r - t->n * rows;
 }
 
 // The row's first sorted target at or past vocabulary id `first`.
@@ -255,10 +259,9 @@ struct LmLogits {
 
     __device__ static int32_t num_tiles(const Args& a) { return a.mtiles * a.ntiles; }
     __device__ static Tile decode(int32_t tile, const Args& a) {
-        Tile t;
-        grouped_mn(tile, a, &t.m, &t.n);
+        Tile t{};
+        grouped_mn(tile, a.group, a.mtiles, a.ntiles, &t);
         t.kblocks = a.kblocks;
-        t.slice = 0;
         t.bn = a.bn;
         t.bm = a.bm;
         return t;
@@ -378,30 +381,56 @@ struct LmDlogits : LmLogits {
     }
 };
 
-// dx: A = dl piece rows (K-major, K = the piece's columns), B = W read MN-major as B[n = d][k = v].
-struct LmDx {
+// The gradients of a piece:
+//   dx:  A = dl piece rows (K-major, K = the piece's columns or a slice of them), B = W read MN-major as
+//        B[n = d][k = v]
+//   dW:  A = dl^T (MN-major: vocabulary contiguous), B = x (MN-major: d contiguous); K = T. TMA returns
+//        zeros for rows past T, so the contraction needs no padding.
+// kTogether: both in one grid, dx's tiles, the long ones, first; SMs take tiles as they get free, so that
+// those that finish early go on with the other gradient. Otherwise one of the two, SMs in step.
+template <bool kTogether>
+struct LmGrads {
     using Args = LmArgs;
     using Tile = LmTile;
-    static constexpr bool kAMnMajor = false, kBMnMajor = true;
+    static constexpr bool kBMnMajor = true;
     static constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBRows, false, true);
+    static constexpr bool kDynamicSchedule = kTogether;
 
-    __device__ static int32_t num_tiles(const Args& a) {
-        return a.mtiles * a.ntiles * ((a.kblocks + a.kb_slice - 1) / a.kb_slice);
-    }
+    __device__ static int32_t num_tiles(const Args& a) { return a.dx_tiles + a.dw_tiles; }
     __device__ static Tile decode(int32_t tile, const Args& a) {
-        Tile t;
-        const int32_t per_slice = a.mtiles * a.ntiles;
-        t.slice = tile / per_slice;
-        grouped_mn(tile - t.slice * per_slice, a, &t.m, &t.n);
-        t.kblocks = min(a.kb_slice, a.kblocks - t.slice * a.kb_slice);
+        Tile t{};
         t.bn = kBN2;
-        t.bm = a.bm;
+        t.dw = tile >= a.dx_tiles;
+        if (t.dw) {
+            grouped_mn(tile - a.dx_tiles, a.dw_group, a.dw_mtiles, a.ntiles, &t);
+            t.kblocks = a.dw_kblocks;
+            t.bm = kBM;
+        } else {
+            const int32_t per_slice = a.mtiles * a.ntiles;
+            t.slice = tile / per_slice;
+            grouped_mn(tile - t.slice * per_slice, a.group, a.mtiles, a.ntiles, &t);
+            t.kblocks = min(a.kb_slice, a.kblocks - t.slice * a.kb_slice);
+            t.bm = a.bm;
+        }
         return t;
     }
-    __device__ static uint32_t idesc(const Tile&) { return kIdesc; }
+    __device__ static bool a_mn_major(const Tile& t) { return t.dw; }
+    __device__ static uint32_t idesc(const Tile& t) {
+        return t.dw ? idesc_bf16_f32(kBM, kBRows, true, true) : kIdesc;
+    }
     __device__ static uint32_t tx_bytes(const Tile& t) { return (t.bm + kBN2) * kBK * 2; }
+    // maps: 0 dl rows, 1 W (64-wide boxes), 2 dl (64-wide boxes), 3 x (64-wide boxes)
     __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
                                 const CUtensorMap* ta, const CUtensorMap* tb, const Args& a) {
+        if (t.dw) {
+#pragma unroll
+            for (int j = 0; j < kBM / 64; ++j)
+                tma_load_2d(sa + j * kMnBoxBytes, ta + 2, bar, t.m * kBM + 64 * j, kb * kBK);
+#pragma unroll
+            for (int j = 0; j < kBRows / 64; ++j)
+                tma_load_2d(sb + j * kMnBoxBytes, ta + 3, bar, t.n * kBN2 + 64 * j, kb * kBK);
+            return;
+        }
         const int32_t k = (t.slice * a.kb_slice + kb) * kBK;
         tma_load_2d(sa, ta, bar, k, t.m * kBM);
 #pragma unroll
@@ -409,6 +438,12 @@ struct LmDx {
             tma_load_2d(sb + j * kMnBoxBytes, tb, bar, t.n * kBN2 + 64 * j, a.v0 + k);
     }
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
+        if (t.dw) {
+            const int64_t v = static_cast<int64_t>(a.v0) + t.m * kBM + row_in_tile - (threadIdx.x & 31);
+            const int32_t d0 = t.n * kBN2;
+            store_tile_bf16(taddr, stage, a.out1 + v * a.D + d0, a.D, min(kBN2, a.D - d0), live_rows(v, a.V));
+            return;
+        }
         const int lane = threadIdx.x & 31;
         const int64_t row0 = static_cast<int64_t>(t.m) * kBM + row_in_tile - lane;  // the warp's first
         const int live = live_rows(row0, a.T);
@@ -451,31 +486,6 @@ struct LmDx {
             }
             store_rows(stage, w, reinterpret_cast<char*>(sums + row0 * a.D + d0), 4ll * a.D, live);
         }
-    }
-};
-
-// dW: A = dl^T (MN-major: vocabulary contiguous), B = x (MN-major: d contiguous); K = T. TMA returns
-// zeros for rows past T, so the contraction needs no padding.
-struct LmDw {
-    using Args = LmArgs;
-    using Tile = LmTile;
-    static constexpr bool kAMnMajor = true, kBMnMajor = true;
-    static constexpr uint32_t kIdesc = idesc_bf16_f32(kBM, kBRows, true, true);
-
-    __device__ static int32_t num_tiles(const Args& a) { return a.mtiles * a.ntiles; }
-    __device__ static Tile decode(int32_t tile, const Args& a) { return LmLogits::decode(tile, a); }
-    __device__ static void load(const Tile& t, int32_t kb, uint8_t* sa, uint8_t* sb, uint64_t* bar,
-                                const CUtensorMap* ta, const CUtensorMap* tb, const Args&) {
-#pragma unroll
-        for (int j = 0; j < kBM / 64; ++j) tma_load_2d(sa + j * kMnBoxBytes, ta, bar, t.m * kBM + 64 * j, kb * kBK);
-#pragma unroll
-        for (int j = 0; j < kBRows / 64; ++j)
-            tma_load_2d(sb + j * kMnBoxBytes, tb, bar, t.n * kBN2 + 64 * j, kb * kBK);
-    }
-    __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4* stage, const Args& a) {
-        const int64_t v = static_cast<int64_t>(a.v0) + t.m * kBM + row_in_tile - (threadIdx.x & 31);
-        const int32_t d0 = t.n * kBN2;
-        store_tile_bf16(taddr, stage, a.out0 + v * a.D + d0, a.D, min(kBN2, a.D - d0), live_rows(v, a.V));
     }
 };
 
@@ -584,28 +594,40 @@ constexpr size_t kRegionAlign = 256;
 constexpr int kPlanSms = 152;                 // SMs of the GB300, for sizes that must not depend on the device
 constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of one dl piece
 constexpr int32_t kMinPiece = 2048;           // but at least this many columns
+constexpr int kFirstTicket = 32;              // word of the workspace with the first piece's tile counter
 
 struct LmPlan {
     int32_t mtiles, ntiles;  // of the logits, in 128 x 256 tiles
     int32_t fwd_bn, fwd_ntiles;  // the forward's tiles
-    int32_t piece;           // columns per piece of the backward (a multiple of 256)
+    int32_t piece, pieces;   // columns per piece of the backward (a multiple of 256), and pieces
+    size_t clear_bytes;
     int32_t dx_ntiles;
     int32_t slices, kb_slice;
     bool direct;
     size_t off_sid, off_sp, off_zt, off_ent, off_coef, off_part, off_dl, off_sums, total;
 };
 
-// Slices of dx's contraction: a grid of few tiles leaves SMs idle, and each slice costs a round of
-// fp32 sums. The time of s slices is taken as the K steps of the busiest SM (0.35 us each) plus
-// the sums' traffic at 6 TB/s.
-int32_t pick_slices(int64_t tiles, int32_t kblocks, double sum_bytes) {
+// Whether a piece's two gradients run in one grid. Together they save the rounds in which SMs wait for the
+// last tiles, which counts with few rows; apart they keep to one set of operands at a time, which counts
+// once the weights and their gradient pass the 129 MB L2 by far. Together and apart: 64 x 2048 x 32000
+// (131 MB of weights) 90 and 98 us, 512 x 2048 x 32000 195 and 212 us, 300 x 1024 x 50257 106 and 114 us;
+// 1024 x 2048 x 32000 312 and 305 us, 2039 x 2048 x 32000 501 and 497 us; 4096 x 4096 x 50257 (412 MB)
+// 3.25 and 3.08 ms, 16 x 4096 x 131072 (1074 MB) 543 and 496 us.
+bool gradients_together(int64_t T, int32_t cols, int32_t D) { return T <= 512 && 2ll * cols * D <= (192ll << 20); }
+
+// Slices of dx's contraction: a grid of few tiles leaves SMs idle, and each slice costs a round of fp32
+// sums. Times in K steps of one SM (0.35 us): the rounds of dx's tiles or, in a grid with dW's (dw_steps,
+// where a tile's epilogue is worth some 3 steps), all tiles over all SMs, whichever is longer, and the
+// sums' traffic at 6 TB/s.
+int32_t pick_slices(int64_t tiles, int32_t kblocks, double dw_steps, double sum_bytes) {
     int32_t best = 1;
     double best_t = 1e30;
+    const double all = (static_cast<double>(tiles) * kblocks + dw_steps) / kPlanSms;
     for (int32_t s = 1; s <= 64 && s <= kblocks; ++s) {
         const int32_t kb = (kblocks + s - 1) / s;
         if ((kblocks + kb - 1) / kb != s) continue;
-        const double t =
-            0.35 * static_cast<double>(ceil_div(tiles * s, kPlanSms)) * kb + (s > 1 ? s * sum_bytes / 6e6 : 0.0);
+        const double t = std::max(static_cast<double>(ceil_div(tiles * s, kPlanSms)) * kb, all) +
+                         (s > 1 ? s * sum_bytes / (0.35 * 6e6) : 0.0);
         if (t < best_t) best_t = t, best = s;
     }
     return best;
@@ -637,10 +659,16 @@ void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
     p->piece = static_cast<int32_t>(piece);
     p->dx_ntiles = static_cast<int32_t>(ceil_div(D, kBN2));
     const int32_t kblocks = p->piece / kBK;
-    p->slices = pick_slices(static_cast<int64_t>(p->mtiles) * p->dx_ntiles, kblocks, 8.0 * T * D);
+    const double dw_tiles = static_cast<double>(p->piece / kBM) * p->dx_ntiles;
+    const double dw_steps =
+        gradients_together(T, p->piece, D) ? dw_tiles * (static_cast<double>(ceil_div(T, kBK)) + 3.0) : 0.0;
+    p->slices = pick_slices(static_cast<int64_t>(p->mtiles) * p->dx_ntiles, kblocks, dw_steps, 8.0 * T * D);
     p->kb_slice = (kblocks + p->slices - 1) / p->slices;
     p->direct = p->slices == 1 && p->piece >= V;
-    size_t off = kRegionAlign;  // the status word
+    // the status word, then one tile counter per piece, all cleared by each call
+    p->pieces = static_cast<int32_t>(pieces);
+    p->clear_bytes = sizeof(uint32_t) * (kFirstTicket + p->pieces);
+    size_t off = (p->clear_bytes + kRegionAlign - 1) / kRegionAlign * kRegionAlign;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += (bytes + kRegionAlign - 1) / kRegionAlign * kRegionAlign;
@@ -668,7 +696,7 @@ bool sizes_ok(int64_t T, int32_t D, int32_t V, int32_t K) {
     if (T >= (int64_t{1} << 31) || V > (1 << 30)) return false;
     // tile indices are 32-bit
     const int64_t mt = ceil_div(T, kBM), nt = ceil_div(V, kBN2), dt = ceil_div(D, kBN2);
-    return mt * nt < (int64_t{1} << 31) && mt * dt * 64 < (int64_t{1} << 31) && 2 * nt * dt < (int64_t{1} << 31);
+    return mt * nt < (int64_t{1} << 31) && 64 * mt * dt + 2 * nt * dt < (int64_t{1} << 31);
 }
 
 template <typename P>
@@ -688,7 +716,8 @@ uint32_t box_rows(int64_t T) { return static_cast<uint32_t>(T >= kBM ? kBM : cei
 
 moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward, cudaStream_t stream) {
     uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
-    if (cudaMemsetAsync(status, 0, sizeof(uint32_t), stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaMemsetAsync(status, 0, backward ? pl.clear_bytes : sizeof(uint32_t), stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
     float* coef = backward ? at<float>(p, pl.off_coef) : nullptr;
     cudaError_t e;
     if (p.teacher_ids == nullptr && !backward) return MOE_OK;  // the forward takes the labels as they are
@@ -768,10 +797,12 @@ moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
     make_plan(p.T, p.D, p.V, p.K, &pl);
     __nv_bfloat16* dl = at<__nv_bfloat16>(p, pl.off_dl);
     float* sums = at<float>(p, pl.off_sums);
-    CUtensorMap tx, tw, tdl, tw_mn, tdl_mn, tx_mn;
+    CUtensorMap tx, tw;
+    GemmMaps grads{};
     if (!make_tmap(&tx, p.x, p.D, p.T, kBK, box_rows(p.T)) || !make_tmap(&tw, p.w, p.D, p.V, kBK, kBN2) ||
-        !make_tmap(&tdl, dl, pl.piece, p.T, kBK, box_rows(p.T)) || !make_tmap(&tw_mn, p.w, p.D, p.V, 64, kBK) ||
-        !make_tmap(&tdl_mn, dl, pl.piece, p.T, 64, kBK) || !make_tmap(&tx_mn, p.x, p.D, p.T, 64, kBK))
+        !make_tmap(&grads.m[0], dl, pl.piece, p.T, kBK, box_rows(p.T)) ||
+        !make_tmap(&grads.m[1], p.w, p.D, p.V, 64, kBK) || !make_tmap(&grads.m[2], dl, pl.piece, p.T, 64, kBK) ||
+        !make_tmap(&grads.m[3], p.x, p.D, p.T, 64, kBK))
         return MOE_ERR_CUDA;
     moe_status_t st = prepare_targets(p, pl, true, stream);
     if (st != MOE_OK) return st;
@@ -794,34 +825,43 @@ moe_status_t launch_lm_bwd(const LmProblem& p, cudaStream_t stream) {
         st = launch_gemm<LmDlogits>(tx, tw, a, sm_count_grid(static_cast<int64_t>(a.mtiles) * a.ntiles, p.sm_count),
                                     stream);
         if (st != MOE_OK) return st;
-        if (p.dx) {
-            LmArgs b = a;
-            b.ntiles = pl.dx_ntiles;
-            b.kblocks = cols / kBK;
-            b.kb_slice = pl.kb_slice;
-            b.group = row_group(2ll * pl.kb_slice * kBK, pl.mtiles);
-            b.direct = pl.direct;
-            b.accumulate = v0 > 0;
-            b.out0 = static_cast<__nv_bfloat16*>(p.dx);
-            b.fout = sums;
-            // the first piece is a whole one and starts every slice's sums; a shorter last piece adds to fewer
-            const int32_t slices = static_cast<int32_t>(ceil_div(b.kblocks, b.kb_slice));
-            slices_used = std::max(slices_used, slices);
-            st = launch_gemm<LmDx>(tdl, tw_mn, b,
-                                   sm_count_grid(static_cast<int64_t>(b.mtiles) * b.ntiles * slices, p.sm_count),
-                                   stream);
+        LmArgs b = a;
+        b.ntiles = pl.dx_ntiles;
+        b.kblocks = cols / kBK;
+        b.kb_slice = pl.kb_slice;
+        b.group = row_group(2ll * pl.kb_slice * kBK, pl.mtiles);
+        b.direct = pl.direct;
+        b.accumulate = v0 > 0;
+        b.out0 = static_cast<__nv_bfloat16*>(p.dx);
+        b.fout = sums;
+        // the first piece is a whole one and starts every slice's sums; a shorter last piece adds to fewer
+        const int32_t slices = static_cast<int32_t>(ceil_div(b.kblocks, b.kb_slice));
+        slices_used = std::max(slices_used, slices);
+        b.dx_tiles = p.dx ? b.mtiles * b.ntiles * slices : 0;
+        // dW: row blocks whose tiles fill a round of the SMs, so that whole rows are written at a time
+        b.dw_mtiles = cols / kBM;
+        b.dw_kblocks = static_cast<int32_t>(ceil_div(p.T, kBK));
+        b.dw_group = std::max(1, std::min(kPlanSms / b.ntiles, b.dw_mtiles));
+        b.dw_tiles = p.dw ? b.dw_mtiles * b.ntiles : 0;
+        b.out1 = static_cast<__nv_bfloat16*>(p.dw);
+        const int32_t dx_tiles = b.dx_tiles, dw_tiles = b.dw_tiles;
+        if (dx_tiles > 0 && dw_tiles > 0 && gradients_together(p.T, cols, p.D)) {
+            b.ticket = b.status + kFirstTicket + v0 / pl.piece;
+            st = launch_gemm<LmGrads<true>>(grads, b, sm_count_grid(static_cast<int64_t>(dx_tiles) + dw_tiles, p.sm_count),
+                                            stream);
             if (st != MOE_OK) return st;
+            continue;
         }
-        if (p.dw) {
-            LmArgs c = a;
-            c.mtiles = cols / kBM;
-            c.ntiles = pl.dx_ntiles;
-            c.kblocks = static_cast<int32_t>(ceil_div(p.T, kBK));
-            c.group = std::max(1, std::min(kPlanSms / c.ntiles, c.mtiles));
-            c.out0 = static_cast<__nv_bfloat16*>(p.dw);
-            st = launch_gemm<LmDw>(tdl_mn, tx_mn, c,
-                                   sm_count_grid(static_cast<int64_t>(c.mtiles) * c.ntiles, p.sm_count), stream);
-            if (st != MOE_OK) return st;
+        if (dx_tiles > 0) {
+            b.dw_tiles = 0;
+            if ((st = launch_gemm<LmGrads<false>>(grads, b, sm_count_grid(dx_tiles, p.sm_count), stream)) != MOE_OK)
+                return st;
+        }
+        if (dw_tiles > 0) {
+            b.dx_tiles = 0;
+            b.dw_tiles = dw_tiles;
+            if ((st = launch_gemm<LmGrads<false>>(grads, b, sm_count_grid(dw_tiles, p.sm_count), stream)) != MOE_OK)
+                return st;
         }
     }
     if (p.dx && !pl.direct) {

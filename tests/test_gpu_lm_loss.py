@@ -253,6 +253,11 @@ def test_several_pieces_of_the_vocabulary(kind):
     R.check(dw, wdw, bdw, "dw")
 
 
+@pytest.mark.parametrize("T,D,V", [(520, 128, 5000), (513, 64, 129), (512, 1024, 4000), (8, 64, 9000), (120, 2048, 700)])
+def test_gradients_in_one_grid_and_in_two(T, D, V):
+    ce(T, D, V, seed=T + D + V).check()
+
+
 def test_repeats_and_another_stream_give_the_same_bits():
     c = distill(300, 256, 2000, 16, seed=27, tau=2.0)
     loss, lse = c.fwd()
