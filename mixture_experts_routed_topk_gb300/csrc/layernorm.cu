@@ -20,6 +20,12 @@
 // rows in block order: the result does not depend on the order in which blocks finish.
 //
 // Longer rows are read two or three times, mostly from L2.
+//
+// Measured (device time; the copy rate is 6.79 TB/s): bf16 16384 x 7168 forward 87 us (5.4 TB/s), backward
+// 121 us (5.8 TB/s), both bound by instruction issue and the waits in the row sums as much as by memory
+// (a block per row without the ring and with the parameters read anew: 157 and 265 us); 4096 x 2048 11 and
+// 17 us and fp16 8191 x 1001 14 and 25 us, where a group has seven rows or fewer and the latency of a launch,
+// of the first loads and of four rounds decides.
 #include <algorithm>
 #include <atomic>
 
