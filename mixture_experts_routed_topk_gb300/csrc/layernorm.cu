@@ -562,10 +562,16 @@ __global__ void __launch_bounds__(32 * kGradWarps)
     if (out == nullptr) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + lane;
+    // all of a warp's rows at once: one latency instead of one per row
+    float v[(kLnMaxBlocks + kGradWarps - 1) / kGradWarps];
     float s = 0.0f;
-    if (j < D)
-        for (int b = warp; b < blocks; b += kGradWarps)
-            s += partial[(static_cast<int64_t>(b) * 2 + blockIdx.y) * D + j];
+#pragma unroll
+    for (int u = 0; u < static_cast<int>(sizeof(v) / sizeof(v[0])); ++u) {
+        const int b = warp + u * kGradWarps;
+        v[u] = j < D && b < blocks ? partial[(static_cast<int64_t>(b) * 2 + blockIdx.y) * D + j] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < static_cast<int>(sizeof(v) / sizeof(v[0])); ++u) s += v[u];
     acc[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && j < D) {
