@@ -218,8 +218,8 @@ struct Row {
 };
 
 // This thread's parameters, in the order of its elements.
-template <class R, typename P = Param>
-__device__ __forceinline__ void load_params(const P& a, int32_t D, int lane, float none, float (&out)[kLnN]) {
+template <class R>
+__device__ __forceinline__ void load_params(const Param& a, int32_t D, int lane, float none, float (&out)[kLnN]) {
 #pragma unroll
     for (int i = 0; i < R::kVecs; ++i) {
         float t[R::kVec];

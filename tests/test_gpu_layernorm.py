@@ -190,6 +190,25 @@ def test_gradient_is_the_difference_of_the_forward():
     assert abs(float(diff - (dx.double() * v.double()).sum())) < T * D * (h * h + 2.0 ** -22 / h)
 
 
+def test_offsets_past_32_bits():
+    T, D = 300_001, 7168  # over 2^31 elements
+    x = torch.zeros(T, D, dtype=BF16, device="cuda")
+    rows = [0, 149_797, 299_593, T - 1]  # both sides of 2^30 and of 2^31 elements
+    x[rows] = rand(len(rows), D, seed=18, dtype=BF16).cuda()
+    y, mean, rstd = fwd(x, None, None)
+    want, wmean, wrstd = fwd(x[rows].contiguous(), None, None)
+    assert torch.equal(y[rows], want) and torch.equal(mean[rows], wmean) and torch.equal(rstd[rows], wrstd)
+    assert not y[rows[1] + 1].any()
+    del y
+    dx, dg, db = bwd(x, x, None, mean, rstd, F32)
+    wdx, wdg, wdb = bwd(x[rows].contiguous(), x[rows].contiguous(), None, wmean, wrstd, F32)
+    assert torch.equal(dx[rows], wdx)
+    # the other rows add nothing: the same terms, added in another order
+    terms = (x[rows].double().abs() * ((x[rows].double() - wmean[:, None]) * wrstd[:, None]).abs()).sum(0)
+    assert ((dg - wdg).abs() <= 16 * R.U32 * terms).all()
+    assert ((db - wdb).abs() <= 16 * R.U32 * x[rows].double().abs().sum(0)).all()
+
+
 def test_graph_replay():
     dy, x = rand(50, 640, seed=16, dtype=BF16).cuda(), rand(50, 640, seed=17, dtype=BF16).cuda()
     y, mean, rstd = fwd(x, None, None)

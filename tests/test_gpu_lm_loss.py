@@ -258,6 +258,38 @@ def test_gradients_in_one_grid_and_in_two(T, D, V):
     ce(T, D, V, seed=T + D + V).check()
 
 
+def test_weights_past_32_bits():
+    T, D, V = 3, 4096, 600_003  # over 2^31 elements of w and of dw
+    w = torch.randn(V, D, device="cuda", dtype=BF16).mul_(2.0 / D ** 0.5)
+    x = torch.randn(T, D, generator=gen(34)).to(BF16).cuda()
+    dloss = torch.randn(T, generator=gen(35)).cuda()
+    targets = torch.tensor([V - 1, 524_288, 7], dtype=I32, device="cuda")  # V - 1: its row is past 2^31
+    ws = B.alloc_workspace(B.moe_lm_workspace_bytes(T, D, V))
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    B.moe_lm_ce_fwd(x, w, targets, loss, lse, ws)
+    dx, dw = torch.empty_like(x), torch.full_like(w, 3.0)
+    B.moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, ws)
+    assert B.moe_get_status(ws) == 0
+    z = torch.cat([x.double() @ w[a:a + 50_000].double().T for a in range(0, V, 50_000)], 1)
+    # |x| |w| bounds the sum of a logit's absolute products; no row of w is longer than 3 (2 on average)
+    dz = (D // 16 + 16) * R.ACC * x.double().norm(dim=1) * 3.0
+    want = torch.logsumexp(z, 1)
+    blse = dz + 8 * R.U32 * (z.abs().amax(1) + want.abs() + 2) + (300 + V // 4096) * R.U32
+    R.check(lse, want, blse, "lse")
+    zt = z.gather(1, targets.long()[:, None])[:, 0]
+    R.check(loss, want - zt, 2 * blse + 8 * R.U32 * want.abs(), "loss")
+    dl = dloss.double()[:, None] * torch.exp(z - lse.double()[:, None])
+    dl[range(T), targets.long()] -= dloss.double()
+    for rows in (slice(0, 300), slice(524_200, 524_400), slice(V - 300, V)):
+        part = dl[:, rows]
+        e = dz[:, None] + 8 * R.U32 * (z[:, rows].abs() + lse.double().abs()[:, None] + 2)
+        bdl = (part.abs() + dloss.double().abs()[:, None] * 8 * R.U32) * e * 1.01 + R.round_bound(part, BF16)
+        ref = part.T @ x.double()
+        bound = (bdl.T @ x.double().abs()) * 1.01 + 80 * R.ACC * (part.abs().T @ x.double().abs()) + R.round_bound(ref, BF16)
+        R.check(dw[rows], ref, bound, f"dw {rows}")
+    assert torch.isfinite(dx.float()).all()
+
+
 def test_repeats_and_another_stream_give_the_same_bits():
     c = distill(300, 256, 2000, 16, seed=27, tau=2.0)
     loss, lse = c.fwd()
