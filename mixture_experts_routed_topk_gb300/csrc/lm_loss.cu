@@ -60,25 +60,9 @@ __device__ __forceinline__ float exp2_full(float x) {
 
 // ------------------------------------------------------------------------------------ targets
 
-// Cross entropy's backward: sid[t] = the label, or kNoTarget; coef[t] = dloss[t], or 0.
-__global__ void __launch_bounds__(256) k_lm_labels(const int32_t* __restrict__ targets, int32_t ignore_index,
-                                                   int64_t T, int32_t V, const float* __restrict__ dloss,
-                                                   int32_t* __restrict__ sid, float* __restrict__ coef,
-                                                   uint32_t* __restrict__ status) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (t >= T) return;
-    const int32_t id = targets[t];
-    const bool ignored = id == ignore_index, inside = id >= 0 && id < V;
-    if (!ignored && !inside) atomicOr(status, MOE_DEV_BAD_TARGET);
-    const bool ok = !ignored && inside;
-    sid[t] = ok ? id : kNoTarget;
-    coef[t] = ok ? dloss[t] : 0.0f;
-}
-
 // Distillation: one warp per row. sid / sp: the kept ids in ascending order (equal ids in the order
-// given) with their probabilities, then kNoTarget / 0. ent[t] = sum_j p_j log p_j. coef as above.
+// given) with their probabilities, then kNoTarget / 0. ent[t] = sum_j p_j log p_j. coef[t] = tau dloss[t], or 0
+// for a row without a distribution (backward only).
 // An entry with a negative id is not kept (its logit is not looked at).
 __global__ void __launch_bounds__(128)
     k_lm_teacher(const int32_t* __restrict__ ids, const float* __restrict__ logits, int64_t T, int32_t K, int32_t V,
@@ -168,7 +152,9 @@ struct LmArgs : GemmArgs {
     float zscale;        // accumulator to scaled logit (logit_scale)
     float scale2;        // the same in units of log 2, for base-2 exponentials
     const float* lse;    // [T]
-    const float* coef;   // [T]
+    const float* coef;   // [T] distillation: the factor of the row's dl
+    const float* dloss;  // [T] cross entropy: the same, where the label counts
+    int32_t ignore_index;
     int32_t pitch;       // row length of the dl piece
     int32_t kb_slice;    // K steps per slice of the contraction (dx)
     bool accumulate;     // dx: add to the slice's sums instead of starting them
@@ -346,10 +332,20 @@ struct LmDlogits : LmLogits {
         int32_t next = kNoTarget;
         const int32_t* sid = a.sid + row * a.K;
         if (live) {
-            coef = __ldg(a.coef + row);
             lse2 = __ldg(a.lse + row) * kLog2e;
-            j = first_target(sid, a.K, n0);
-            if (j < a.K) next = __ldg(sid + j);
+            if (a.sp == nullptr) {  // the labels as the caller gave them
+                const int32_t id = __ldg(sid);
+                const bool inside = id >= 0 && id < a.V, ignored = id == a.ignore_index;
+                if (!inside && !ignored && n0 == 0) atomicOr(a.status, MOE_DEV_BAD_TARGET);
+                if (inside && !ignored) {
+                    coef = __ldg(a.dloss + row);
+                    if (id >= n0) next = id;
+                }
+            } else {
+                coef = __ldg(a.coef + row);
+                j = first_target(sid, a.K, n0);
+                if (j < a.K) next = __ldg(sid + j);
+            }
         }
         const bool zero = coef == 0.0f;
 #pragma unroll 1
@@ -723,16 +719,12 @@ moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward
     uint32_t* status = reinterpret_cast<uint32_t*>(p.ws);
     if (cudaMemsetAsync(status, 0, backward ? pl.clear_bytes : sizeof(uint32_t), stream) != cudaSuccess)
         return MOE_ERR_CUDA;
+    if (p.teacher_ids == nullptr) return MOE_OK;  // the grids take the labels as they are
     float* coef = backward ? at<float>(p, pl.off_coef) : nullptr;
-    cudaError_t e;
-    if (p.teacher_ids == nullptr && !backward) return MOE_OK;  // the forward takes the labels as they are
-    if (p.teacher_ids == nullptr)
-        e = launch_pdl(k_lm_labels, dim3(static_cast<unsigned>(ceil_div(p.T, 256))), dim3(256), 0, stream, p.targets,
-                       p.ignore_index, p.T, p.V, p.dloss, at<int32_t>(p, pl.off_sid), coef, status);
-    else
-        e = launch_pdl(k_lm_teacher, dim3(static_cast<unsigned>(ceil_div(p.T, 4))), dim3(128), 0, stream,
-                       p.teacher_ids, p.teacher_logits, p.T, p.K, p.V, 1.0f / p.temperature, p.temperature, p.dloss,
-                       at<int32_t>(p, pl.off_sid), at<float>(p, pl.off_sp), at<float>(p, pl.off_ent), coef, status);
+    const cudaError_t e =
+        launch_pdl(k_lm_teacher, dim3(static_cast<unsigned>(ceil_div(p.T, 4))), dim3(128), 0, stream, p.teacher_ids,
+                   p.teacher_logits, p.T, p.K, p.V, 1.0f / p.temperature, p.temperature, p.dloss,
+                   at<int32_t>(p, pl.off_sid), at<float>(p, pl.off_sp), at<float>(p, pl.off_ent), coef, status);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -751,7 +743,11 @@ LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     a.V = p.V;
     a.K = p.K;
     a.bm = static_cast<int32_t>(box_rows(p.T));
-    a.sid = at<int32_t>(p, pl.off_sid);
+    // cross entropy: labels as the caller gave them (one outside the vocabulary finds no tile of the
+    // forward; the join and the backward tell ignored labels from wrong ones)
+    a.sid = p.teacher_ids ? at<int32_t>(p, pl.off_sid) : p.targets;
+    a.ignore_index = p.ignore_index;
+    a.dloss = p.dloss;
     a.sp = p.teacher_ids ? at<float>(p, pl.off_sp) : nullptr;
     const double scale = logit_scale(p.D, p.temperature);
     a.zscale = static_cast<float>(scale);
@@ -777,8 +773,6 @@ moe_status_t launch_lm_fwd(const LmProblem& p, cudaStream_t stream) {
     moe_status_t st = prepare_targets(p, pl, false, stream);
     if (st != MOE_OK) return st;
     LmArgs a = common_args(p, pl);
-    // a label outside the vocabulary finds no tile; the join tells ignored labels from wrong ones
-    if (p.targets) a.sid = p.targets;
     a.mtiles = pl.mtiles;
     a.ntiles = pl.fwd_ntiles;
     a.bn = pl.fwd_bn;
