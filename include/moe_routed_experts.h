@@ -614,7 +614,8 @@ moe_status_t moe_router_topk_bwd(const void *logits, int32_t dtype, const int32_
  * Bytes of workspace the moe_lm_* calls need: K is the number of teacher entries per row (1 for cross
  * entropy). The same size serves the forward and the backward call. It does not hold the T V logits: the
  * backward pass goes over pieces of the vocabulary of at most 512 MB (or 2048 columns). 0 for sizes
- * outside the limits: T >= 1, D a multiple of 64, 1 <= V <= 2^30, 1 <= K <= 256. Pure arithmetic.
+ * outside the limits: T >= 1, D a multiple of 64, 1 <= V <= 2^30, 1 <= K <= 256, and fewer than 2^28 tiles
+ * of 128 rows x 256 columns of the logits. Pure arithmetic.
  */
 size_t moe_lm_workspace_bytes(int64_t T, int32_t D, int32_t V, int32_t K);
 

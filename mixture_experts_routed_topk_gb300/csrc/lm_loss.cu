@@ -695,9 +695,9 @@ void make_plan(int64_t T, int32_t D, int32_t V, int32_t K, LmPlan* p) {
 bool sizes_ok(int64_t T, int32_t D, int32_t V, int32_t K) {
     if (T <= 0 || D <= 0 || V <= 0 || K <= 0 || K > kLmMaxK || D % 64 != 0) return false;
     if (T >= (int64_t{1} << 31) || V > (1 << 30)) return false;
-    // tile indices are 32-bit
+    // tile indices are 32-bit (the forward's tiles have 32 columns at least, an eighth of the full ones)
     const int64_t mt = ceil_div(T, kBM), nt = ceil_div(V, kBN2), dt = ceil_div(D, kBN2);
-    return mt * nt < (int64_t{1} << 31) && 64 * mt * dt + 2 * nt * dt < (int64_t{1} << 31);
+    return 8 * mt * nt < (int64_t{1} << 31) && 64 * mt * dt + 2 * nt * dt < (int64_t{1} << 31);
 }
 
 template <typename P>

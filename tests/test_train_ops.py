@@ -203,6 +203,7 @@ def test_vocabulary_workspace_does_not_grow_with_the_logits(lib):
     size = binding.moe_lm_workspace_bytes
     assert size(0, 64, 10) == 0 and size(4, 65, 10) == 0 and size(4, 64, 0) == 0 and size(4, 64, 10, 257) == 0
     assert size(1, 64, 1) > 0
+    assert size(1 << 25, 64, 1 << 18) == 0  # 2^28 tiles of logits
     T, D, V = 32768, 4096, 131072
     logits = 2 * T * V
     assert size(T, D, V) < logits // 4
