@@ -39,7 +39,6 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kNoTarget = INT_MAX;
 constexpr int kLmMaxK = 256;
 
@@ -147,10 +146,9 @@ struct LmArgs : GemmArgs {
     int32_t K;           // targets per row
     const int32_t* sid;  // [T, K] sorted target ids
     const float* sp;     // [T, K] their probabilities; null: 1
-    float* zt;           // [T, K] out: the targets' logits
-    float2* part;        // [ntiles][T] out: (maximum, sum) of the tile's exponentials, base 2
-    float zscale;        // accumulator to scaled logit (logit_scale)
-    float scale2;        // the same in units of log 2, for base-2 exponentials
+    float* zt;           // [T, K] out: the targets' accumulators
+    float2* part;        // [ntiles][T] out: the tile's largest accumulator, and the sum of its exponentials against it
+    float scale2;        // accumulator to scaled logit (logit_scale) in units of log 2, for base-2 exponentials
     const float* lse;    // [T]
     const float* coef;   // [T] distillation: the factor of the row's dl
     const float* dloss;  // [T] cross entropy: the same, where the label counts
@@ -268,7 +266,11 @@ struct LmLogits {
     }
 };
 
-// Forward: a tile's share of the row's softmax sum, and the targets' logits.
+// Forward: a tile's share of the row's softmax sum, and the targets' logits. Both the maximum and the targets
+// are kept as the accumulators they are, and exponentials are taken of differences to the maximum: the largest
+// term is then exactly 1 and the sum 1 or more, and a target that is the maximum is exactly 0 below it, however
+// large the logit. With each scaled and rounded for itself, a row that is sure of its target would get a loss
+// off by roundings of the logit's size, and below 0 as often as not.
 struct LmLse : LmLogits {
     __device__ static void epilogue(const Tile& t, uint32_t taddr, int row_in_tile, uint4*, const Args& a) {
         const int64_t row = static_cast<int64_t>(t.m) * kBM + row_in_tile;
@@ -301,18 +303,19 @@ struct LmLse : LmLogits {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (next == c0 + i) z = w[i];
-                a.zt[row * a.K + j] = __uint_as_float(z) * a.zscale;
+                a.zt[row * a.K + j] = __uint_as_float(z);
                 ++j;
                 next = j < a.K ? __ldg(sid + j) : kNoTarget;
             }
             float cm = __uint_as_float(w[0]);
 #pragma unroll
             for (int i = 1; i < 32; ++i) cm = fmaxf(cm, __uint_as_float(w[i]));
-            const float top = fmaxf(m, cm * scale2);
+            const float top = fmaxf(m, cm);
             const float base = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: its terms are 0
-            s *= exp2_fast(m - base);
+            float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // small terms meet each other before they meet the 1
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s += exp2_fast(fmaf(__uint_as_float(w[i]), scale2, -base));
+            for (int i = 0; i < 32; ++i) q[i & 3] += exp2_fast((__uint_as_float(w[i]) - base) * scale2);
+            s = fmaf(s, exp2_fast((m - base) * scale2), (q[0] + q[1]) + (q[2] + q[3]));
             m = top;
         }
         if (live) a.part[static_cast<int64_t>(t.n) * a.T + row] = make_float2(m, s);
@@ -495,14 +498,16 @@ struct LmGrads {
 // Joins a row's tiles and forms its loss. A block owns 32 rows, one per lane; its warps take the
 // tiles in turn and meet in shared memory in warp order. Then (distillation) each warp sums the targets
 // of two rows. sp null: cross entropy, where sid holds the labels as the caller gave them.
+// With the row's largest accumulator m and s = sum exp(z - m): a target's -log q is (m - its accumulator),
+// scaled, plus log s. Both are 0 or more.
 constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     k_lm_join(const float2* __restrict__ part, int32_t ntiles, int64_t T, int32_t K, const int32_t* __restrict__ sid,
               const float* __restrict__ sp, const float* __restrict__ zt, const float* __restrict__ ent, float tau,
-              int32_t ignore_index, int32_t V, float* __restrict__ loss, float* __restrict__ lse_out,
-              uint32_t* __restrict__ status) {
+              float zscale, float scale2, int32_t ignore_index, int32_t V, float* __restrict__ loss,
+              float* __restrict__ lse_out, uint32_t* __restrict__ status) {
     __shared__ float2 acc[kJoinWarps][32];
-    __shared__ float s_lse[32];
+    __shared__ float2 s_row[32];  // the row's largest accumulator and log s
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     griddep_wait();
@@ -511,7 +516,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     if (row < T) {
         auto add = [&](const float2& p) {
             const float top = fmaxf(m, p.x);
-            s = (s == 0.0f ? 0.0f : s * exp2_fast(m - top)) + (p.y == 0.0f ? 0.0f : p.y * exp2_fast(p.x - top));
+            s = (s == 0.0f ? 0.0f : s * exp2_fast((m - top) * scale2)) +
+                (p.y == 0.0f ? 0.0f : p.y * exp2_fast((p.x - top) * scale2));
             m = top;
         };
         int n = warp;
@@ -533,15 +539,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w)
-            if (acc[w][lane].y != 0.0f) s += acc[w][lane].y * exp2_fast(acc[w][lane].x - top);
-        const float lse = kLn2 * top + logf(s);
-        lse_out[row] = lse;
-        s_lse[lane] = lse;
+            if (acc[w][lane].y != 0.0f) s += acc[w][lane].y * exp2_fast((acc[w][lane].x - top) * scale2);
+        const float log_s = logf(s);
+        lse_out[row] = fmaf(top, zscale, log_s);
+        s_row[lane] = make_float2(top, log_s);
         if (sp == nullptr) {
             const int32_t id = sid[row];
             const bool inside = id >= 0 && id < V, ignored = id == ignore_index;
             if (!inside && !ignored) atomicOr(status, MOE_DEV_BAD_TARGET);
-            loss[row] = inside && !ignored ? lse - zt[row] : 0.0f;
+            loss[row] = inside && !ignored ? fmaf(top - zt[row], zscale, log_s) : 0.0f;
         }
     }
     if (sp == nullptr) return;
@@ -549,14 +555,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     for (int r = warp; r < 32; r += kJoinWarps) {
         const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + r;
         if (t >= T) break;
-        const float lse = s_lse[r];
+        const float2 top_log = s_row[r];
         float l = 0.0f;
         bool any = false;
         for (int j = lane; j < K; j += 32) {
             if (sid[t * K + j] == kNoTarget) break;  // sorted: nothing after it
             any = true;
             const float p = sp[t * K + j];
-            if (p != 0.0f) l += p * (lse - zt[t * K + j]);
+            if (p != 0.0f) l += p * fmaf(top_log.x - zt[t * K + j], zscale, top_log.y);
         }
         __syncwarp();
         l = warp_sum(l);
@@ -749,9 +755,7 @@ LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     a.ignore_index = p.ignore_index;
     a.dloss = p.dloss;
     a.sp = p.teacher_ids ? at<float>(p, pl.off_sp) : nullptr;
-    const double scale = logit_scale(p.D, p.temperature);
-    a.zscale = static_cast<float>(scale);
-    a.scale2 = static_cast<float>(scale * 1.4426950408889634);
+    a.scale2 = static_cast<float>(logit_scale(p.D, p.temperature) * 1.4426950408889634);
     a.status = reinterpret_cast<uint32_t*>(p.ws);
     return a;
 }
@@ -786,7 +790,8 @@ moe_status_t launch_lm_fwd(const LmProblem& p, cudaStream_t stream) {
     return launch_pdl(k_lm_join, dim3(static_cast<unsigned>(ceil_div(p.T, 32))), dim3(32 * kJoinWarps), 0, stream,
                       static_cast<const float2*>(a.part), pl.fwd_ntiles, p.T, p.K, a.sid, a.sp,
                       static_cast<const float*>(a.zt), static_cast<const float*>(at<float>(p, pl.off_ent)),
-                      p.temperature, p.ignore_index, p.V, p.loss, p.lse, a.status) == cudaSuccess
+                      p.temperature, static_cast<float>(logit_scale(p.D, p.temperature)), a.scale2, p.ignore_index, p.V,
+                      p.loss, p.lse, a.status) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
