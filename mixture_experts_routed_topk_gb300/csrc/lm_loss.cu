@@ -62,7 +62,8 @@ __device__ __forceinline__ float exp2_full(float x) {
 // Distillation: one warp per row. sid / sp: the kept ids in ascending order (equal ids in the order
 // given) with their probabilities, then kNoTarget / 0. ent[t] = sum_j p_j log p_j. coef[t] = tau dloss[t], or 0
 // for a row without a distribution (backward only).
-// An entry with a negative id is not kept (its logit is not looked at).
+// An entry with a negative id is not kept (its logit is not looked at). The row's largest logit is taken off
+// before the temperature divides: logits near the ends of their type would overflow under one below 1.
 __global__ void __launch_bounds__(128)
     k_lm_teacher(const int32_t* __restrict__ ids, const float* __restrict__ logits, int64_t T, int32_t K, int32_t V,
                  float inv_tau, float tau, const float* __restrict__ dloss, int32_t* __restrict__ sid,
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(128)
             bad = bad || id >= V;
             row_id[j] = ok ? id : kNoTarget;
             if (ok) {
-                a[i] = __ldg(logits + t * K + j) * inv_tau;
+                a[i] = __ldg(logits + t * K + j);
                 nan = nan || a[i] != a[i];
                 m = fmaxf(m, a[i]);
                 ++kept;
@@ -106,7 +107,10 @@ __global__ void __launch_bounds__(128)
     const bool none = kept == 0 || (m == -INFINITY && !nan);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kLmMaxK / 32; ++i) s += none ? 0.0f : expf(a[i] - m);
+    for (int i = 0; i < kLmMaxK / 32; ++i) {
+        a[i] = (a[i] - m) * inv_tau;
+        s += none ? 0.0f : expf(a[i]);
+    }
     s = warp_sum(s);
     const float log_s = logf(s);
     float e = 0.0f;
@@ -116,8 +120,8 @@ __global__ void __launch_bounds__(128)
         if (j < K) {
             const int32_t id = none ? kNoTarget : row_id[j];
             const bool ok = id != kNoTarget;
-            const float p = ok ? expf(a[i] - m) / s : 0.0f;
-            if (ok && p != 0.0f) e += p * (a[i] - m - log_s);
+            const float p = ok ? expf(a[i]) / s : 0.0f;
+            if (ok && p != 0.0f) e += p * (a[i] - log_s);
             int rank = 0;
             for (int l = 0; l < K; ++l) {
                 const int32_t other = none ? kNoTarget : row_id[l];

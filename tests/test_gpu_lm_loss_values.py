@@ -7,6 +7,7 @@ import torch
 
 import train_ops_ref as R
 from mixture_experts_routed_topk_gb300 import binding as B
+from test_gpu_lm_loss import Case, head
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,18 @@ def test_distillation_of_rows_that_are_sure(D, tau):
     for loss in (one, far):
         R.check(loss, tau * tau * want, tau * tau * (bound + 4 * R.U32 * want), "loss")
         assert (loss >= 0).all()
+
+
+# ------------------------------------------------------------- teacher logits at the ends of their type
+
+@pytest.mark.parametrize("tau", [2.0 ** -10, 0.5, 0.9, 1.0, 4.0])
+def test_teacher_logits_at_the_ends_of_their_type(tau):
+    x, w, dloss = head(6, 64, 300, 50)
+    x = (x.float() * min(1.0, tau)).to(BF16)  # the student's logits stay ordinary at the temperature
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    logits = torch.tensor([[low, low, low], [low, 0.0, 1.0], [high, high, 0.0], [high, low, high], [0.9 * high, high, 1.0],
+                           [-torch.inf, low, low]])
+    if tau < 1.0:
+        logits[1] *= torch.tensor([1.0, tau, tau])
+    ids = torch.tensor([[5, 0, 299]] * 6, dtype=I32)
+    Case(x, w, dloss, ids=ids, logits=logits, tau=tau).check()
