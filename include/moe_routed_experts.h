@@ -658,7 +658,7 @@ moe_status_t moe_lm_ce_bwd(const void *x, const void *w, const int32_t *targets,
  *                   looked at), an id >= V sets MOE_DEV_BAD_TARGET and counts as not kept. Repeated ids count
  *                   each for itself
  *   teacher_logits  device fp32 [T,K]
- *   temperature     tau > 0, finite
+ *   temperature     tau, 2^-60 to 2^60
  * A row without kept entries, or with nothing but -inf in them, has loss 0. The rest as for
  * moe_lm_ce_fwd, with moe_lm_workspace_bytes(T, D, V, K) bytes of workspace.
  */

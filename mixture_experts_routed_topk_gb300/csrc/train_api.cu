@@ -23,7 +23,8 @@ constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 // The checks of the four vocabulary-loss calls (T = 0 asks for no pointers).
 moe_status_t check_lm(const LmProblem& p, size_t workspace_bytes, bool backward) {
     if (p.T < 0 || p.D <= 0 || p.V <= 0 || p.K <= 0) return MOE_ERR_INVALID_ARG;
-    if (!(p.temperature > 0.0f && p.temperature < 3.0e38f)) return MOE_ERR_INVALID_ARG;
+    // the loss has the square as a factor and the logits the reciprocal: past this they leave fp32
+    if (!(p.temperature >= 0x1p-60f && p.temperature <= 0x1p60f)) return MOE_ERR_INVALID_ARG;
     const size_t need = lm_workspace_bytes(p.T > 0 ? p.T : 1, p.D, p.V, p.K);
     if (need == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(p.dw, 16)) return MOE_ERR_MISALIGNED;
