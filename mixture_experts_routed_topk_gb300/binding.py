@@ -648,10 +648,18 @@ def _workspace(t, device: int) -> int:
     return _operand(t, "workspace", torch.uint8, (t.numel(),) if isinstance(t, torch.Tensor) else (0,), device)
 
 
-def _current_stream(stream) -> int:
+def _stream_of(stream, device: int) -> int:
+    """The handle of the call's stream. The library launches on the current device, so that has to be the tensors'."""
+    current = torch._C._cuda_getDevice()
+    if device != current:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        return torch._C._cuda_getCurrentRawStream(current)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != current:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{current}")
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _norm_params(x, D: int, device: int, *params):
@@ -677,7 +685,7 @@ def moe_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps: float = 1e-5, stream=N
     _check("moe_layernorm_fwd", load().moe_layernorm_fwd(
         px, pg, pb, MOE_DTYPE[x.dtype], pd, _operand(y, "y", x.dtype, (T, D), dev),
         _operand(mean, "mean", torch.float32, (T,), dev), _operand(rstd, "rstd", torch.float32, (T,), dev), T, D,
-        float(eps), _current_stream(stream)))
+        float(eps), _stream_of(stream, dev)))
 
 
 def moe_layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
@@ -693,7 +701,7 @@ def moe_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, st
         _operand(dy, "dy", x.dtype, (T, D), dev), px, pg, _operand(mean, "mean", torch.float32, (T,), dev),
         _operand(rstd, "rstd", torch.float32, (T,), dev), MOE_DTYPE[x.dtype], pd,
         _operand(dx, "dx", x.dtype, (T, D), dev), pdg, pdb, T, D, 0 if workspace is None else _workspace(workspace, dev),
-        0 if workspace is None else workspace.numel(), _current_stream(stream)))
+        0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
 
 
 _LOGIT_DTYPES = (torch.float32, torch.bfloat16)
@@ -712,7 +720,7 @@ def moe_router_topk_fwd(logits, topk_ids, topk_scores, normalize: bool = True, s
     K, pi = _choices(topk_ids, T, dev)
     _check("moe_router_topk_fwd", load().moe_router_topk_fwd(
         pz, MOE_DTYPE[logits.dtype], pi, _operand(topk_scores, "topk_scores", torch.float32, (T, K), dev), T, E, K,
-        1 if normalize else 0, _current_stream(stream)))
+        1 if normalize else 0, _stream_of(stream, dev)))
 
 
 def moe_router_topk_bwd(logits, topk_ids, dscores, dlogits, normalize: bool = True, stream=None) -> None:
@@ -723,7 +731,7 @@ def moe_router_topk_bwd(logits, topk_ids, dscores, dlogits, normalize: bool = Tr
     _check("moe_router_topk_bwd", load().moe_router_topk_bwd(
         pz, MOE_DTYPE[logits.dtype], pi, _operand(dscores, "dscores", torch.float32, (T, K), dev),
         _operand(dlogits, "dlogits", logits.dtype, (T, E), dev), T, E, K, 1 if normalize else 0,
-        _current_stream(stream)))
+        _stream_of(stream, dev)))
 
 
 def moe_lm_workspace_bytes(T: int, D: int, V: int, K: int = 1) -> int:
@@ -763,7 +771,7 @@ def moe_lm_ce_fwd(x, w, targets, loss, lse, workspace, ignore_index: int = -100,
     T, D, V, dev, px, pw = _head(x, w)
     _check("moe_lm_ce_fwd", load().moe_lm_ce_fwd(
         px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(loss, "loss", T, dev),
-        _vector(lse, "lse", T, dev), T, D, V, _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
+        _vector(lse, "lse", T, dev), T, D, V, _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
 
 
 def moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, workspace, ignore_index: int = -100, stream=None) -> None:
@@ -773,7 +781,7 @@ def moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, workspace, ignore_index: in
     _check("moe_lm_ce_bwd", load().moe_lm_ce_bwd(
         px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(lse, "lse", T, dev),
         _vector(dloss, "dloss", T, dev), _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V,
-        _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
+        _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
 
 
 def moe_lm_distill_fwd(x, w, teacher_ids, teacher_logits, loss, lse, workspace, temperature: float = 1.0,
@@ -785,7 +793,7 @@ def moe_lm_distill_fwd(x, w, teacher_ids, teacher_logits, loss, lse, workspace, 
     K, pi, pl = _teacher(teacher_ids, teacher_logits, T, dev)
     _check("moe_lm_distill_fwd", load().moe_lm_distill_fwd(
         px, pw, pi, pl, float(temperature), _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev), T, D, V, K,
-        _workspace(workspace, dev), workspace.numel(), _current_stream(stream)))
+        _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
 
 
 def moe_lm_distill_bwd(x, w, teacher_ids, teacher_logits, lse, dloss, dx, dw, workspace, temperature: float = 1.0,
@@ -797,4 +805,4 @@ def moe_lm_distill_bwd(x, w, teacher_ids, teacher_logits, lse, dloss, dx, dw, wo
     _check("moe_lm_distill_bwd", load().moe_lm_distill_bwd(
         px, pw, pi, pl, float(temperature), _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev),
         _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V, K, _workspace(workspace, dev),
-        workspace.numel(), _current_stream(stream)))
+        workspace.numel(), _stream_of(stream, dev)))
