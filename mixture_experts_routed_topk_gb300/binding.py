@@ -636,11 +636,21 @@ def _operand(t, name: str, dtype, shape, device: int) -> int:
     _refuse(t, name, dtype, shape, device)
 
 
+_INT32_MAX = (1 << 31) - 1
+
+
+def _int32(n: int, name: str) -> int:
+    """A size that the library takes as a 32-bit number (ctypes would wrap a larger one around)."""
+    if n > _INT32_MAX:
+        raise ValueError(f"{name}: a size of {n} does not fit 32 bits")
+    return n
+
+
 def _rows(x, name: str, dtypes):
     """T, D, device and pointer of a contiguous [T, D] tensor of one of the dtypes."""
     if isinstance(x, torch.Tensor) and x.dtype in dtypes and x.dim() == 2 and x.is_cuda and x.is_contiguous():
         T, D = x.shape
-        return T, D, x.get_device(), x.data_ptr()
+        return T, _int32(D, name), x.get_device(), x.data_ptr()
     _need(x, name, tuple(dtypes), 2)
 
 
@@ -689,7 +699,7 @@ def moe_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps: float = 1e-5, stream=N
 
 
 def moe_layernorm_bwd_workspace_bytes(T: int, D: int) -> int:
-    return int(load().moe_layernorm_bwd_workspace_bytes(T, D))
+    return int(load().moe_layernorm_bwd_workspace_bytes(T, D)) if D <= _INT32_MAX else 0
 
 
 def moe_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream=None) -> None:
@@ -710,7 +720,7 @@ _LOGIT_DTYPES = (torch.float32, torch.bfloat16)
 def _choices(topk_ids, T: int, dev: int):
     """K and the pointer of topk_ids [T, K]."""
     K = topk_ids.shape[1] if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
-    return K, _operand(topk_ids, "topk_ids", torch.int32, (T, K), dev)
+    return _int32(K, "topk_ids"), _operand(topk_ids, "topk_ids", torch.int32, (T, K), dev)
 
 
 def moe_router_topk_fwd(logits, topk_ids, topk_scores, normalize: bool = True, stream=None) -> None:
@@ -736,7 +746,7 @@ def moe_router_topk_bwd(logits, topk_ids, dscores, dlogits, normalize: bool = Tr
 
 def moe_lm_workspace_bytes(T: int, D: int, V: int, K: int = 1) -> int:
     """Workspace of the moe_lm_* calls; K is the number of teacher entries per row (1 for cross entropy)."""
-    return int(load().moe_lm_workspace_bytes(T, D, V, K))
+    return int(load().moe_lm_workspace_bytes(T, D, V, K)) if max(D, V, K) <= _INT32_MAX else 0
 
 
 _BF16 = (torch.bfloat16,)
@@ -746,13 +756,13 @@ def _head(x, w):
     """T, D, V, device and the pointers of x [T, D] and w [V, D]."""
     T, D, dev, px = _rows(x, "x", _BF16)
     V = w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 2 else 0
-    return T, D, V, dev, px, _operand(w, "w", torch.bfloat16, (V, D), dev)
+    return T, D, _int32(V, "w"), dev, px, _operand(w, "w", torch.bfloat16, (V, D), dev)
 
 
 def _teacher(teacher_ids, teacher_logits, T: int, dev: int):
     """K and the pointers of teacher_ids and teacher_logits [T, K]."""
     K = teacher_ids.shape[1] if isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2 else 0
-    return (K, _operand(teacher_ids, "teacher_ids", torch.int32, (T, K), dev),
+    return (_int32(K, "teacher_ids"), _operand(teacher_ids, "teacher_ids", torch.int32, (T, K), dev),
             _operand(teacher_logits, "teacher_logits", torch.float32, (T, K), dev))
 
 
