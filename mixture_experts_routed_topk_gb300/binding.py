@@ -770,6 +770,14 @@ def _vector(t, name: str, T: int, dev: int) -> int:
     return _operand(t, name, torch.float32, (T,), dev)
 
 
+def _ignored(ignore_index) -> int:
+    """ignore_index as a label can have it."""
+    i = int(ignore_index)
+    if not -_INT32_MAX - 1 <= i <= _INT32_MAX:
+        raise ValueError(f"ignore_index {i} does not fit 32 bits, as the targets do")
+    return i
+
+
 def _grad(t, name: str, shape, dev: int) -> int:
     return 0 if t is None else _operand(t, name, torch.bfloat16, shape, dev)
 
@@ -780,7 +788,7 @@ def moe_lm_ce_fwd(x, w, targets, loss, lse, workspace, ignore_index: int = -100,
     MOE_DEV_BAD_TARGET in the workspace's status word and counts as ignored."""
     T, D, V, dev, px, pw = _head(x, w)
     _check("moe_lm_ce_fwd", load().moe_lm_ce_fwd(
-        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(loss, "loss", T, dev),
+        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), _ignored(ignore_index), _vector(loss, "loss", T, dev),
         _vector(lse, "lse", T, dev), T, D, V, _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
 
 
@@ -789,7 +797,7 @@ def moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, dw, workspace, ignore_index: in
     moe_lm_ce_fwd."""
     T, D, V, dev, px, pw = _head(x, w)
     _check("moe_lm_ce_bwd", load().moe_lm_ce_bwd(
-        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), int(ignore_index), _vector(lse, "lse", T, dev),
+        px, pw, _operand(targets, "targets", torch.int32, (T,), dev), _ignored(ignore_index), _vector(lse, "lse", T, dev),
         _vector(dloss, "dloss", T, dev), _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V,
         _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
 

@@ -187,3 +187,11 @@ def test_workspaces_of_sizes_past_32_bits():
     assert binding.moe_layernorm_bwd_workspace_bytes(4, WRAP + 64) == 0
     for sizes in ((4, WRAP + 64, 100, 1), (4, 64, WRAP + 100, 1), (4, 64, 100, WRAP + 1)):
         assert binding.moe_lm_workspace_bytes(*sizes) == 0
+
+
+@pytest.mark.parametrize("name", ["moe_lm_ce_fwd", "moe_lm_ce_bwd"])
+@pytest.mark.parametrize("ignore", [1 << 31, -(1 << 31) - 1, 1 << 32, (1 << 40) + 7])
+def test_an_ignore_index_past_32_bits(checked, name, ignore):
+    with pytest.raises(ValueError, match="ignore_index"):
+        sized_calls(**SMALL, ignore=ignore)[name]()
+    assert not checked
