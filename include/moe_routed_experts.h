@@ -629,7 +629,10 @@ size_t moe_lm_workspace_bytes(int64_t T, int32_t D, int32_t V, int32_t K);
  *   loss, lse    device fp32 [T] (lse also of ignored rows)
  *   workspace    device, moe_lm_workspace_bytes(T, D, V, 1) bytes, 256-byte aligned; its first 4 bytes are
  *                the status word (moe_get_status)
- * bf16 products, fp32 accumulation; sums and exponentials in fp32.
+ * bf16 products, fp32 accumulation; sums and exponentials in fp32. The tensor cores' accumulation rounds
+ * towards zero; the logits are multiplied by 1 + min(D, 65536) 2^-30 for it, which is about what a dense row
+ * loses. A row of few non-zero elements loses nothing, and its logits are off by that factor. Of a row whose
+ * target is its largest logit the loss is 0 or more.
  */
 moe_status_t moe_lm_ce_fwd(const void *x, const void *w, const int32_t *targets, int32_t ignore_index,
                            float *loss, float *lse, int64_t T, int32_t D, int32_t V, void *workspace,

@@ -739,12 +739,19 @@ moe_status_t prepare_targets(const LmProblem& p, const LmPlan& pl, bool backward
 }
 
 // 1 / temperature, and what the tensor cores' accumulation takes off. They cut the fp32 accumulator's low
-// bits off after each 16 products, towards zero: a logit comes out too small by 1.5e-8 to 1.6e-8 of itself
-// per such step (measured for D = 256 to 7168 on rows that lean towards their target). 2^-26 per step is
-// given back. Relative error of the loss at D = 4096, before and after: rows that lean towards their target
-// 1.2e-5 and 1.5e-6, normal rows 6.1e-7 and 2.5e-7, rows with two thirds of their weight in a few columns
-// 7.4e-7 and 3.0e-7; rows with 2 % of their elements, which lose nothing, 5e-8 and 5e-7.
-double logit_scale(int32_t D, float temperature) { return (1.0 + D * 0x1p-30) / static_cast<double>(temperature); }
+// bits off after each 16 products, towards zero, so that a logit comes out too small, by this part of itself per
+// such step (measured for D = 256 to 65536): normal rows 1.1e-8 to 2.1e-8, rows that lean towards the weight row
+// 1.6e-8 to 1.8e-8, rows whose products are all positive 2.2e-8 to 9.6e-8. 2^-26 (1.5e-8) per step, which is
+// about the least that dense rows lose, is given back. Relative error of the loss at D = 4096, before and
+// after: rows that lean towards their target 1.2e-5 and 1.5e-6, normal rows 6.1e-7 and 2.5e-7, rows with two
+// thirds of their weight in a few columns 7.4e-7 and 3.0e-7.
+// Rows of few non-zero elements lose nothing and are off by the factor instead: by 5e-7 with 2 % of the elements,
+// by D 2^-30 at most, a 64th of the bound D 2^-24 of a sum of D products in fp32. D counts up to kScaleMaxD only,
+// the largest that was measured.
+constexpr int32_t kScaleMaxD = 65536;
+double logit_scale(int32_t D, float temperature) {
+    return (1.0 + std::min(D, kScaleMaxD) * 0x1p-30) / static_cast<double>(temperature);
+}
 
 LmArgs common_args(const LmProblem& p, const LmPlan& pl) {
     LmArgs a{};

@@ -100,3 +100,43 @@ def test_teacher_logits_at_the_ends_of_their_type(tau):
         logits[1] *= torch.tensor([1.0, tau, tau])
     ids = torch.tensor([[5, 0, 299]] * 6, dtype=I32)
     Case(x, w, dloss, ids=ids, logits=logits, tau=tau).check()
+
+
+# --------------------------------------------------------------- what the factor on the logits does
+
+FACTOR = 2.0 ** -30  # per element of D, up to 65536 of them
+
+
+def given_back(D):
+    return min(D, 65536) * FACTOR
+
+
+@pytest.mark.parametrize("D", [64, 1024, 4096, 65536, 1 << 20])
+def test_rows_of_one_element_are_off_by_the_factor_at_most(D):
+    # their products are exact and lose nothing, so the factor is all that they can be off by
+    T, V = 16, 40
+    x = torch.zeros(T, D)
+    x[torch.arange(T), torch.randint(0, D, (T,), generator=gen(60))] = 20 * torch.randn(T, generator=gen(61))
+    x, w, t = x.to(BF16), torch.randn(V, D, generator=gen(62)).to(BF16), torch.randint(0, V, (T,), generator=gen(63))
+    loss, lse = ce_fwd(x, w, t)
+    z = x.double() @ w.double().T
+    want, zt = torch.logsumexp(z, 1), z.gather(1, t[:, None])[:, 0]
+    size = z.abs().amax(1)
+    bound = 1.01 * given_back(D) * size + R.U32 * (8 * (size + want.abs() + 2) + 64)
+    R.check(lse, want, bound, "lse")
+    R.check(loss, want - zt, 2 * bound, "loss")
+
+
+@pytest.mark.parametrize("D", [1024, 4096, 16384])
+def test_the_factor_gives_back_what_rows_that_lean_lose(D):
+    # with one word, lse is its logit. On average no more than half of the factor is left, whichever way: without it
+    # the mean is off by the whole of it
+    T = 256
+    w = (torch.randn(1, D, generator=gen(D + 64)) / D ** 0.5).to(BF16)
+    x = (torch.randn(T, D, generator=gen(D + 65)) + 8 * w.float()).to(BF16)
+    _, lse = ce_fwd(x, w, torch.zeros(T))
+    z = (x.double() @ w.double().T)[:, 0]
+    rows = z > 4
+    assert rows.sum() > T // 2
+    off = (lse.cpu().double() / z - 1)[rows].mean()
+    assert abs(float(off)) < 0.5 * given_back(D), float(off) / given_back(D)
