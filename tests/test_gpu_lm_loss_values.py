@@ -140,3 +140,45 @@ def test_the_factor_gives_back_what_rows_that_lean_lose(D):
     assert rows.sum() > T // 2
     off = (lse.cpu().double() / z - 1)[rows].mean()
     assert abs(float(off)) < 0.5 * given_back(D), float(off) / given_back(D)
+
+
+# ------------------------------------------------------------------- gradients against differences
+
+@pytest.mark.parametrize("kind", ["ce", "distill"])
+@pytest.mark.parametrize("of", ["w", "x"])
+def test_the_softmax_part_of_the_gradient_is_the_difference_of_the_forward(kind, of):
+    # Moved is what the targets' part of the gradient does not see: rows of w that are nobody's target, or columns
+    # of x in which the targets' rows are 0. All terms have one sign, so nothing cancels.
+    T, D, V, cols, h = 64, 64, 40, 8, 1.0 / 256
+    x = torch.randint(0, 16, (T, D), generator=gen(70)).float() / 16
+    w = torch.randint(-8, 9, (V, D), generator=gen(71)).float() / 16
+    w[V // 2:, :cols] = torch.randint(4, 9, (V // 2, cols), generator=gen(72)).float() / 16
+    w[:V // 2, :cols] = 0.0
+    move = torch.zeros(V, D) if of == "w" else torch.zeros(T, D)
+    move[V // 2 if of == "w" else 0:, :cols] = 1.0
+    dloss = 0.5 + torch.rand(T, generator=gen(73))
+    if kind == "ce":
+        kw = dict(targets=torch.randint(0, V // 2, (T,), generator=gen(74)).to(I32))
+    else:
+        kw = dict(ids=torch.randint(0, V // 2, (T, 3), generator=gen(74)).to(I32),
+                  logits=torch.randn(T, 3, generator=gen(75)), tau=2.0)
+
+    def case(s):
+        xs, ws = (x, w + s * h * move) if of == "w" else (x + s * h * move, w)
+        assert torch.equal(xs.to(BF16).float(), xs) and torch.equal(ws.to(BF16).float(), ws)  # moved by exact steps
+        return Case(xs.to(BF16), ws.to(BF16), dloss, **kw)
+
+    up, down = (case(s).fwd()[0].double().cpu() for s in (1, -1))
+    diff = float(((up - down) * dloss.double()).sum()) / (2 * h)
+    c = case(0)
+    dx, dw = c.bwd(c.fwd()[1])
+    got = float(((dw if of == "w" else dx).double().cpu() * move.double()).sum())
+    # dl and the result each rounded by half a bf16 step; a third derivative of at most a tenth of the cube of
+    # what the logits move per unit; and the fp32 losses, a few steps of the logits' products, over 2 h
+    tau = kw.get("tau", 1.0)
+    a = float((x[:, :cols].sum(1) if of == "w" else w[V // 2:, :cols].sum(1)).max()) / tau
+    size = float((x.double() @ w.double().abs().T).max()) / tau
+    bound = 2 * 2.0 ** -8 * abs(got) + float(dloss.sum()) * tau * tau * (
+        0.1 * a ** 3 * h * h / 6 + 2 * (20 * R.ACC * size + 64 * R.U32 * 8) / (2 * h))
+    assert bound < 0.05 * abs(got), (bound, got)
+    assert abs(diff - got) < bound, (diff, got, bound)
