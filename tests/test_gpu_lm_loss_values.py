@@ -94,8 +94,8 @@ def test_teacher_logits_at_the_ends_of_their_type(tau):
     x, w, dloss = head(6, 64, 300, 50)
     x = (x.float() * min(1.0, tau)).to(BF16)  # the student's logits stay ordinary at the temperature
     low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
-    logits = torch.tensor([[low, low, low], [low, 0.0, 1.0], [high, high, 0.0], [high, low, high], [0.9 * high, high, 1.0],
-                           [-torch.inf, low, low]])
+    logits = torch.tensor([[low, low, low], [low, 0.0, 1.0], [high, high, 0.0], [high, low, high],
+                           [0.9 * high, high, 1.0], [-torch.inf, low, low]])
     if tau < 1.0:
         logits[1] *= torch.tensor([1.0, tau, tau])
     ids = torch.tensor([[5, 0, 299]] * 6, dtype=I32)
@@ -182,3 +182,60 @@ def test_the_softmax_part_of_the_gradient_is_the_difference_of_the_forward(kind,
         0.1 * a ** 3 * h * h / 6 + 2 * (20 * R.ACC * size + 64 * R.U32 * 8) / (2 * h))
     assert bound < 0.05 * abs(got), (bound, got)
     assert abs(diff - got) < bound, (diff, got, bound)
+
+
+# ----------------------------------------------------------------------- weights past 32 bits, and pieces
+
+def test_dx_from_weights_past_32_bits():
+    # dx comes from rows of w on both sides of 2^31 elements, summed over slices of the vocabulary. An eighth of the
+    # rows, one after another, has a value of its own in every eighth column: a slice that is missed, or read from
+    # elsewhere, shows in those columns. The targets' rows have none, so that theirs does not hide it.
+    T, D, V, parts, value = 3, 4096, 600_003, 8, 1.0 / 16
+    w = torch.randn(V, D, device="cuda", dtype=BF16).mul_(0.5 / D ** 0.5)
+    targets = torch.tensor([V - 1, 524_288, 7], dtype=I32, device="cuda")
+    step = -(-V // parts)
+    for b in range(parts):
+        w[b * step:(b + 1) * step, b::parts] += value
+    w[targets.long()] = 0
+    x = torch.randn(T, D // parts, parts, generator=gen(80))
+    x = (x - x.mean(1, keepdim=True)).view(T, D).to(BF16).cuda()  # so that every eighth has about the same probability
+    dloss = torch.tensor([1.0, -0.5, 2.0], device="cuda")
+    z = torch.cat([x.double() @ w[a:a + 50_000].double().T for a in range(0, V, 50_000)], 1)
+    lse = torch.logsumexp(z, 1).float()
+    ws = B.alloc_workspace(B.moe_lm_workspace_bytes(T, D, V))
+    dx = torch.full_like(x, 3.0)
+    B.moe_lm_ce_bwd(x, w, targets, lse, dloss, dx, None, ws)
+    assert B.moe_get_status(ws) == 0
+    size = x.double().norm(dim=1)[:, None] * 2.0  # no row of w is longer: 0.5 at random and 1/16 in 512 columns
+    dz = (D // 16 + 16) * R.ACC * size
+    dl = dloss.double()[:, None] * torch.exp(z - lse.double()[:, None])
+    # what an eighth adds to its columns
+    share = value * torch.stack([dl[:, b * step:(b + 1) * step].sum(1).abs() for b in range(parts)], 1)
+    dl[range(T), targets.long()] -= dloss.double()
+    bdl = dl.abs() * (dz + 8 * R.U32 * (z.abs() + lse.double().abs()[:, None] + 2)) * 1.01 + R.round_bound(dl, BF16)
+    want, bound = (torch.zeros(T, D, dtype=torch.double, device="cuda") for _ in range(2))
+    for a in range(0, V, 50_000):
+        part, rows = slice(a, a + 50_000), w[a:a + 50_000].double()
+        want += dl[:, part] @ rows
+        bound += bdl[:, part] @ rows.abs() + (V // 16 + 64) * R.ACC * (dl[:, part].abs() @ rows.abs())
+    bound = 1.01 * bound + R.round_bound(want, BF16)
+    columns = torch.arange(D, device="cuda") % parts
+    assert (bound < 0.5 * share[:, columns] / 8).all()  # half of what a slice of a sixty-fourth adds
+    R.check(dx, want, bound, "dx")
+
+
+def test_both_gradients_in_one_grid_over_several_pieces():
+    # 2 T V bytes pass the 512 MB of a piece, with few enough rows and weights for the joint grid
+    T, D, V = 512, 64, 600_001
+    x, w, dloss = head(T, D, V, 81)
+    t = torch.randint(0, V, (T,), generator=gen(82)).to(I32)
+    t[::5] = -100
+    t[1], t[2], t[3] = V - 1, V // 2, 300_032
+    c = Case(x, w, dloss, targets=t)
+    lse = c.fwd()[1]
+    dx, dw = c.bwd(lse)
+    assert B.moe_get_status(c.ws) == 0
+    want = R.lm_bwd(c.dev["x"], c.dev["w"], c.sparse("cuda"), lse, c.dev["dloss"], 1.0)
+    R.check(dx, want[0], want[2], "dx")
+    R.check(dw, want[1], want[3], "dw")
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw), c.bwd(lse)))
