@@ -97,7 +97,8 @@ class MoeLm:
         return self.loss
 
     def status(self) -> int:
-        """The device status bits of the step's calls (synchronises)."""
+        """The device status bits of the step's last call on each workspace (synchronises). The loss's forward and
+        backward share one, so the forward's bits last only until the backward, which raises bad targets again."""
         return moe.moe_get_status(self.ws_fwd) | moe.moe_get_status(self.ws_bwd) | moe.moe_get_status(self.ws_head)
 
 
@@ -150,11 +151,11 @@ def train(steps: int = 100, distill: bool = False, log=None, **sizes) -> list[fl
         else:
             loss = model.forward_backward(tokens, targets)
         losses.append(float(loss.mean()))
+        if model.status():  # before the next step's calls clear it
+            raise RuntimeError(f"step {step}: device status {model.status():#x}")
         opt.step()
         if log and (step % 10 == 0 or step == steps - 1):
             log(f"step {step}: loss {losses[-1]:.4f}")
-    if model.status():
-        raise RuntimeError(f"device status {model.status():#x}")
     return losses
 
 
