@@ -316,10 +316,15 @@ struct LmLse : LmLogits {
             for (int i = 1; i < 32; ++i) cm = fmaxf(cm, __uint_as_float(w[i]));
             const float top = fmaxf(m, cm);
             const float base = top == -INFINITY ? 0.0f : top;  // nothing but -inf so far: its terms are 0
-            float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // small terms meet each other before they meet the 1
+            // small terms meet each other before they meet the 1; two numbers to an instruction
+            float2 q[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) q[i & 3] += exp2_fast((__uint_as_float(w[i]) - base) * scale2);
-            s = fmaf(s, exp2_fast((m - base) * scale2), (q[0] + q[1]) + (q[2] + q[3]));
+            for (int i = 0; i < 32; i += 2) {
+                const float2 z = make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+                const float2 d = __fmul2_rn(__fadd2_rn(z, make_float2(-base, -base)), make_float2(scale2, scale2));
+                q[(i >> 1) & 1] = __fadd2_rn(q[(i >> 1) & 1], make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+            }
+            s = fmaf(s, exp2_fast((m - base) * scale2), (q[0].x + q[0].y) + (q[1].x + q[1].y));
             m = top;
         }
         if (live) a.part[static_cast<int64_t>(t.n) * a.T + row] = make_float2(m, s);
