@@ -12,8 +12,9 @@
 // Rows up to 8192 elements: persistent blocks of 512 threads, in groups of 32 to 512 threads that own
 // one row at a time (16 elements per thread). A group asynchronously copies the rows it will need
 // next into a ring in shared memory, so that loads are in flight while it waits in the two row sums; it
-// takes two rows through those sums at a time, and keeps the parameters in registers. Where rows start on 16-byte boundaries a thread copies and reads only its own elements; otherwise the
-// group copies the aligned 16-byte pieces that cover the row, and each thread picks out its elements.
+// takes two rows through those sums at a time, and keeps the parameters in registers. Where rows start on
+// 16-byte boundaries a thread copies and reads only its own elements; otherwise the group copies the aligned
+// 16-byte pieces that cover the row, and each thread picks out its elements.
 //
 // The backward blocks keep their column sums of dy xhat and dy in registers, so dgamma and dbeta cost
 // no extra pass over x and dy. Each block writes one row of partial sums, and a second kernel adds the
@@ -24,8 +25,9 @@
 // Measured (device time; the copy rate is 6.79 TB/s): bf16 16384 x 7168 forward 87 us (5.4 TB/s), backward
 // 121 us (5.8 TB/s), both bound by instruction issue and the waits in the row sums as much as by memory
 // (a block per row without the ring and with the parameters read anew: 157 and 265 us); 4096 x 2048 11 and
-// 17 us and fp16 8191 x 1001 14 and 25 us, where a group has seven rows or fewer and the latency of a launch,
-// of the first loads and of four rounds decides.
+// 16 us and fp16 8191 x 1001 13 and 24 us, where a group has seven rows or fewer and the latency of a launch,
+// of the first loads and of four rounds decides. Long rows, bf16 4096 x 16384: 90 us forward, and 712 us
+// backward, whose column sums go through global memory for every row (39 and 59 us at the copy rate).
 #include <algorithm>
 #include <atomic>
 

@@ -13,8 +13,9 @@
 // A row whose label is ignored, or none of whose teacher entries is kept, has loss 0 and c_t = 0.
 //
 // All products run on the tcgen05 pipeline of gemm_pipeline.cuh (bf16 operands, fp32 accumulation):
-//   forward: the epilogue reduces a 128 x 256 logit tile to one (maximum, sum of exponentials) per
-//     row and picks the targets' logits out of it; k_lm_join joins a row's tiles.
+//   forward: the epilogue reduces a logit tile of 128 rows and 32 to 256 columns (pick_columns) to one
+//     (maximum, sum of exponentials) per row and picks the targets' logits out of it; k_lm_join joins a
+//     row's tiles.
 //   backward: over pieces of the vocabulary that fit the workspace, the epilogue of the recomputed
 //     logits writes dl in bf16; one more grid turns the piece into its rows of dW and its share of
 //     dx. dx is summed over pieces and over slices of the contraction in fp32 and rounded once.
@@ -25,10 +26,13 @@
 // search, and each thread picks them out of the 32 logits that it holds in registers. Ids that repeat
 // in a row count once each, in order.
 //
-// Measured (device time; cuBLAS's bf16 rate is 1913 TFLOP/s in bursts, 1729 sustained): 4096 x 2048 x 32000
-// (T x D x V) forward 289 us (1855 TFLOP/s), backward 951 us (1693): dl 307, dx 331, dW 311 us, with the
-// tensor pipe 85 % busy in the forward and 78, 84 and 84 % in the backward. The exponentials run under the
-// next tile's products. 16 x 2048 x 32000 forward 31 us: 26 us of it read W's 131 MB.
+// Measured, calls back to back (cuBLAS's bf16 rate is 1915 TFLOP/s in bursts, 1717 sustained): 4096 x 2048 x
+// 32000 (T x D x V) forward 307 us (1749 TFLOP/s), backward 1003 us (1605), 1045 us (1541) as a loop of calls
+// on changing inputs sees it. The backward's shares are 32 % dl, 35 % dx and 33 % dW, with the tensor pipe 78, 84
+// and 84 % busy; 85 % in the forward, whose exponentials run under the next tile's products.
+// 16 x 2048 x 32000 forward 32 us: some 26 us of it read W's 131 MB. 64 x 2048 x 32000 backward 85 us, where
+// the traffic takes 39: dl's 125 tiles leave 27 SMs idle, and W is read from memory twice, once for the logits
+// and again for dx, as it does not fit L2 beside what is written.
 #include <algorithm>
 #include <climits>
 
@@ -625,10 +629,10 @@ struct LmPlan {
 
 // Whether a piece's two gradients run in one grid. Together they save the rounds in which SMs wait for the
 // last tiles, which counts with few rows; apart they keep to one set of operands at a time, which counts
-// once the weights and their gradient pass the 129 MB L2 by far. Together and apart: 64 x 2048 x 32000
-// (131 MB of weights) 90 and 98 us, 512 x 2048 x 32000 195 and 212 us, 300 x 1024 x 50257 106 and 114 us;
-// 1024 x 2048 x 32000 312 and 305 us, 2039 x 2048 x 32000 501 and 497 us; 4096 x 4096 x 50257 (412 MB)
-// 3.25 and 3.08 ms, 16 x 4096 x 131072 (1074 MB) 543 and 496 us.
+// once the weights and their gradient pass the 129 MB L2 by far. The whole backward, together and apart: 64 x
+// 2048 x 32000 (131 MB of weights) 85 and 88 us, 512 x 2048 x 32000 171 and 179 us, 300 x 1024 x 50257 105 and
+// 113 us; 1024 x 2048 x 32000 286 and 287 us, 2039 x 2048 x 32000 528 and 521 us; 4096 x 4096 x 50257 (412 MB)
+// 3.23 and 3.14 ms, 16 x 4096 x 131072 (1074 MB) 517 and 504 us.
 bool gradients_together(int64_t T, int32_t cols, int32_t D) { return T <= 512 && 2ll * cols * D <= (192ll << 20); }
 
 // Slices of dx's contraction: a grid of few tiles leaves SMs idle, and each slice costs a round of fp32
