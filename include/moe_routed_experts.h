@@ -1,7 +1,8 @@
 /*
  * moe_routed_experts.h -- C ABI of the routed top-k mixture-of-experts expert layer (forward,
- * backward and block-scaled forwards) and of the operators around it in a training step (layer norm,
- * top-k router, vocabulary losses) for NVIDIA GB300 (sm_103a).
+ * backward and block-scaled forwards), of the operators around it in a training step (layer norm, norms
+ * around a block, top-k router, vocabulary losses) and of those of a decoding step (the layer for a few
+ * tokens, the choice of the next token) for NVIDIA GB300 (sm_103a).
  *
  * The layer (the expert path shared by the TeraMoE README, Dist-MoE 0.1.0 and the Primus MegaMoE
  * guide; the MoonEP page describes its weight layout):
@@ -679,11 +680,53 @@ moe_status_t moe_lm_distill_bwd(const void *x, const void *w, const int32_t *tea
                                 const float *dloss, void *dx, void *dw, int64_t T, int32_t D, int32_t V,
                                 int32_t K, void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------ */
+/* The operators of a decoding step: the layer for a few tokens and the choice of the next       */
+/* token (the norms around a block, which a training step runs too, stand above). The            */
+/* conventions at the top hold, but for the alignment and shape limits that an entry point       */
+/* states itself. All are deterministic.                                                        */
+/* ------------------------------------------------------------------------------------------ */
+
+/*
+ * Bytes of workspace of moe_routed_experts_fwd_few and moe_layer_fwd_few (0 for T = 0 and for sizes
+ * outside their limits: T <= 32, T K <= 512, D and F multiples of 64, E <= 4096). Pure arithmetic.
+ */
+size_t moe_few_workspace_bytes(int64_t T, int32_t D, int32_t F, int32_t E, int32_t K);
+
+/*
+ * The layer for 1 to 32 tokens, in two kernels that stream each chosen expert's weights once:
+ *     out[t] = sum_{k<K} score[t,k] * W2[e] ( SiLU(Wg[e] x_t) * (Wu[e] x_t) ),   e = ids[t,k]
+ * Arguments, types and alignment as for moe_routed_experts_fwd; a workspace of
+ * moe_few_workspace_bytes(T, D, F, E, K), whose first 4 bytes are the status word. T > 32 or T K > 512:
+ * MOE_ERR_UNSUPPORTED_SHAPE.
+ * H = SiLU(g) u is rounded to bf16 as there; the pairs' outputs are not, they are scaled and added up in
+ * fp32 and rounded once. A pair with a score of 0 is passed over (its expert's weights are not read for
+ * it, and need not be finite). An id outside [0, E) sets MOE_DEV_BAD_EXPERT_ID and contributes 0; ids may
+ * repeat. A token without pairs gets a row of zeros. out may not overlap x or the weights.
+ */
+moe_status_t moe_routed_experts_fwd_few(const void *x, const int32_t *topk_ids, const void *topk_scores,
+                                        int32_t scores_dtype, const void *w13, const void *w2, void *out, int64_t T,
+                                        int32_t D, int32_t F, int32_t E, int32_t K, void *workspace,
+                                        size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The same from the router's logits on: moe_router_topk_fwd's choice and moe_routed_experts_fwd_few on it,
+ * without a launch between them.
+ *   logits       device [T,E], fp32 or bf16 (MOE_DTYPE_F32, MOE_DTYPE_BF16), element-aligned
+ *   normalize    as for moe_router_topk_fwd
+ *   topk_ids     device int32 [T,K];  topk_scores  device fp32 [T,K]: written, as moe_router_topk_fwd does
+ * K <= E (MOE_ERR_INVALID_ARG otherwise). A row of nothing but -inf has scores of 0, and an output of 0.
+ */
+moe_status_t moe_layer_fwd_few(const void *x, const void *logits, int32_t dtype, int32_t normalize, const void *w13,
+                               const void *w2, int32_t *topk_ids, float *topk_scores, void *out, int64_t T, int32_t D,
+                               int32_t F, int32_t E, int32_t K, void *workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
 /*
  * Reads the device status word at the start of `workspace` (a forward, backward, routing or
  * vocabulary-loss workspace) into *device_bits (host memory): 0, or an OR of MOE_DEV_* bits raised
- * since the last moe_fwd_dispatch / moe_routed_experts_fwd / moe_routing / moe_lm_* on that
- * workspace. Synchronises `stream` first; the only synchronising entry point.
+ * since the last moe_fwd_dispatch / moe_routed_experts_fwd / moe_routing / moe_lm_* / moe_*_fwd_few on
+ * that workspace. Synchronises `stream` first; the only synchronising entry point.
  */
 moe_status_t moe_get_status(const void *workspace, uint32_t *device_bits, moe_stream_t stream);
 

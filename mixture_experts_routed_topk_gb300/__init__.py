@@ -1,5 +1,6 @@
-"""Routed top-k mixture-of-experts expert layer for GB300 (sm_103a), and the operators around it in a
-training step: layer norm, the top-k router and the vocabulary losses.
+"""Routed top-k mixture-of-experts expert layer for GB300 (sm_103a), the operators around it in a training
+step (layer norm, the norms around a block, the top-k router and the vocabulary losses) and those of a decoding
+step (the layer for a few tokens and the choice of the next token).
 
 The compute path is the C-ABI library ``libmoe_gb300.so`` (hand-written CUDA kernels); the
 functions re-exported here are its thin ctypes binding. Importing this package does not load the
@@ -45,6 +46,9 @@ __all__ = [
     "moe_lm_ce_bwd",
     "moe_lm_distill_fwd",
     "moe_lm_distill_bwd",
+    "moe_few_workspace_bytes",
+    "moe_routed_experts_fwd_few",
+    "moe_layer_fwd_few",
     "MOE_WEIGHT_W13",
     "MOE_WEIGHT_W2",
     "moe_get_status",

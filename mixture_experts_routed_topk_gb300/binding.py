@@ -125,6 +125,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 [vp, vp, vp, vp, ctypes.c_float, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
             "moe_lm_distill_bwd": (
                 [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_few_workspace_bytes": ([i64, i32, i32, i32, i32], sz),
+            "moe_routed_experts_fwd_few": (
+                [vp, vp, vp, i32, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_layer_fwd_few": (
+                [vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -824,3 +829,45 @@ def moe_lm_distill_bwd(x, w, teacher_ids, teacher_logits, lse, dloss, dx, dw, wo
         px, pw, pi, pl, float(temperature), _vector(lse, "lse", T, dev), _vector(dloss, "dloss", T, dev),
         _grad(dx, "dx", (T, D), dev), _grad(dw, "dw", (V, D), dev), T, D, V, K, _workspace(workspace, dev),
         workspace.numel(), _stream_of(stream, dev)))
+
+
+# ------------------------------------------------------------------------ a decoding step
+
+def moe_few_workspace_bytes(T: int, D: int, F: int, E: int, K: int) -> int:
+    """Workspace of moe_routed_experts_fwd_few and moe_layer_fwd_few."""
+    return int(load().moe_few_workspace_bytes(T, D, F, E, K)) if max(D, F, E, K) <= _INT32_MAX else 0
+
+
+def _experts(x, w13, w2):
+    """T, D, F, E, device and the pointers of x [T,D], w13 [E,2,F,D] and w2 [E,D,F]."""
+    T, D, dev, px = _rows(x, "x", _BF16)
+    E, F = (w13.shape[0], w13.shape[2]) if isinstance(w13, torch.Tensor) and w13.dim() == 4 else (0, 0)
+    return (T, D, _int32(F, "w13"), _int32(E, "w13"), dev, px, _operand(w13, "w13", torch.bfloat16, (E, 2, F, D), dev),
+            _operand(w2, "w2", torch.bfloat16, (E, D, F), dev))
+
+
+def moe_routed_experts_fwd_few(x, topk_ids, topk_scores, w13, w2, out, workspace, stream=None) -> None:
+    """The layer for 1 to 32 tokens (T K at most 512), as moe_routed_experts_fwd: each chosen expert's weights are
+    streamed once, by two kernels. The workspace is moe_few_workspace_bytes(T, D, F, E, K) bytes."""
+    T, D, F, E, dev, px, p13, p2 = _experts(x, w13, w2)
+    K, pi = _choices(topk_ids, T, dev)
+    bf16 = isinstance(topk_scores, torch.Tensor) and topk_scores.dtype is torch.bfloat16
+    ps = _operand(topk_scores, "topk_scores", torch.bfloat16 if bf16 else torch.float32, (T, K), dev)
+    _check("moe_routed_experts_fwd_few", load().moe_routed_experts_fwd_few(
+        px, pi, ps, MOE_SCORES_BF16 if bf16 else MOE_SCORES_F32, p13, p2,
+        _operand(out, "out", torch.bfloat16, (T, D), dev), T, D, F, E, K, _workspace(workspace, dev), workspace.numel(),
+        _stream_of(stream, dev)))
+
+
+def moe_layer_fwd_few(x, logits, w13, w2, topk_ids, topk_scores, out, workspace, normalize: bool = True,
+                      stream=None) -> None:
+    """moe_router_topk_fwd on logits [T,E] (fp32 or bf16) into topk_ids and topk_scores, and the layer on its choice,
+    without a launch between them. Limits and workspace as for moe_routed_experts_fwd_few."""
+    T, D, F, E, dev, px, p13, p2 = _experts(x, w13, w2)
+    K, pi = _choices(topk_ids, T, dev)
+    bf16 = isinstance(logits, torch.Tensor) and logits.dtype is torch.bfloat16
+    pz = _operand(logits, "logits", torch.bfloat16 if bf16 else torch.float32, (T, E), dev)
+    _check("moe_layer_fwd_few", load().moe_layer_fwd_few(
+        px, pz, 1 if bf16 else 0, 1 if normalize else 0, p13, p2, pi,
+        _operand(topk_scores, "topk_scores", torch.float32, (T, K), dev), _operand(out, "out", torch.bfloat16, (T, D), dev),
+        T, D, F, E, K, _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))

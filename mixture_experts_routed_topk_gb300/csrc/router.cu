@@ -30,16 +30,6 @@ namespace {
 
 constexpr int kRouterThreads = 128;
 
-// The float's position in the order of the reals as an unsigned integer; never 0. The addition makes
-// -0 equal to +0 and every NaN the canonical one, whose key is the largest.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const int32_t b = __float_as_int(v + 0.0f);
-    return static_cast<uint32_t>(b ^ ((b >> 31) | INT32_MIN));
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
-}
-
 // Element i of a thread's kN: kVec consecutive experts at a time, kThreads threads side by side.
 // Ascending in i, so the first of a thread's equal keys is the one with the lowest expert id.
 template <int kThreads, int kVec>

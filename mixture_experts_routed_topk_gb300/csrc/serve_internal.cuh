@@ -1,0 +1,40 @@
+// serve_internal.cuh -- launchers of the operators of a decoding step (the layer for a few tokens, the
+// choice of the next token), shared by their kernels and the C ABI. Not part of the public C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// The layer for a few tokens (few_tokens.cu): tokens are the columns of its products, up to four tiles of
+// eight, and the bits of a 32-bit mask per expert; a (token, expert) pair's score and H row are looked up in
+// shared memory.
+constexpr int kFewMaxTokens = 32;
+constexpr int kFewMaxPairs = 512;
+
+struct FewProblem {
+    const void* x;        // bf16 [T, D]
+    const int32_t* ids;   // [T, K], or null: chosen from the logits
+    const void* scores;   // [T, K] fp32 or bf16
+    int32_t scores_dtype;
+    const void* logits;   // [T, E] fp32 or bf16
+    int32_t logits_dtype;
+    bool normalize;
+    int32_t* ids_out;     // [T, K], with logits
+    float* scores_out;    // [T, K]
+    const void* w13;      // bf16 [E, 2, F, D]
+    const void* w2;       // bf16 [E, D, F]
+    void* out;            // bf16 [T, D]
+    uint32_t* status;
+    void* h;              // bf16 [T*K, F]
+    int32_t T, D, F, E, K;
+    int sm_count;
+};
+moe_status_t launch_few(const FewProblem& p, cudaStream_t stream);
+
+}  // namespace moe
