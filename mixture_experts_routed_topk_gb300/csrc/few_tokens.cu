@@ -2,26 +2,37 @@
 //
 //   out[t] = sum_k s[t,k] W2[e] (SiLU(Wg[e] x_t) * (Wu[e] x_t)),   e = ids[t,k]
 //
-// With a few tokens the layer is the stream of its experts' weights: 6 F D bytes for each distinct expert,
-// and 2 to 64 operations for each of them. So the weights are the M side of every product (16 rows of an
-// mma.sync tile), the tokens are its N side (eight columns a tile, a token keeps its column with every
-// expert), and everything is arranged for the stream: one warp keeps a ring of 16 KB stages filled by TMA,
-// eight warps take one 64-element piece of K of each stage. tcgen05 tiles have 128 rows of weights or more,
-// which is too coarse to share a layer of 8 experts out over 152 SMs, and their rate is not needed: at the
-// memory's rate an SM gets 12 weights a clock, the mma.sync path takes 1024 per column tile.
+// With a few tokens the layer is the stream of its experts' weights: 6 F D bytes for each distinct expert, and 2
+// to 64 operations for each of them. So the weights are the M side of every product (16 rows of an mma.sync
+// tile), an expert's tokens are its N side (eight columns a tile, one tile for most experts), and everything is
+// arranged for the stream. tcgen05 tiles have 128 rows of weights or more, which is too coarse to share a layer of
+// 8 experts out over 152 SMs, and their rate is not needed: at the memory's rate an SM gets 12 weights a clock.
+//
+// The weights are cut into pieces of 16 rows x 64 elements of K. Each warp takes every eighth piece of its block's
+// rows and copies the next two to four of them, with the tokens' columns, into a ring in shared memory in just the
+// 16-byte units that its lanes will read: each lane reads only what it copied itself, so the only order to keep is
+// a lane's wait for its own copies, and no warp waits for another until a tile's sums meet. Measured on the way
+// (1 token, D = 7168, F = 2048, 8 experts; the weights alone take 104 us at the copy rate): a loading warp with TMA
+// boxes of 2 KB 152 us and a ring filled by TMA for each warp 189 us (issue of small boxes and the chain of barrier,
+// products and refill), loads into three sets of registers 143 us, this 109 us.
 //
 //   k_few_gate_up   a tile is 8 gate rows and the same 8 up rows of one expert, over all of D:
 //                   the warps' sums meet in shared memory, SiLU(g) u is written to H (bf16)
-//   k_few_down      a tile is up to 16 rows of the output, over all experts and all of F: each expert's sums
-//                   are scaled by the tokens' scores in fp32 and stay in registers; out is rounded once
+//   k_few_down      a tile is up to 16 rows of the output, over all experts and all of F: each warp adds an
+//                   expert's sums, scaled by the tokens' scores in fp32, to its own 16 rows x T in shared
+//                   memory; the warps' sums meet at the end, and out is rounded once
 //
 // Both kernels first make the plan that the routing kernels make for the large forward: the distinct experts
 // in ascending order, for each the mask of its tokens and its first row of H. Every block makes it anew from
 // the ids (or chooses them from the router's logits), which is quicker than another launch. The second kernel
-// is launched while the first one's last weights are on their way, and fills its ring with W2 before it waits
-// for H; that is what the two rings of less than half an SM's shared memory are for.
+// may start while the first one runs, makes its plan and copies its first weights before it waits for H.
 //
 // A pair whose score is 0 is passed over: it costs no weights. All sums are fp32, in a fixed order.
+//
+// Measured (calls in a graph, other experts in each): 1 x 2048 x 1408, 6 experts 23 us (15.3 at the copy rate);
+// 1 x 7168 x 2048, 8 experts 109 us (104); 16 tokens there 723 us (724); 32 x 4096 x 1536, 8 of 128 experts 697 us
+// (622). Furthest from the weights' time are few experts with many tokens, whose columns cost as much as the weights
+// they meet: 32 x 2048 x 1408, 4 of 8 experts 52 us (20).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,20 +46,23 @@
 namespace moe {
 namespace {
 
-constexpr int kFewWarps = 8;                        // warps that compute; one more loads
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
 constexpr int kFewRows = 16;                        // weight rows of a tile
-constexpr int kFewK = 64;                           // elements of K in a piece: a 128-byte swizzled row
-constexpr int kFewPiece = kFewRows * kFewK * 2;     // 2 KB
-constexpr int kFewStage = kFewWarps * kFewPiece;    // a piece for each warp
+constexpr int kFewK = 64;                           // elements of K in a piece
 constexpr int kFewF = kFewRows / 2;                 // f values of a gate/up tile
 
-// Ring stages, for kTiles column tiles: two blocks (one of each kernel) share an SM's 228 KB.
-template <int kTiles>
-constexpr int kFewStages = kTiles == 4 ? 5 : 6;
+// How a launch is laid out: the most column tiles, warps of a block, blocks that share an SM. A warp's ring has
+// 12 KB: four pieces with one column tile, three with two, two with three or four.
+template <int kTiles_, int kWarps_, int kBlocks_>
+struct Shape {
+    static constexpr int kTiles = kTiles_, kWarps = kWarps_, kBlocks = kBlocks_;
+    static constexpr int kThreads = 32 * kWarps;
+};
+constexpr int kFewRing = 12 * 1024;
 
 struct FewArgs {
     const __nv_bfloat16* x;
+    const __nv_bfloat16* w13;
+    const __nv_bfloat16* w2;
     const int32_t* ids;
     const void* scores;
     const void* logits;
@@ -62,45 +76,41 @@ struct FewArgs {
     bool scores_bf16, logits_bf16, normalize;
 };
 
-// The plan in shared memory: U experts, the bits of their tokens, their first slots (rows of H), and the
-// score of each slot. pairs: the arrays' capacity.
+// The plan in shared memory: U experts, the bits of their tokens, their first slots (rows of H), and each
+// slot's token and score.
 struct Plan {
     int32_t* expert;
     uint32_t* mask;
     int32_t* base;
+    int32_t* token;
     float* score;
 };
-constexpr int kPlanBytesPerPair = 16;
+constexpr int kPlanBytesPerPair = 20;
 
-struct FewBars {
-    uint64_t full[8], empty[8];
-    int abort;
-    int32_t sums[kFewWarps];
-};
-
-template <int kTiles>
-constexpr size_t few_smem_bytes(int pairs) {
-    return 1024 + kFewStages<kTiles> * kFewStage + kFewWarps * kTiles * 512 + sizeof(FewBars) +
-           static_cast<size_t>(pairs) * kPlanBytesPerPair;
-}
-
-template <int kTiles>
+// Shared memory: the warps' rings (in which the plan is made first), their sums, the plan.
+template <class S>
 struct FewSmem {
+    static constexpr int kRing = S::kWarps * kFewRing;
+    static constexpr int kSums = S::kWarps * S::kTiles * 512;
+    static_assert(kRing >= 4 * kMaxExperts + 8 * kFewMaxPairs, "room to make the plan in");
+    static_assert(S::kBlocks * (kRing + kSums + 4 * S::kWarps + kPlanBytesPerPair * 256 + 1024) <= 228 * 1024, "fits");
+    static_assert(kRing + kSums + 4 * S::kWarps + kPlanBytesPerPair * kFewMaxPairs <= 227 * 1024, "fits");
+    static size_t bytes(int pairs) {
+        return kRing + kSums + sizeof(int32_t) * S::kWarps + static_cast<size_t>(pairs) * kPlanBytesPerPair;
+    }
     uint8_t* ring;
-    float* red;  // [kFewWarps][kTiles][16][8]
-    FewBars* bars;
+    float* red;  // [kWarps][8 kTiles][16]: a warp's sums of 16 rows for each column or token
+    int32_t* sums;
     Plan plan;
-    __device__ FewSmem(uint8_t* base, int pairs) {
-        ring = base + ((1024u - (smem_addr(base) & 1023u)) & 1023u);  // the swizzle counts from 1024-byte lines
-        uint8_t* p = ring + kFewStages<kTiles> * kFewStage;
-        red = reinterpret_cast<float*>(p);
-        p += kFewWarps * kTiles * 512;
-        bars = reinterpret_cast<FewBars*>(p);
-        p += sizeof(FewBars);
-        plan.expert = reinterpret_cast<int32_t*>(p);
+    __device__ FewSmem(uint8_t* p, int pairs) {
+        ring = p;
+        red = reinterpret_cast<float*>(p + kRing);
+        sums = reinterpret_cast<int32_t*>(p + kRing + kSums);
+        plan.expert = sums + S::kWarps;
         plan.mask = reinterpret_cast<uint32_t*>(plan.expert + pairs);
         plan.base = reinterpret_cast<int32_t*>(plan.mask + pairs);
-        plan.score = reinterpret_cast<float*>(plan.base + pairs);
+        plan.token = plan.base + pairs;
+        plan.score = reinterpret_cast<float*>(plan.token + pairs);
     }
 };
 
@@ -149,17 +159,67 @@ __device__ void choose(const L* row, int32_t E, int32_t K, bool normalize, int l
     for (int k = lane; k < K; k += 32) scores[k] = m == -INFINITY ? 0.0f : scores[k] * inv;
 }
 
-// Makes the plan; returns the number of experts. scratch: the ring, before anything is loaded into it.
-template <bool kFirst>
-__device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, FewBars* bars) {
+// The plan of up to 32 pairs, by one warp with a pair to each lane, which compares itself to the others twice.
+// Returns the number of experts. scratch: 96 words.
+__device__ int plan_in_warp(int32_t id, float score, bool live, int pairs, int K, int lane, int32_t* scratch,
+                            const Plan& plan) {
+    constexpr int32_t kNone = 0x7fffffff;
+    float* scores = reinterpret_cast<float*>(scratch + 32);
+    scratch[lane] = live ? id : -1;
+    scores[lane] = score;
+    __syncwarp();
+    const int token = lane / K;
+    uint32_t mask = 0u;                        // the expert's tokens
+    bool first = live, first_of_token = live;  // nobody before names the expert, or names it for this token
+    float sum = 0.0f;                          // of a token that names an expert twice, in order
+    for (int p = 0, t = 0, k = 0; p < pairs; ++p) {
+        if (scratch[p] == id) {
+            mask |= 1u << t;
+            if (p < lane) first = false;
+            if (t == token) {
+                sum += scores[p];
+                if (p < lane) first_of_token = false;
+            }
+        }
+        if (++k == K) k = 0, ++t;
+    }
+    __syncwarp();
+    scratch[lane] = first ? id : kNone;
+    scratch[32 + lane] = first_of_token ? id : kNone;
+    __syncwarp();
+    int before = 0, base = 0;  // experts with lower ids, and their slots
+    for (int p = 0; p < pairs; ++p) {
+        before += scratch[p] < id ? 1 : 0;
+        base += scratch[32 + p] < id ? 1 : 0;
+    }
+    if (first) {
+        plan.expert[before] = id;
+        plan.mask[before] = mask;
+        plan.base[before] = base;
+    }
+    if (first_of_token) {
+        const int slot = base + __popc(mask & ((1u << token) - 1u));
+        plan.token[slot] = token;
+        plan.score[slot] = sum;
+    }
+    return __popc(__ballot_sync(0xffffffffu, first));
+}
+
+// Makes the plan; returns the number of experts. scratch: the rings, before anything is copied into them.
+template <class S, bool kFirst>
+__device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, int32_t* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pairs = a.T * a.K;
     uint32_t* table = reinterpret_cast<uint32_t*>(scratch);  // [E] the tokens of each expert
     int32_t* ids = reinterpret_cast<int32_t*>(table + a.E);  // [pairs]
     float* scores = reinterpret_cast<float*>(ids + pairs);
-    for (int e = tid; e < a.E; e += kFewThreads) table[e] = 0u;
+    auto given_score = [&](int p) {
+        return a.scores_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.scores)[p])
+                             : static_cast<const float*>(a.scores)[p];
+    };
+    const bool speaks = kFirst && blockIdx.x == 0;  // writes what the caller gets to see
     if (a.logits != nullptr) {
-        for (int t = warp; t < a.T; t += kFewWarps + 1) {
+        for (int t = warp; t < a.T; t += S::kWarps) {
             const int64_t row = static_cast<int64_t>(t) * a.E;
             if (a.logits_bf16)
                 choose(static_cast<const __nv_bfloat16*>(a.logits) + row, a.E, a.K, a.normalize, lane, ids + t * a.K,
@@ -168,30 +228,55 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, F
                 choose(static_cast<const float*>(a.logits) + row, a.E, a.K, a.normalize, lane, ids + t * a.K,
                        scores + t * a.K);
         }
-    } else {
-        for (int p = tid; p < pairs; p += kFewThreads) {
-            ids[p] = a.ids[p];
-            scores[p] = a.scores_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.scores)[p])
-                                      : static_cast<const float*>(a.scores)[p];
-        }
+        if (a.T > 1) __syncthreads();
+        else __syncwarp();
+        if (speaks && (a.T > 1 || warp == 0))
+            for (int p = a.T > 1 ? tid : lane; p < pairs; p += a.T > 1 ? S::kThreads : 32) {
+                a.ids_out[p] = ids[p];
+                a.scores_out[p] = scores[p];
+            }
     }
+    // A block's first weights wait for this. 6 pairs: 1.7 us by the whole block, 0.9 us by one warp.
+    if (pairs <= 32) {
+        if (warp == 0) {
+            int32_t id = 0;
+            float score = 0.0f;
+            if (lane < pairs) {
+                id = a.logits ? ids[lane] : a.ids[lane];
+                score = a.logits ? scores[lane] : given_score(lane);
+            }
+            const bool bad = static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.E);
+            __syncwarp();
+            const int experts = plan_in_warp(id, score, lane < pairs && !bad && score != 0.0f, pairs, a.K, lane,
+                                             reinterpret_cast<int32_t*>(scratch), plan);
+            const bool any_bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                sums[0] = experts;
+                if (speaks) *a.status = any_bad ? MOE_DEV_BAD_EXPERT_ID : 0u;
+            }
+        }
+        __syncthreads();
+        return sums[0];
+    }
+    for (int e = tid; e < a.E; e += S::kThreads) table[e] = 0u;
+    if (a.logits == nullptr)
+        for (int p = tid; p < pairs; p += S::kThreads) {
+            ids[p] = a.ids[p];
+            scores[p] = given_score(p);
+        }
     __syncthreads();
     int bad = 0;
-    for (int p = tid; p < pairs; p += kFewThreads) {
+    for (int p = tid; p < pairs; p += S::kThreads) {
         const uint32_t e = static_cast<uint32_t>(ids[p]);
         if (e >= static_cast<uint32_t>(a.E)) bad = 1;
         else if (scores[p] != 0.0f) atomicOr(&table[e], 1u << (p / a.K));
-        if (kFirst && blockIdx.x == 0 && a.logits != nullptr) {
-            a.ids_out[p] = ids[p];
-            a.scores_out[p] = scores[p];
-        }
     }
     bad = __syncthreads_or(bad);
-    if (kFirst && blockIdx.x == 0 && tid == 0) *a.status = bad ? MOE_DEV_BAD_EXPERT_ID : 0u;
+    if (speaks && tid == 0) *a.status = bad ? MOE_DEV_BAD_EXPERT_ID : 0u;
     // ascending experts; (experts, slots) are counted together, in the halves of a word
     int32_t run = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32 * kFewWarps) {
-        const uint32_t m = warp < kFewWarps && e0 + tid < a.E ? table[e0 + tid] : 0u;
+    for (int e0 = 0; e0 < a.E; e0 += S::kThreads) {
+        const uint32_t m = e0 + tid < a.E ? table[e0 + tid] : 0u;
         const int32_t own = m ? (1 << 16) + __popc(m) : 0;
         int32_t upto = own;
 #pragma unroll
@@ -199,13 +284,13 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, F
             const int32_t v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        if (warp < kFewWarps && lane == 31) bars->sums[warp] = upto;
+        if (lane == 31) sums[warp] = upto;
         __syncthreads();
         int32_t before = run + upto - own;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-            if (w < warp) before += bars->sums[w];
-            run += bars->sums[w];
+        for (int w = 0; w < S::kWarps; ++w) {
+            if (w < warp) before += sums[w];
+            run += sums[w];
         }
         if (m) {
             plan.expert[before >> 16] = e0 + tid;
@@ -215,17 +300,17 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, F
         __syncthreads();
     }
     const int experts = run >> 16;
-    for (int u = warp; u < experts; u += kFewWarps + 1) {  // a lane per token
+    for (int u = warp; u < experts; u += S::kWarps) {  // a lane per token
         const uint32_t m = plan.mask[u];
         if ((m >> lane) & 1u) {
             float s = 0.0f;
             for (int k = 0; k < a.K; ++k)
                 if (ids[lane * a.K + k] == plan.expert[u]) s += scores[lane * a.K + k];
-            plan.score[plan.base[u] + __popc(m & ((1u << lane) - 1u))] = s;
+            const int slot = plan.base[u] + __popc(m & ((1u << lane) - 1u));
+            plan.token[slot] = lane;
+            plan.score[slot] = s;
         }
     }
-    // the ring's next writer is TMA
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     return experts;
 }
@@ -239,265 +324,341 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// This lane's part of a column tile's 64 elements of K: the 16-byte units lane % 4 and lane % 4 + 4 of the
-// row of column lane / 4. The products run over K in an order of their own (step s takes words s of those
-// units), the same for weights and tokens, so both come in 16-byte loads.
-struct Column {
-    uint4 lo, hi;
-};
+// A lane's part of 64 elements of K of one row: the 16-byte units lane % 4 and lane % 4 + 4. The products run
+// over K in an order of their own (step s takes words s of those units), the same for weights and tokens, so both
+// come in 16-byte loads, two of which take a row's 128 bytes whole.
+struct Units {
+    uint32_t lo[4], hi[4];
 
-template <int kTiles>
-__device__ __forceinline__ void multiply(float (&acc)[kTiles][4], const uint8_t* piece, const Column (&b)[kTiles],
-                                         uint32_t mask, int lane) {
-    const int row = lane >> 2;
-    const uint8_t* p = piece + row * 128 + (((lane & 3) ^ row) << 4);  // rows 0-7 and 8-15 have the same swizzle
-    const uint8_t* q = piece + row * 128 + (((lane & 3) ^ row ^ 4) << 4);
-    uint32_t a0[4], a1[4], a2[4], a3[4];
-    *reinterpret_cast<uint4*>(a0) = *reinterpret_cast<const uint4*>(p);
-    *reinterpret_cast<uint4*>(a1) = *reinterpret_cast<const uint4*>(p + 1024);
-    *reinterpret_cast<uint4*>(a2) = *reinterpret_cast<const uint4*>(q);
-    *reinterpret_cast<uint4*>(a3) = *reinterpret_cast<const uint4*>(q + 1024);
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-        if (kTiles > 1 && ((mask >> (8 * j)) & 0xffu) == 0u) continue;  // none of the tile's tokens
-        const uint32_t lo[4] = {b[j].lo.x, b[j].lo.y, b[j].lo.z, b[j].lo.w};
-        const uint32_t hi[4] = {b[j].hi.x, b[j].hi.y, b[j].hi.z, b[j].hi.w};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) mma_16x8x16(acc[j], a0[s], a1[s], a2[s], a3[s], lo[s], hi[s]);
-    }
-}
-
-// Adds up the warps' 16 x 8 tiles: every warp stores its own, then sum(row, token) adds them in warp order.
-template <int kTiles>
-struct WarpTiles {
-    float* red;
-    __device__ void store(const float (&acc)[kTiles][4], int warp, int lane) {
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");  // the last tile has been read
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            float* p = red + (warp * kTiles + j) * 128 + (lane >> 2) * 8 + (lane & 3) * 2;
-            *reinterpret_cast<float2*>(p) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2*>(p + 64) = make_float2(acc[j][2], acc[j][3]);
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
-    }
-    __device__ float sum(int row, int token) const {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) s += red[(w * kTiles + token / 8) * 128 + row * 8 + token % 8];
-        return s;
+    __device__ void take(const uint8_t* lo_at, const uint8_t* hi_at) {
+        *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(lo_at);
+        *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(hi_at);
     }
 };
 
-// A place in a ring of kStages.
-template <int kStages>
-struct RingAt {
-    uint32_t s = 0, phase = 0;
-    __device__ void next() {
-        if (++s == kStages) s = 0, phase ^= 1u;
+// The weights of a piece as a lane holds them: rows lane / 4 and lane / 4 + 8.
+struct Weights {
+    Units top, bottom;
+};
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there = true) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A lane's own ring of pieces in shared memory: what it copies there it alone reads, so a wait for its own copies
+// is all the order there is to keep. Unit i of all lanes lies together, without bank conflicts.
+struct Ring {
+    uint8_t* mine;  // this lane's first unit of place 0
+    int slot;       // bytes of a piece: the weights' units, then those of its column tiles
+    int depth;      // pieces
+    int at = 0;
+    __device__ Ring(uint8_t* ring, int tiles, int warp, int lane)
+        : mine(ring + warp * kFewRing + 16 * lane), slot(2048 + 1024 * tiles), depth(tiles == 1 ? 4 : tiles == 2 ? 3 : 2) {}
+    __device__ uint32_t place(int i) const { return smem_addr(mine + i * slot); }
+    __device__ void get(Weights& w) const {
+        if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint8_t* p = mine + at * slot;
+        w.top.take(p, p + 512);
+        w.bottom.take(p + 1024, p + 1536);
+    }
+    __device__ void column(int j, Units& b) const {
+        const uint8_t* p = mine + at * slot + 2048 + 1024 * j;
+        b.take(p, p + 512);
+    }
+    __device__ void next() { at = at + 1 == depth ? 0 : at + 1; }
+};
+
+// Column tiles of the expert with the most tokens; every warp finds it for itself.
+__device__ int most_tiles(const Plan& plan, int experts, int lane) {
+    uint32_t most = 1u;
+    for (int u = lane; u < experts; u += 32) most = max(most, static_cast<uint32_t>(__popc(plan.mask[u])));
+    return static_cast<int>((__reduce_max_sync(0xffffffffu, most) + 7u) / 8u);
+}
+
+// The sums of a warp: 16 rows x 8 columns a tile. A single tile has two chains of products, so that one does
+// not wait for the other.
+template <int kTiles>
+struct Sums {
+    static constexpr int kChains = kTiles == 1 ? 2 : 1;
+    float c[kTiles][kChains][4];
+
+    __device__ void clear() {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int h = 0; h < kChains; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[j][h][i] = 0.0f;
+    }
+    // Value i of tile j: row lane / 4 + 8 (i / 2), column 8 j + 2 (lane % 4) + i % 2.
+    __device__ float value(int j, int i) const { return kChains == 2 ? c[j][0][i] + c[j][kChains - 1][i] : c[j][0][i]; }
+
+    __device__ void add(int j, const Weights& w, const Units& b) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            mma_16x8x16(c[j][s % kChains], w.top.lo[s], w.bottom.lo[s], w.top.hi[s], w.bottom.hi[s], b.lo[s], b.hi[s]);
     }
 };
 
-template <int kTiles>
-__device__ void setup(FewBars* bars, const CUtensorMap* map) {
-    if (threadIdx.x == 0) {
-        bars->abort = 0;
-        for (int s = 0; s < kFewStages<kTiles>; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], kFewWarps);
-        }
-        mbar_init_fence();
-        tma_prefetch_descriptor(map);
-    }
+// The warps' sums of a row for a column, in warp order.
+template <class S>
+__device__ __forceinline__ float sum_of_warps(const float* red, int row, int column) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < S::kWarps; ++w) s += red[(w * 8 * S::kTiles + column) * 16 + row];
+    return s;
 }
 
-// The loading warp's part of a stage: once the stage is empty, n pieces of `bytes` each, lane i issuing
-// load(i, destination). False when the wait gave up.
-template <int kTiles, class Load>
-__device__ __forceinline__ bool fill(RingAt<kFewStages<kTiles>>& at, uint8_t* ring, FewBars* bars, uint32_t* status,
-                                     int n, uint32_t bytes, int lane, Load load) {
-    int ok = 1;
-    if (lane == 0) {
-        ok = mbar_wait(&bars->empty[at.s], at.phase ^ 1u, &bars->abort, status, MOE_DEV_TIMEOUT) ? 1 : 0;
-        if (ok) mbar_arrive_expect_tx(&bars->full[at.s], n * bytes);
+// A warp's way through its block's rows of weights, `pieces` pieces to each: it takes the pieces w, w + kWarps, ...
+// of all the rows strung together, so that the warps' shares are equal however many pieces a row has. A row's
+// place (major, minor) goes on by `step` from row to row, and minor counts up to `limit`.
+struct Walk {
+    int p, row = 0, major, minor;
+    __device__ Walk(int warp, int2 start, int pieces, int2 step, int limit)
+        : p(warp), major(start.x), minor(start.y) {
+        settle(pieces, step, limit);
     }
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    if (lane < n) load(lane, ring + at.s * kFewStage + lane * kFewPiece, &bars->full[at.s]);
-    at.next();
-    return true;
-}
-
-// After a wait that gave up: the copies in flight get a moment to land before the block's memory is freed.
-template <int kTiles>
-__device__ void land(RingAt<kFewStages<kTiles>> at, uint32_t filled, FewBars* bars) {
-    constexpr uint32_t kStages = kFewStages<kTiles>;
-    const unsigned long long t0 = global_timer_ns();
-    for (uint32_t i = 0; i < kStages && i < filled; ++i) {
-        at.phase ^= at.s == 0 ? 1u : 0u;
-        at.s = at.s == 0 ? kStages - 1 : at.s - 1;
-        while (!mbar_try_wait(&bars->full[at.s], at.phase) && global_timer_ns() - t0 < 2000000ull) {
-        }
+    // Moves on from past a row's end; true in a new row.
+    __device__ bool settle(int pieces, int2 step, int limit) {
+        if (p < pieces) return false;
+        do {
+            p -= pieces;
+            ++row;
+            major += step.x;
+            minor += step.y;
+            if (minor >= limit) minor -= limit, ++major;
+        } while (p >= pieces);
+        return true;
     }
-}
+};
 
-template <int kTiles>
-__global__ void __launch_bounds__(kFewThreads, 2)
-    k_few_gate_up(const __grid_constant__ CUtensorMap w13, const FewArgs a) {
-    extern __shared__ __align__(1024) uint8_t raw[];
-    FewSmem<kTiles> sm(raw, a.T * a.K);
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_gate_up(const FewArgs a) {
+    constexpr int kTiles = S::kTiles;
+    extern __shared__ __align__(16) uint8_t raw[];
+    FewSmem<S> sm(raw, a.T * a.K);
+    const Plan& plan = sm.plan;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    setup<kTiles>(sm.bars, &w13);
     griddep_wait();
-    const int experts = make_plan<true>(a, sm.ring, sm.plan, sm.bars);
+    const int experts = make_plan<S, true>(a, sm.ring, plan, sm.sums);
     const int per_expert = a.F / kFewF, tiles = experts * per_expert, pieces = a.D / kFewK;
-    RingAt<kFewStages<kTiles>> at;
-    if (warp == kFewWarps) {
-        bool ok = true;
-        uint32_t filled = 0;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-            const int u = tile / per_expert, f = (tile - u * per_expert) * kFewF, e = sm.plan.expert[u];
-            for (int c = 0; ok && c < pieces; c += kFewWarps, ++filled)
-                ok = fill<kTiles>(at, sm.ring, sm.bars, a.status, min(kFewWarps, pieces - c), kFewPiece, lane,
-                                  [&](int i, uint8_t* to, uint64_t* bar) {
-                                      tma_load_3d(to, &w13, bar, (c + i) * kFewK, f, 2 * e);
-                                  });
-        }
-        // the last loads are on their way: the down kernel may start on its own
-        griddep_launch_dependents();
-        if (!ok && lane == 0) land<kTiles>(at, filled, sm.bars);
-        return;
-    }
-    auto columns = [&](int tile, int c, Column (&b)[kTiles]) {
-        const uint32_t mask = tile < tiles && c + warp < pieces ? sm.plan.mask[tile / per_expert] : 0u;
+    const int first = blockIdx.x, stride = gridDim.x;
+    const int rows = first < tiles ? (tiles - 1 - first) / stride + 1 : 0;  // the block's tiles
+    griddep_launch_dependents();
+    // a tile's place: expert of the plan, tile of the expert
+    const int2 start = make_int2(first / per_expert, first % per_expert);
+    const int2 step = make_int2(stride / per_expert, stride % per_expert);
+    // copies into the ring, as far ahead as it is deep
+    Walk ahead(warp, start, pieces, step, per_expert);
+    int coming = 0;  // columns of the expert whose pieces are copied
+    const __nv_bfloat16 *column[kTiles], *gate = nullptr;
+    const int64_t up = static_cast<int64_t>(a.F) * a.D;
+    auto aim = [&] {
+        if (ahead.row < rows) {
+            const int u = ahead.major;
+            coming = __popc(plan.mask[u]);
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            const int t = 8 * j + (lane >> 2);
-            b[j].lo = b[j].hi = make_uint4(0u, 0u, 0u, 0u);
-            if ((mask >> t) & 1u) {
-                const __nv_bfloat16* p = a.x + static_cast<int64_t>(t) * a.D + (c + warp) * kFewK + 8 * (lane & 3);
-                b[j].lo = __ldg(reinterpret_cast<const uint4*>(p));
-                b[j].hi = __ldg(reinterpret_cast<const uint4*>(p + 32));
+            for (int j = 0; j < kTiles; ++j) {
+                const int col = 8 * j + (lane >> 2);
+                if (j == 0 || 8 * j < coming)
+                    column[j] = a.x + (col < coming ? static_cast<int64_t>(plan.token[plan.base[u] + col]) * a.D : 0) + 8 * (lane & 3);
             }
+            gate = a.w13 + (2 * static_cast<int64_t>(plan.expert[u]) * a.F + ahead.minor * kFewF + (lane >> 2)) * a.D + 8 * (lane & 3);
         }
     };
-    WarpTiles<kTiles> meet{sm.red};
-    Column next[kTiles];
-    columns(blockIdx.x, 0, next);
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int u = tile / per_expert;
-        const uint32_t mask = sm.plan.mask[u];
-        float acc[kTiles][4] = {};
-        for (int c = 0; c < pieces; c += kFewWarps) {
-            Column b[kTiles];
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) b[j] = next[j];
-            // a stage ahead, over the end of the tile
-            if (c + kFewWarps < pieces) columns(tile, c + kFewWarps, next);
-            else columns(tile + gridDim.x, 0, next);
-            mbar_wait(&sm.bars->full[at.s], at.phase, &sm.bars->abort, a.status, MOE_DEV_TIMEOUT);
-            if (c + warp < pieces)
-                multiply<kTiles>(acc, sm.ring + at.s * kFewStage + warp * kFewPiece, b, mask, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.bars->empty[at.s]);
-            at.next();
-        }
-        meet.store(acc, warp, lane);
-        const int f = threadIdx.x & 7, t = threadIdx.x >> 3;
-        if (t < 8 * kTiles && ((mask >> t) & 1u)) {
-            const float g = meet.sum(f, t), up = meet.sum(f + 8, t);
-            const int64_t slot = sm.plan.base[u] + __popc(mask & ((1u << t) - 1u));
-            // H is rounded to bf16 here, as the large forward's
-            a.h[slot * a.F + (tile - u * per_expert) * kFewF + f] = __float2bfloat16_rn(g / (1.0f + __expf(-g)) * up);
-        }
-    }
-}
-
-template <int kTiles>
-__global__ void __launch_bounds__(kFewThreads, 2)
-    k_few_down(const __grid_constant__ CUtensorMap w2, const FewArgs a) {
-    extern __shared__ __align__(1024) uint8_t raw[];
-    FewSmem<kTiles> sm(raw, a.T * a.K);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    setup<kTiles>(sm.bars, &w2);
-    // Before griddep_wait(): ids, scores and logits were written by kernels that had completed when the gate/up
-    // kernel passed its own wait, and it lets this one start only after that; nobody writes the weights.
-    const int experts = make_plan<false>(a, sm.ring, sm.plan, sm.bars);
-    const int tiles = (a.D + a.rows - 1) / a.rows, pieces = a.F / kFewK;
-    RingAt<kFewStages<kTiles>> at;
-    if (warp == kFewWarps) {
-        bool ok = true;
-        uint32_t filled = 0;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-            for (int u = 0; ok && u < experts; ++u) {
-                const int row = sm.plan.expert[u] * a.D + tile * a.rows;
-                for (int c = 0; ok && c < pieces; c += kFewWarps, ++filled)
-                    ok = fill<kTiles>(at, sm.ring, sm.bars, a.status, min(kFewWarps, pieces - c),
-                                      a.rows * kFewK * 2, lane, [&](int i, uint8_t* to, uint64_t* bar) {
-                                          tma_load_2d(to, &w2, bar, (c + i) * kFewK, row);
-                                      });
-            }
-        griddep_launch_dependents();
-        griddep_wait();
-        if (!ok && lane == 0) land<kTiles>(at, filled, sm.bars);
-        return;
-    }
-    griddep_wait();  // H
-    auto columns = [&](int u, int c, Column (&b)[kTiles]) {
-        const bool live = u < experts && c + warp < pieces;
-        const uint32_t mask = live ? sm.plan.mask[u] : 0u;
-        const int64_t base = live ? sm.plan.base[u] : 0;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            const int t = 8 * j + (lane >> 2);
-            b[j].lo = b[j].hi = make_uint4(0u, 0u, 0u, 0u);
-            if ((mask >> t) & 1u) {
-                const __nv_bfloat16* p =
-                    a.h + (base + __popc(mask & ((1u << t) - 1u))) * a.F + (c + warp) * kFewK + 8 * (lane & 3);
-                b[j].lo = __ldcg(reinterpret_cast<const uint4*>(p));
-                b[j].hi = __ldcg(reinterpret_cast<const uint4*>(p + 32));
-            }
-        }
-    };
-    WarpTiles<kTiles> meet{sm.red};
-    Column next[kTiles];
-    columns(0, 0, next);
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        float total[kTiles][4] = {};
-        for (int u = 0; u < experts; ++u) {
-            const uint32_t mask = sm.plan.mask[u];
-            float acc[kTiles][4] = {};
-            for (int c = 0; c < pieces; c += kFewWarps) {
-                Column b[kTiles];
-#pragma unroll
-                for (int j = 0; j < kTiles; ++j) b[j] = next[j];
-                if (c + kFewWarps < pieces) columns(u, c + kFewWarps, next);
-                else columns(u + 1 < experts ? u + 1 : 0, 0, next);  // the next expert, or the next tile's first
-                mbar_wait(&sm.bars->full[at.s], at.phase, &sm.bars->abort, a.status, MOE_DEV_TIMEOUT);
-                if (c + warp < pieces)
-                    multiply<kTiles>(acc, sm.ring + at.s * kFewStage + warp * kFewPiece, b, mask, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.bars->empty[at.s]);
-                at.next();
-            }
-            // only tokens of this expert: another's column is 0 times weights that need not be finite
+    auto load = [&](uint32_t to) {
+        if (ahead.row < rows) {
+            const int k = ahead.p * kFewK;
+            copy16(to, gate + k);
+            copy16(to + 512, gate + k + 32);
+            copy16(to + 1024, gate + up + k);
+            copy16(to + 1536, gate + up + k + 32);
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
+                if (j == 0 || 8 * j < coming) {
+                    const bool on = 8 * j + (lane >> 2) < coming;
+                    copy16(to + 2048 + 1024 * j, column[j] + k, on);
+                    copy16(to + 2560 + 1024 * j, column[j] + k + 32, on);
+                }
+            ahead.p += S::kWarps;
+            if (ahead.settle(pieces, step, per_expert)) aim();
+        }
+        copy_group();
+    };
+    Ring ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < ring.depth; ++i) load(ring.place(i));
+    Walk now(warp, start, pieces, step, per_expert);
+    Sums<kTiles> acc;
+    for (int row = 0; row < rows; ++row) {
+        const int tile = first + row * stride, u = tile / per_expert;
+        const int count = __popc(plan.mask[u]), base = plan.base[u];
+        acc.clear();
+        while (now.row == row) {
+            Weights w;
+            ring.get(w);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = 8 * j + 2 * (lane & 3) + i;
-                    if ((mask >> t) & 1u) {
-                        const float s = sm.plan.score[sm.plan.base[u] + __popc(mask & ((1u << t) - 1u))];
-                        total[j][i] = fmaf(s, acc[j][i], total[j][i]);
-                        total[j][2 + i] = fmaf(s, acc[j][2 + i], total[j][2 + i]);
-                    }
+            for (int j = 0; j < kTiles; ++j)
+                if (j == 0 || 8 * j < count) {
+                    Units b;
+                    ring.column(j, b);
+                    acc.add(j, w, b);
+                }
+            load(ring.place(ring.at));
+            ring.next();
+            now.p += S::kWarps;
+            now.settle(pieces, step, per_expert);
+        }
+        // the warps' sums meet
+        if (row > 0) __syncthreads();  // the last tile's have been read
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sm.red[((warp * kTiles + j) * 8 + 2 * (lane & 3) + (i & 1)) * 16 + (lane >> 2) + 8 * (i >> 1)] = acc.value(j, i);
+        __syncthreads();
+        for (int o = threadIdx.x; o < kFewF * count; o += S::kThreads) {
+            const int f = o & 7, col = o >> 3;
+            const float g = sum_of_warps<S>(sm.red, f, col), v = sum_of_warps<S>(sm.red, f + 8, col);
+            // H is rounded to bf16 here, as the large forward's
+            a.h[static_cast<int64_t>(base + col) * a.F + (tile - u * per_expert) * kFewF + f] =
+                __float2bfloat16_rn(g / (1.0f + __expf(-g)) * v);
+        }
+    }
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewArgs a) {
+    constexpr int kTiles = S::kTiles;
+    extern __shared__ __align__(16) uint8_t raw[];
+    FewSmem<S> sm(raw, a.T * a.K);
+    const Plan& plan = sm.plan;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // Before griddep_wait(): ids, scores and logits were written by kernels that had completed when the gate/up
+    // kernel passed its own wait, and it lets this one start only after that; nobody writes the weights.
+    const int experts = make_plan<S, false>(a, sm.ring, plan, sm.sums);
+    const int tiles = (a.D + a.rows - 1) / a.rows, pieces = a.F / kFewK;
+    const int first = blockIdx.x, stride = gridDim.x;
+    const int mine = first < tiles ? (tiles - 1 - first) / stride + 1 : 0;  // the block's tiles
+    const int rows = mine * experts;                                        // and their rows of each expert
+    // a row's place: the block's tile, expert of the plan
+    const int2 start = make_int2(0, 0), step = make_int2(0, 1);
+    Walk ahead(warp, start, pieces, step, experts);
+    int coming = 0;
+    bool has_top = false, has_bottom = false;
+    const __nv_bfloat16 *column = nullptr, *down = nullptr;
+    auto aim = [&] {
+        if (ahead.row < rows) {
+            const int u = ahead.minor, d = (first + ahead.major * stride) * a.rows;
+            const int end = min(a.rows, a.D - d);
+            coming = __popc(plan.mask[u]);
+            column = a.h + static_cast<int64_t>(plan.base[u]) * a.F + 8 * (lane & 3);
+            has_top = (lane >> 2) < end;
+            has_bottom = (lane >> 2) + 8 < end;
+            down = a.w2 + (static_cast<int64_t>(plan.expert[u]) * a.D + d + (has_top ? lane >> 2 : 0)) * a.F + 8 * (lane & 3);
+        }
+    };
+    auto load_weights = [&](uint32_t to) {
+        if (ahead.row >= rows) return;
+        const __nv_bfloat16* p = down + ahead.p * kFewK;
+        const __nv_bfloat16* q = has_bottom ? p + 8 * static_cast<int64_t>(a.F) : p;
+        copy16(to, p, has_top);
+        copy16(to + 512, p + 32, has_top);
+        copy16(to + 1024, q, has_bottom);
+        copy16(to + 1536, q + 32, has_bottom);
+    };
+    auto load_columns = [&](uint32_t to) {
+        if (ahead.row < rows) {
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+                if (j == 0 || 8 * j < coming) {
+                    const int col = 8 * j + (lane >> 2);
+                    const bool on = col < coming;
+                    const __nv_bfloat16* p = column + (on ? static_cast<int64_t>(col) * a.F : 0) + ahead.p * kFewK;
+                    copy16(to + 2048 + 1024 * j, p, on);
+                    copy16(to + 2560 + 1024 * j, p + 32, on);
                 }
         }
-        meet.store(total, warp, lane);
-        for (int o = threadIdx.x; o < 128 * kTiles; o += 32 * kFewWarps) {
+        copy_group();
+    };
+    auto move_on = [&] {
+        ahead.p += S::kWarps;
+        if (ahead.settle(pieces, step, experts)) aim();
+    };
+    Ring ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
+    const Walk begin = ahead;
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < ring.depth; ++i) {
+        load_weights(ring.place(i));
+        move_on();
+    }
+    griddep_wait();  // H
+    griddep_launch_dependents();
+    ahead = begin;
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < ring.depth; ++i) {
+        load_columns(ring.place(i));
+        move_on();
+    }
+    Walk now(warp, start, pieces, step, experts);
+    float* own = sm.red + warp * 128 * kTiles;  // [token][16]
+    Sums<kTiles> acc;
+    int row = 0;
+    for (int tile = first; tile < tiles; tile += stride) {
+#pragma unroll
+        for (int i = 0; i < 4 * kTiles; ++i) own[32 * i + lane] = 0.0f;
+        for (int u = 0; u < experts; ++u, ++row) {
+            const int count = __popc(plan.mask[u]), base = plan.base[u];
+            acc.clear();
+            while (now.row == row) {
+                Weights w;
+                ring.get(w);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+                    if (j == 0 || 8 * j < count) {
+                        Units b;
+                        ring.column(j, b);
+                        acc.add(j, w, b);
+                    }
+                const uint32_t to = ring.place(ring.at);
+                load_weights(to);
+                load_columns(to);
+                if (ahead.row < rows) move_on();
+                ring.next();
+                now.p += S::kWarps;
+                now.settle(pieces, step, experts);
+            }
+            __syncwarp();  // a token's sums belong to another lane with another expert
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                if (j > 0 && 8 * j >= count) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = 8 * j + 2 * (lane & 3) + i;
+                    if (col < count) {
+                        float* t = own + plan.token[base + col] * 16 + (lane >> 2);
+                        const float s = plan.score[base + col];
+                        t[0] = fmaf(s, acc.value(j, i), t[0]);
+                        t[8] = fmaf(s, acc.value(j, 2 + i), t[8]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        for (int o = threadIdx.x; o < 128 * kTiles; o += S::kThreads) {
             const int r = o & 15, t = o >> 4, d = tile * a.rows + r;
             if (r < a.rows && d < a.D && t < a.T)
-                a.out[static_cast<int64_t>(t) * a.D + d] = __float2bfloat16_rn(meet.sum(r, t));
+                a.out[static_cast<int64_t>(t) * a.D + d] = __float2bfloat16_rn(sum_of_warps<S>(sm.red, r, t));
         }
+        __syncthreads();
     }
 }
 
@@ -509,22 +670,26 @@ cudaError_t allow_smem() {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
     if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
-template <int kTiles>
-moe_status_t run(const CUtensorMap& w13, const CUtensorMap& w2, const FewArgs& a, int sm_count, cudaStream_t stream) {
-    if (allow_smem<&k_few_gate_up<kTiles>>() != cudaSuccess || allow_smem<&k_few_down<kTiles>>() != cudaSuccess)
+template <class S>
+moe_status_t run(FewArgs& a, int blocks, cudaStream_t stream) {
+    if (allow_smem<&k_few_gate_up<S>>() != cudaSuccess || allow_smem<&k_few_down<S>>() != cudaSuccess)
         return MOE_ERR_CUDA;
     const int pairs = a.T * a.K;
-    const size_t smem = few_smem_bytes<kTiles>(pairs);
+    const size_t smem = FewSmem<S>::bytes(pairs);
+    // Down tiles of equal height, as many as fill whole rounds of the SMs: D = 2048 makes 147 tiles of 14 rows for
+    // 152 SMs, where tiles of 16 would leave 24 SMs without one.
+    const int rounds = static_cast<int>(ceil_div(a.D, static_cast<int64_t>(kFewRows) * blocks));
+    a.rows = static_cast<int>(ceil_div(a.D, static_cast<int64_t>(rounds) * blocks));
     const int64_t most = static_cast<int64_t>(std::min(pairs, a.E)) * (a.F / kFewF);
     const int down = (a.D + a.rows - 1) / a.rows;
-    if (launch_pdl(k_few_gate_up<kTiles>, dim3(sm_count_grid(most, sm_count)), dim3(kFewThreads), smem, stream, w13, a) !=
+    if (launch_pdl(k_few_gate_up<S>, dim3(sm_count_grid(most, blocks)), dim3(S::kThreads), smem, stream, a) !=
             cudaSuccess ||
-        launch_pdl(k_few_down<kTiles>, dim3(sm_count_grid(down, sm_count)), dim3(kFewThreads), smem, stream, w2, a) !=
+        launch_pdl(k_few_down<S>, dim3(sm_count_grid(down, blocks)), dim3(S::kThreads), smem, stream, a) !=
             cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
@@ -551,19 +716,17 @@ moe_status_t launch_few(const FewProblem& p, cudaStream_t stream) {
     a.F = p.F;
     a.E = p.E;
     a.K = p.K;
-    // Down tiles of equal height, as many as fill whole rounds of the SMs: D = 2048 makes 147 tiles of 14 rows for
-    // 152 SMs, where tiles of 16 would leave 24 SMs without one.
-    const int rounds = static_cast<int>(ceil_div(p.D, static_cast<int64_t>(kFewRows) * p.sm_count));
-    a.rows = static_cast<int>(ceil_div(p.D, static_cast<int64_t>(rounds) * p.sm_count));
-    CUtensorMap w13, w2;
-    if (!make_tmap_pairs(&w13, p.w13, static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.F),
-                         static_cast<uint64_t>(p.E) * 2, kFewK, kFewF) ||
-        !make_tmap(&w2, p.w2, static_cast<uint64_t>(p.F), static_cast<uint64_t>(p.E) * p.D, kFewK,
-                   static_cast<uint32_t>(a.rows)))
-        return MOE_ERR_CUDA;
-    if (p.T <= 8) return run<1>(w13, w2, a, p.sm_count, stream);
-    if (p.T <= 16) return run<2>(w13, w2, a, p.sm_count, stream);
-    return run<4>(w13, w2, a, p.sm_count, stream);
+    a.w13 = static_cast<const __nv_bfloat16*>(p.w13);
+    a.w2 = static_cast<const __nv_bfloat16*>(p.w2);
+    // Two blocks to an SM keep more loads in flight: 8 x 4096 x 1536, 64 experts 235 us, against 250 with one. One
+    // to an SM where the down kernel has no more than one full tile for each (D <= 16 SMs): its tiles would be cut
+    // in half for two, and with one block of each kernel on an SM the down kernel is there and has its first
+    // weights before the gate/up kernel ends (1 x 2048 x 1408, 6 experts: 24.1 us, against 26.2 with two; 4 x 2048:
+    // 65.7 and 71.2).
+    const int blocks = (p.D <= kFewRows * p.sm_count ? 1 : 2) * p.sm_count;
+    if (p.T <= 8) return run<Shape<1, 8, 2>>(a, blocks, stream);
+    if (p.T <= 16) return run<Shape<2, 8, 2>>(a, blocks, stream);
+    return run<Shape<4, 7, 2>>(a, blocks, stream);
 }
 
 }  // namespace moe
