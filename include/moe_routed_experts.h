@@ -71,7 +71,7 @@ enum {
 /* Dtype of topk_scores. */
 enum { MOE_SCORES_F32 = 0, MOE_SCORES_BF16 = 1 };
 
-/* Element types of the layer norm and router entry points. */
+/* Element types of the norms', the router's and the sampling entry points. */
 enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 };
 
 /* Regions of the forward workspace, for moe_workspace_layout. */
@@ -585,6 +585,56 @@ moe_status_t moe_layernorm_bwd(const void *dy, const void *x, const void *gamma,
                                const float *rstd, int32_t dtype, int32_t param_dtype, void *dx, void *dgamma,
                                void *dbeta, int64_t T, int32_t D, void *workspace, size_t workspace_bytes,
                                moe_stream_t stream);
+
+/*
+ * The norms after and before a block, with the block's gate and the residual's scale, in one pass:
+ *   u      = block post_rstd post_gamma,  post_rstd = 1 / sqrt(sum_d block^2 / D + eps)
+ *   stream = residual_scale residual + gate u
+ *   normed = stream pre_rstd pre_gamma,   pre_rstd = 1 / sqrt(sum_d stream^2 / D + eps)
+ *   block, residual      device [T,D] of `dtype` (MOE_DTYPE_*): a block's output, and the residual stream before it
+ *   stream_out, normed   device [T,D] of `dtype`: the stream after the block, and the next block's input. Either may
+ *                        be block or residual itself (not both the same)
+ *   post_rstd            device fp32 [T], kept for the backward pass; NULL = no norm after the block (u = block),
+ *                        and then post_gamma has to be NULL
+ *   pre_rstd             device fp32 [T], kept for the backward pass
+ *   post_gamma, pre_gamma  device [D] of `param_dtype`; NULL = 1
+ *   gate                 device [D] of `param_dtype` (gate_per_token = 0) or [T,D] of `dtype` (otherwise; not
+ *                        stream_out or normed); NULL = 1
+ * eps >= 0, residual_scale finite, 1 <= D <= 2^24, T < 2^31; pointers aligned to their element type. Arithmetic in
+ * fp32; normed is of the stream before its rounding, and each output is rounded once.
+ */
+moe_status_t moe_block_norm_fwd(const void *block, const void *residual, const void *post_gamma, const void *gate,
+                                int32_t gate_per_token, const void *pre_gamma, int32_t dtype, int32_t param_dtype,
+                                float residual_scale, float eps, void *stream_out, void *normed, float *post_rstd,
+                                float *pre_rstd, int64_t T, int32_t D, moe_stream_t stream);
+
+/* Bytes of workspace moe_block_norm_bwd needs (0 for T = 0 or sizes outside the limits). Pure arithmetic. */
+size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int32_t D);
+
+/*
+ * Its backward pass. With hat = stream pre_rstd, bh = block post_rstd and g = dnormed pre_gamma:
+ *   da = dstream + pre_rstd (g - hat mean_d(g hat)),  dresidual = residual_scale da
+ *   gb = da gate post_gamma,  dblock = post_rstd (gb - bh mean_d(gb bh))   (no norm after the block: da gate)
+ *   dpre_gamma = sum_t dnormed hat,  dpost_gamma = sum_t da gate bh
+ *   dgate = da bh post_gamma, for a channel gate summed over t
+ *   dstream              device [T,D] of `dtype`: the gradient of stream_out from elsewhere; NULL = 0
+ *   dnormed              device [T,D] of `dtype`
+ *   stream_in            device [T,D]: stream_out of the forward call
+ *   block                as there; may be NULL without a gate and a norm after the block (it is not read then)
+ *   post_rstd, pre_rstd  of the forward call; post_rstd NULL = no norm after the block
+ *   dblock, dresidual    device [T,D] of `dtype`; they may be two different ones of dstream, dnormed, block, stream_in
+ *   dpost_gamma, dpre_gamma  device [D] of `param_dtype`, written in full; NULL = not computed
+ *   dgate                as gate; NULL = not computed
+ *   workspace            device, moe_block_norm_bwd_workspace_bytes(T, D) bytes, 256-byte aligned; may be NULL when
+ *                        no gradient of a [D] parameter is asked for. It holds no status word.
+ * Sums in fp32, in a fixed order. T = 0 writes zero parameter gradients.
+ */
+moe_status_t moe_block_norm_bwd(const void *dstream, const void *dnormed, const void *block, const void *stream_in,
+                                const void *post_gamma, const void *gate, int32_t gate_per_token, const void *pre_gamma,
+                                const float *post_rstd, const float *pre_rstd, int32_t dtype, int32_t param_dtype,
+                                float residual_scale, void *dblock, void *dresidual, void *dpost_gamma, void *dgate,
+                                void *dpre_gamma, int64_t T, int32_t D, void *workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
 
 /*
  * The router's choice: for each row of logits [T,E], the K largest, largest first and equal ones by

@@ -39,6 +39,9 @@ __all__ = [
     "moe_layernorm_fwd",
     "moe_layernorm_bwd_workspace_bytes",
     "moe_layernorm_bwd",
+    "moe_block_norm_fwd",
+    "moe_block_norm_bwd_workspace_bytes",
+    "moe_block_norm_bwd",
     "moe_router_topk_fwd",
     "moe_router_topk_bwd",
     "moe_lm_workspace_bytes",

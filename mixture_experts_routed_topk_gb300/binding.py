@@ -125,6 +125,13 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 [vp, vp, vp, vp, ctypes.c_float, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
             "moe_lm_distill_bwd": (
                 [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_block_norm_fwd": (
+                [vp, vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, i64, i32, vp],
+                ctypes.c_int),
+            "moe_block_norm_bwd_workspace_bytes": ([i64, i32], sz),
+            "moe_block_norm_bwd": (
+                [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, i64, i32, vp,
+                 sz, vp], ctypes.c_int),
             "moe_few_workspace_bytes": ([i64, i32, i32, i32, i32], sz),
             "moe_routed_experts_fwd_few": (
                 [vp, vp, vp, i32, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
@@ -612,7 +619,7 @@ def moe_fwd_nvfp4_stages(x, topk_ids, topk_scores, w13_nv, w2_nv, out, workspace
         int(stage_end), _ptr(workspace), workspace.numel(), _stream_handle(stream)))
 
 
-# ------------------------------------------------- layer norm, router and vocabulary losses
+# ------------------------------------- layer norm, norms around a block, router and vocabulary losses
 #
 # These calls are short on the GPU (a few microseconds at the smallest sizes), so their checks are too:
 # one comparison per property and tensor, and the words for a refusal only once it is one.
@@ -717,6 +724,64 @@ def moe_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, st
         _operand(rstd, "rstd", torch.float32, (T,), dev), MOE_DTYPE[x.dtype], pd,
         _operand(dx, "dx", x.dtype, (T, D), dev), pdg, pdb, T, D, 0 if workspace is None else _workspace(workspace, dev),
         0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
+
+
+def _gate(gate, x, T: int, D: int, device: int):
+    """Whether the gate is one per token ([T,D] of x's dtype; else [D] of the parameters' or None), and its pointer."""
+    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        return 1, _operand(gate, "gate", x.dtype, (T, D), device)
+    return 0, 0
+
+
+def _optional(t, name: str, dtype, shape, device: int) -> int:
+    return 0 if t is None else _operand(t, name, dtype, shape, device)
+
+
+def moe_block_norm_fwd(block, residual, post_gamma, gate, pre_gamma, stream_out, normed, post_rstd, pre_rstd,
+                       residual_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """The RMS norms after and before a block, its gate and the residual's scale, in one pass over rows [T,D] (fp32,
+    bf16 or fp16): stream_out = residual_scale residual + gate rms(block) post_gamma, normed = rms(stream_out) pre_gamma.
+    post_rstd and pre_rstd [T] fp32 are kept for the backward pass; post_rstd None: no norm after the block. The gammas
+    and a gate [D] (each may be None: 1) have one dtype of their own; a gate [T,D] has the rows'."""
+    T, D, dev, pb = _rows(block, "block", MOE_DTYPE)
+    per_token, pg = _gate(gate, block, T, D, dev)
+    pd, (pp, pc, pn) = _norm_params(block, D, dev, ("post_gamma", post_gamma), ("gate", None if per_token else gate),
+                                    ("pre_gamma", pre_gamma))
+    dt, f32 = block.dtype, torch.float32
+    _check("moe_block_norm_fwd", load().moe_block_norm_fwd(
+        pb, _operand(residual, "residual", dt, (T, D), dev), pp, pg or pc, per_token, pn, MOE_DTYPE[dt], pd,
+        float(residual_scale), float(eps), _operand(stream_out, "stream_out", dt, (T, D), dev),
+        _operand(normed, "normed", dt, (T, D), dev), _optional(post_rstd, "post_rstd", f32, (T,), dev),
+        _operand(pre_rstd, "pre_rstd", f32, (T,), dev), T, D, _stream_of(stream, dev)))
+
+
+def moe_block_norm_bwd_workspace_bytes(T: int, D: int) -> int:
+    return int(load().moe_block_norm_bwd_workspace_bytes(T, D)) if D <= _INT32_MAX else 0
+
+
+def moe_block_norm_bwd(dstream, dnormed, block, stream_in, post_gamma, gate, pre_gamma, post_rstd, pre_rstd, dblock,
+                       dresidual, dpost_gamma, dgate, dpre_gamma, workspace, residual_scale: float = 1.0,
+                       stream=None) -> None:
+    """The way back of moe_block_norm_fwd: dblock and dresidual [T,D], and dpost_gamma, dgate and dpre_gamma (each may
+    be None), for the gradients dstream (None: 0) and dnormed of its outputs. stream_in is its stream_out; block may be
+    None without a gate and a norm after the block. The workspace is moe_block_norm_bwd_workspace_bytes(T, D) bytes
+    (None when no gradient of a [D] parameter is asked for)."""
+    T, D, dev, pdn = _rows(dnormed, "dnormed", MOE_DTYPE)
+    per_token, pg = _gate(gate, dnormed, T, D, dev)
+    pd, (pp, pc, pn, pdp, pdc, pdpre) = _norm_params(
+        dnormed, D, dev, ("post_gamma", post_gamma), ("gate", None if per_token else gate), ("pre_gamma", pre_gamma),
+        ("dpost_gamma", dpost_gamma), ("dgate", None if per_token else dgate), ("dpre_gamma", dpre_gamma))
+    dt, f32 = dnormed.dtype, torch.float32
+    if per_token:
+        pdc = _optional(dgate, "dgate", dt, (T, D), dev)
+    _check("moe_block_norm_bwd", load().moe_block_norm_bwd(
+        _optional(dstream, "dstream", dt, (T, D), dev), pdn, _optional(block, "block", dt, (T, D), dev),
+        _operand(stream_in, "stream_in", dt, (T, D), dev), pp, pg or pc, per_token, pn,
+        _optional(post_rstd, "post_rstd", f32, (T,), dev), _operand(pre_rstd, "pre_rstd", f32, (T,), dev),
+        MOE_DTYPE[dt], pd, float(residual_scale), _operand(dblock, "dblock", dt, (T, D), dev),
+        _operand(dresidual, "dresidual", dt, (T, D), dev), pdp, pdc, pdpre, T, D,
+        0 if workspace is None else _workspace(workspace, dev), 0 if workspace is None else workspace.numel(),
+        _stream_of(stream, dev)))
 
 
 _LOGIT_DTYPES = (torch.float32, torch.bfloat16)

@@ -29,133 +29,12 @@
 // of the first loads and of four rounds decides. Long rows, bf16 4096 x 16384: 90 us forward, and 712 us
 // backward, whose column sums go through global memory for every row (39 and 59 us at the copy rate).
 #include <algorithm>
-#include <atomic>
 
-#include "ptx_sm103.cuh"
-#include "train_internal.cuh"
+#include "row_ring.cuh"
 
 namespace moe {
 namespace {
 
-template <typename T, int kVec>
-struct alignas(sizeof(T) * kVec) Pack {
-    T v[kVec];
-};
-
-// gamma or beta: their type and whether 16-byte loads of them are aligned, or null.
-struct Param {
-    const void* p;
-    int32_t dtype;
-    bool vec;
-};
-
-template <typename P, int kVec>
-__device__ __forceinline__ void load_param_as(const void* base, bool vec, int j, float (&out)[kVec]) {
-    const P* p = static_cast<const P*>(base) + j;
-    if (kVec > 1 && vec) {
-        constexpr int kStep = kVec > 1 ? (16 / sizeof(P) < kVec ? 16 / sizeof(P) : kVec) : 1;
-#pragma unroll
-        for (int e = 0; e < kVec; e += kStep) {
-            const auto q = *reinterpret_cast<const Pack<P, kStep>*>(p + e);
-#pragma unroll
-            for (int i = 0; i < kStep; ++i) out[e + i] = to_float(q.v[i]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) out[e] = to_float(p[e]);
-    }
-}
-
-template <int kVec>
-__device__ __forceinline__ void load_param(const Param& a, int j, float none, float (&out)[kVec]) {
-    if (a.p == nullptr) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) out[e] = none;
-    } else if (a.dtype == MOE_DTYPE_F32) {
-        load_param_as<float, kVec>(a.p, a.vec, j, out);
-    } else if (a.dtype == MOE_DTYPE_BF16) {
-        load_param_as<__nv_bfloat16, kVec>(a.p, a.vec, j, out);
-    } else {
-        load_param_as<__half, kVec>(a.p, a.vec, j, out);
-    }
-}
-
-__device__ __forceinline__ void store_param(void* p, int32_t dtype, int64_t j, float v) {
-    if (dtype == MOE_DTYPE_F32) static_cast<float*>(p)[j] = v;
-    else if (dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(p)[j] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[j] = __float2half_rn(v);
-}
-
-constexpr int kLnThreads = 512;
-constexpr int kLnN = 16;  // elements of a row per thread
-
-__device__ __forceinline__ void group_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Sums of kN (2 or 4) values over the kGroup threads of a row; every thread of the group gets them.
-// Lanes trade halves of the values as they add, so that after log2(kN) steps a lane carries one value:
-// 5 or 6 shuffles for what would take 10 or 20. Each group has a named barrier; the two buffers
-// alternate, so that one barrier per sum is enough: a warp writes buffer b again only after the barrier
-// of the sum in between, which every reader has passed.
-template <int kGroup, int kN>
-struct GroupSum {
-    static_assert(kN == 2 || kN == 4, "values");
-    static constexpr int kSpan = 32 / kN;  // lanes that end up with the same value
-    float (*buf)[kN][kLnThreads / 32];
-    int turn = 0;
-
-    __device__ void operator()(float (&v)[kN]) {
-        const int lane = threadIdx.x & 31;
-        float t;
-        {
-            const bool up = lane & 16;
-            if constexpr (kN == 4) {
-                float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
-                a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
-                b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
-                const bool second = lane & 8;
-                t = (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, 8);
-            } else {
-                t = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
-            }
-        }
-#pragma unroll
-        for (int o = kSpan / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if constexpr (kGroup > 32) {
-            constexpr int kWarps = kGroup / 32;
-            const int group = threadIdx.x / kGroup, first = group * kWarps;
-            float(&b)[kN][kLnThreads / 32] = buf[turn];
-            turn ^= 1;
-            if (lane % kSpan == 0) b[lane / kSpan][threadIdx.x >> 5] = t;
-            group_barrier(1 + group, kGroup);
-            // lane l adds value l / kSpan over the warps l % kSpan, l % kSpan + kSpan, ...
-            t = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; w += kSpan)
-                if (w + lane % kSpan < kWarps) t += b[lane / kSpan][first + w + lane % kSpan];
-#pragma unroll
-            for (int o = kSpan / 2; o > 0; o >>= 1)
-                if (o < kWarps) t += __shfl_xor_sync(0xffffffffu, t, o);
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * kSpan);
-    }
-};
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-
-// One tensor's share of a ring stage: kLnThreads x kLnN elements, and 16 bytes more for each of up to 16
-// rows, whose covering pieces may begin before and end after them.
-template <typename T>
-constexpr int kTensorBytes = kLnThreads * kLnN * static_cast<int>(sizeof(T)) + 256;
 // Rows a group takes through its sums together, and rows in the ring: with two at a time, those two, the
 // two being fetched into the places of the last two, and the ones in between. Some 50 KB in flight hide
 // the memory's latency at full rate; the ring takes up to 200 KB of an SM's shared memory. fp32 rows of
@@ -166,72 +45,6 @@ template <typename T, bool kBackward>
 constexpr int kLnStages = kBackward ? (sizeof(T) == 4 ? 3 : 6) : (sizeof(T) == 4 ? 6 : 10);
 template <typename T, bool kBackward>
 constexpr int kLnSmemBytes = kLnStages<T, kBackward> * (kBackward ? 2 : 1) * kTensorBytes<T>;
-
-// The covering pieces of one group's row.
-template <typename T, int kGroup>
-constexpr int kPiecesBytes = kGroup * kLnN * static_cast<int>(sizeof(T)) + 16;
-
-// A row as a group's threads see it in shared memory: element (i, e) of thread `lane` is element
-// index(i, e) of the row.
-template <typename T, int kGroup, bool kAligned>
-struct Row {
-    static constexpr int kVec = kAligned ? 16 / static_cast<int>(sizeof(T)) : 1;
-    static constexpr int kVecs = kLnN / kVec;
-
-    __device__ static int index(int i, int lane) { return (i * kGroup + lane) * kVec; }
-
-    // Starts the copies of row `row` of the tensor [rows, D] at base into this tensor's part of a stage.
-    __device__ static void fetch(uint8_t* part, const T* base, int64_t row, int64_t rows, int32_t D, int lane) {
-        if constexpr (kAligned) {
-            const T* src = base + row * D;
-            uint8_t* dst = part + 16 * static_cast<int>(threadIdx.x);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-                if (index(i, lane) < D) copy_async16(dst + i * kLnThreads * 16, src + index(i, lane));
-        } else {
-            const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
-            const uintptr_t hi = lo + static_cast<uintptr_t>(rows) * D * sizeof(T);
-            const uintptr_t begin = lo + static_cast<uintptr_t>(row) * D * sizeof(T);
-            const uintptr_t first = begin & ~static_cast<uintptr_t>(15);
-            const int pieces = static_cast<int>((begin + D * sizeof(T) + 15 - first) / 16);
-            uint8_t* dst = part + (threadIdx.x / kGroup) * kPiecesBytes<T, kGroup>;
-            for (int c = lane; c < pieces; c += kGroup) {
-                const uintptr_t at = first + 16 * static_cast<uintptr_t>(c);
-                if (at >= lo && at + 16 <= hi) {
-                    copy_async16(dst + 16 * c, reinterpret_cast<const void*>(at));
-                } else {  // the tensor's own first and last piece: only the elements inside it
-                    for (uintptr_t a = at < lo ? lo : at; a < at + 16 && a < hi; a += sizeof(T))
-                        *reinterpret_cast<T*>(dst + 16 * c + (a - at)) = *reinterpret_cast<const T*>(a);
-                }
-            }
-        }
-    }
-
-    // Vector i of this thread's part of the row (index(i, lane) < D).
-    __device__ static Pack<T, kVec> get(const uint8_t* part, const T* base, int64_t row, int32_t D, int i, int lane) {
-        if constexpr (kAligned) {
-            return *reinterpret_cast<const Pack<T, kVec>*>(part + 16 * (i * kLnThreads + static_cast<int>(threadIdx.x)));
-        } else {
-            const uintptr_t begin = reinterpret_cast<uintptr_t>(base) + static_cast<uintptr_t>(row) * D * sizeof(T);
-            const uint8_t* r = part + (threadIdx.x / kGroup) * kPiecesBytes<T, kGroup> + (begin & 15);
-            return *reinterpret_cast<const Pack<T, kVec>*>(r + index(i, lane) * sizeof(T));
-        }
-    }
-};
-
-// This thread's parameters, in the order of its elements.
-template <class R>
-__device__ __forceinline__ void load_params(const Param& a, int32_t D, int lane, float none, float (&out)[kLnN]) {
-#pragma unroll
-    for (int i = 0; i < R::kVecs; ++i) {
-        float t[R::kVec];
-#pragma unroll
-        for (int e = 0; e < R::kVec; ++e) t[e] = none;
-        if (R::index(i, lane) < D) load_param<R::kVec>(a, R::index(i, lane), none, t);
-#pragma unroll
-        for (int e = 0; e < R::kVec; ++e) out[i * R::kVec + e] = t[e];
-    }
-}
 
 // x and y are not declared restrict: y may be x itself. A group has its row in registers before it writes
 // it, and of the neighbouring rows that its pieces touch it uses nothing.
@@ -582,26 +395,6 @@ __global__ void __launch_bounds__(32 * kGradWarps)
         for (int w = 0; w < kGradWarps; ++w) s += acc[w][lane];
         store_param(out, param_dtype, j, s);
     }
-}
-
-bool rows_aligned16(const void* p, int64_t row_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0;
-}
-
-Param param(const void* p, int32_t dtype) { return Param{p, dtype, reinterpret_cast<uintptr_t>(p) % 16 == 0}; }
-
-// Allows the kernel its dynamic shared memory, once per device.
-template <auto kKernel>
-cudaError_t allow_smem(int bytes) {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> done[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-    return e;
 }
 
 // One block per SM, fewer for few rows.

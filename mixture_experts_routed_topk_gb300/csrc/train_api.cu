@@ -1,7 +1,9 @@
-// train_api.cu -- the C ABI of the operators around the expert layer (layer norm, top-k router,
-// vocabulary losses): argument checks, then the launches. As in moe_api.cu, the checks that need no
+// train_api.cu -- the C ABI of the operators around the expert layer (layer norm, norms around a block, top-k
+// router, vocabulary losses): argument checks, then the launches. As in moe_api.cu, the checks that need no
 // GPU run first, and an entry point only enqueues work on the caller's stream.
 #include <cuda_runtime.h>
+
+#include <cmath>
 
 #include "train_internal.cuh"
 
@@ -140,6 +142,115 @@ moe_status_t moe_layernorm_bwd(const void* dy, const void* x, const void* gamma,
     p.D = D;
     p.sm_count = dev.sm_count;
     return launch_layernorm_bwd(p, s);
+}
+
+moe_status_t moe_block_norm_fwd(const void* block, const void* residual, const void* post_gamma, const void* gate,
+                                int32_t gate_per_token, const void* pre_gamma, int32_t dtype, int32_t param_dtype,
+                                float residual_scale, float eps, void* stream_out, void* normed, float* post_rstd,
+                                float* pre_rstd, int64_t T, int32_t D, moe_stream_t stream) {
+    if (bad_dtype(dtype) || bad_dtype(param_dtype) || !(eps >= 0.0f) || !std::isfinite(residual_scale) || T < 0 || D <= 0)
+        return MOE_ERR_INVALID_ARG;
+    if (post_gamma && !post_rstd) return MOE_ERR_INVALID_ARG;
+    if (T > kMaxRows || D > kLnMaxD) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!block || !residual || !stream_out || !normed || !pre_rstd) return MOE_ERR_INVALID_ARG;
+    const size_t a = dtype_size(dtype), pa = dtype_size(param_dtype);
+    if (!aligned(block, a) || !aligned(residual, a) || !aligned(stream_out, a) || !aligned(normed, a) ||
+        !aligned(gate, gate_per_token ? a : pa) || !aligned(post_gamma, pa) || !aligned(pre_gamma, pa) ||
+        !aligned(post_rstd, 4) || !aligned(pre_rstd, 4))
+        return MOE_ERR_MISALIGNED;
+    DeviceInfo dev;
+    const moe_status_t st = sm103(&dev);
+    if (st != MOE_OK) return st;
+    BlockNormProblem p{};
+    p.block = block;
+    p.residual = residual;
+    p.post_gamma = post_gamma;
+    p.gate = gate;
+    p.pre_gamma = pre_gamma;
+    p.gate_per_token = gate && gate_per_token;
+    p.dtype = dtype;
+    p.param_dtype = param_dtype;
+    p.stream = stream_out;
+    p.normed = normed;
+    p.post_rstd = post_rstd;
+    p.pre_rstd = pre_rstd;
+    p.T = T;
+    p.D = D;
+    p.residual_scale = residual_scale;
+    p.eps = eps;
+    p.sm_count = dev.sm_count;
+    return launch_block_norm_fwd(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_block_norm_bwd_workspace_bytes(int64_t T, int32_t D) {
+    if (T <= 0 || T > kMaxRows || D <= 0 || D > kLnMaxD) return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(kBnMaxBlocks) * D;
+}
+
+moe_status_t moe_block_norm_bwd(const void* dstream, const void* dnormed, const void* block, const void* stream_in,
+                                const void* post_gamma, const void* gate, int32_t gate_per_token, const void* pre_gamma,
+                                const float* post_rstd, const float* pre_rstd, int32_t dtype, int32_t param_dtype,
+                                float residual_scale, void* dblock, void* dresidual, void* dpost_gamma, void* dgate,
+                                void* dpre_gamma, int64_t T, int32_t D, void* workspace, size_t workspace_bytes,
+                                moe_stream_t stream) {
+    if (bad_dtype(dtype) || bad_dtype(param_dtype) || !std::isfinite(residual_scale) || T < 0 || D <= 0)
+        return MOE_ERR_INVALID_ARG;
+    if (T > kMaxRows || D > kLnMaxD) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const size_t a = dtype_size(dtype), pa = dtype_size(param_dtype);
+    const bool per_token = gate_per_token != 0;
+    if (!aligned(dpost_gamma, pa) || !aligned(dpre_gamma, pa) || !aligned(dgate, per_token ? a : pa))
+        return MOE_ERR_MISALIGNED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DeviceInfo dev;
+    moe_status_t st;
+    void* sums[3] = {dpre_gamma, dpost_gamma, per_token ? nullptr : dgate};
+    if (T == 0) {  // no rows: the parameters' gradients are zero
+        if (!sums[0] && !sums[1] && !sums[2]) return MOE_OK;
+        if ((st = sm103(&dev)) != MOE_OK) return st;
+        for (void* t : sums)
+            if (t && cudaMemsetAsync(t, 0, pa * D, s) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (!dnormed || !stream_in || !pre_rstd || !dblock || !dresidual) return MOE_ERR_INVALID_ARG;
+    // a gradient of what is not there; without norm and gate the block itself is not needed
+    if ((post_gamma || dpost_gamma) && !post_rstd) return MOE_ERR_INVALID_ARG;
+    if (dgate && !gate) return MOE_ERR_INVALID_ARG;
+    if ((post_rstd || gate) && !block) return MOE_ERR_INVALID_ARG;
+    if (!aligned(dstream, a) || !aligned(dnormed, a) || !aligned(block, a) || !aligned(stream_in, a) ||
+        !aligned(dblock, a) || !aligned(dresidual, a) || !aligned(gate, per_token ? a : pa) || !aligned(post_gamma, pa) ||
+        !aligned(pre_gamma, pa) || !aligned(post_rstd, 4) || !aligned(pre_rstd, 4))
+        return MOE_ERR_MISALIGNED;
+    if (sums[0] || sums[1] || sums[2]) {  // the partial sums of the parameters' gradients
+        if (!workspace) return MOE_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+        if (workspace_bytes < moe_block_norm_bwd_workspace_bytes(T, D)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    if ((st = sm103(&dev)) != MOE_OK) return st;
+    BlockNormProblem p{};
+    p.dstream = dstream;
+    p.dnormed = dnormed;
+    p.block = block;
+    p.stream = const_cast<void*>(stream_in);
+    p.post_gamma = post_gamma;
+    p.gate = gate;
+    p.pre_gamma = pre_gamma;
+    p.gate_per_token = gate && per_token;
+    p.post_rstd_in = post_rstd;
+    p.pre_rstd_in = pre_rstd;
+    p.dtype = dtype;
+    p.param_dtype = param_dtype;
+    p.dblock = dblock;
+    p.dresidual = dresidual;
+    p.dpost_gamma = dpost_gamma;
+    p.dgate = dgate;
+    p.dpre_gamma = dpre_gamma;
+    p.partial = static_cast<float*>(workspace);
+    p.T = T;
+    p.D = D;
+    p.residual_scale = residual_scale;
+    p.sm_count = dev.sm_count;
+    return launch_block_norm_bwd(p, s);
 }
 
 moe_status_t moe_router_topk_fwd(const void* logits, int32_t dtype, int32_t* topk_ids, float* topk_scores, int64_t T,

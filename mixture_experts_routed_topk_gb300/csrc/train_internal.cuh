@@ -73,6 +73,41 @@ constexpr int32_t kLnMaxD = 1 << 24;
 moe_status_t launch_layernorm_fwd(const LayerNormProblem& p, cudaStream_t stream);
 moe_status_t launch_layernorm_bwd(const LayerNormProblem& p, cudaStream_t stream);
 
+// The norms before and after a block with its gate and residual scale (block_norm_*.cu).
+struct BlockNormProblem {
+    const void* block;       // [T, D]; backward: may be null where its gradient does not need it
+    const void* residual;    // forward
+    const void* post_gamma;  // [D] or null: 1
+    const void* gate;        // [D] of param_dtype, [T, D] of dtype, or null: 1
+    const void* pre_gamma;   // [D] or null: 1
+    bool gate_per_token;
+    int32_t dtype, param_dtype;
+    void* stream;    // forward: written; backward: read
+    void* normed;
+    float* post_rstd;  // null: no norm after the block
+    float* pre_rstd;
+    // backward
+    const void* dstream;  // may be null: 0
+    const void* dnormed;
+    const float* post_rstd_in;
+    const float* pre_rstd_in;
+    void* dblock;
+    void* dresidual;
+    void* dpost_gamma;  // these may be null
+    void* dgate;
+    void* dpre_gamma;
+    float* partial;  // [kBnMaxBlocks][2][D] fp32
+    int64_t T;
+    int32_t D;
+    float residual_scale, eps;
+    int sm_count;
+};
+// Rows of the parameter gradients' partial sums, as for the layer norm; long rows have two blocks to an SM.
+constexpr int kBnMaxBlocks = 304;
+
+moe_status_t launch_block_norm_fwd(const BlockNormProblem& p, cudaStream_t stream);
+moe_status_t launch_block_norm_bwd(const BlockNormProblem& p, cudaStream_t stream);
+
 struct RouterProblem {
     const void* logits;  // [T, E] fp32 or bf16
     int32_t dtype;
