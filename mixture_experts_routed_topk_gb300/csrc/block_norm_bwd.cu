@@ -40,12 +40,18 @@ constexpr int kBwdTensors = 12;
 template <typename T>
 constexpr int kBwdSmem = kBwdTensors * kTensorBytes<T, kBnN<T>>;
 
-template <typename T, int kGroup, bool kAligned>
+// What there is of the block's side: nothing (its gradient is da alone), the block, the block and a gate per token.
+enum Side { kNoBlock, kBlock, kTokenGate };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <typename T, int kGroup, bool kAligned, Side kSide>
 __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, const BwdArgs a) {
     constexpr int kN = kBnN<T>;
     using R = Row<T, kGroup, kAligned, kN>;
-    constexpr int kVec = R::kVec, kVecs = R::kVecs, kRows = kLnThreads / kGroup, kTensor = kTensorBytes<T, kN>;
-    using P = Pack<T, kVec>;
+    using C = Chunk<T, kGroup, kAligned, kN>;
+    using Pairs = typename C::Pairs;
+    constexpr int kP = C::kPairs, kRows = kLnThreads / kGroup, kTensor = kTensorBytes<T, kN>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][1][kLnThreads / 32];
     GroupSum<kGroup, 1> sum{buf};
@@ -53,9 +59,10 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
     const int32_t D = a.D;
     const int64_t rows = a.rows, stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
-    // the tensors' places in a stage
-    const int at_ds = 2 * kTensor, at_b = at_ds + (x.dstream ? kTensor : 0), at_g = at_b + (x.block ? kTensor : 0);
-    const int stage = at_g + (x.gate ? kTensor : 0);
+    // the tensors' places in a stage: dnormed, stream, block, gate, dstream
+    constexpr int kBlockAt = 2 * kTensor, kGateAt = 3 * kTensor;
+    constexpr int kStreamGradAt = (kSide == kNoBlock ? 2 : kSide == kBlock ? 3 : 4) * kTensor;
+    const int stage = kStreamGradAt + (x.dstream ? kTensor : 0);
     const int stages = stage <= 3 * kTensor ? 4 : stage <= 4 * kTensor ? 3 : 2;
     griddep_wait();
     griddep_launch_dependents();
@@ -64,29 +71,31 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
             uint8_t* to = ring + slot * stage;
             R::fetch(to, x.dnormed, r, rows, D, lane);
             R::fetch(to + kTensor, x.stream, r, rows, D, lane);
-            if (x.dstream) R::fetch(to + at_ds, x.dstream, r, rows, D, lane);
-            if (x.block) R::fetch(to + at_b, x.block, r, rows, D, lane);
-            if (x.gate) R::fetch(to + at_g, x.gate, r, rows, D, lane);
+            if constexpr (kSide != kNoBlock) R::fetch(to + kBlockAt, x.block, r, rows, D, lane);
+            if constexpr (kSide == kTokenGate) R::fetch(to + kGateAt, x.gate, r, rows, D, lane);
+            if (x.dstream) R::fetch(to + kStreamGradAt, x.dstream, r, rows, D, lane);
         }
         copy_commit();
     };
 #pragma unroll 1
     for (int s = 0; s < stages - 1; ++s) fetch(s, row + s * stride);
-    float pre[kN], post[kN], dpre[kN], dpost[kN];
-    load_params<R>(a.pre_gamma, D, lane, 1.0f, pre);
+    float2 pre[kN / 2], post[kN / 2], dpre[kN / 2], dpost[kN / 2];
     {
-        float t[kN];
-        load_params<R>(a.post_gamma, D, lane, 1.0f, post);
-        load_params<R>(a.channel_gate, D, lane, 1.0f, t);
+        float t[kN], u[kN];
+        load_params<R>(a.pre_gamma, D, lane, 1.0f, t);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) post[i] *= t[i], dpre[i] = 0.0f, dpost[i] = 0.0f;
+        for (int i = 0; i < kN / 2; ++i) pre[i] = make_float2(t[2 * i], t[2 * i + 1]), dpre[i] = dpost[i] = both(0.0f);
+        load_params<R>(a.post_gamma, D, lane, 1.0f, t);
+        load_params<R>(a.channel_gate, D, lane, 1.0f, u);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) post[i] = make_float2(t[2 * i] * u[2 * i], t[2 * i + 1] * u[2 * i + 1]);
     }
     const float inv_d = 1.0f / static_cast<float>(D);
     float next_pre = row < rows ? __ldg(a.pre_rstd + row) : 0.0f;
     float next_post = row < rows && a.post_rstd ? __ldg(a.post_rstd + row) : 1.0f;
     int slot = 0;
     for (; row < rows; row += stride) {
-        const float pre_rstd = next_pre, post_rstd = next_post;
+        const float2 pre_rstd = both(next_pre), post_rstd = both(next_post);
         if (row + stride < rows) {
             next_pre = __ldg(a.pre_rstd + row + stride);
             if (a.post_rstd) next_post = __ldg(a.post_rstd + row + stride);
@@ -100,71 +109,82 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
         }
         fetch(slot == 0 ? stages - 1 : slot - 1, row + (stages - 1) * stride);  // the place read in the last round
         const uint8_t* at = ring + slot * stage;
-        float s[1] = {0.0f};
+        float2 part = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (R::index(i, lane) < D) {
-                const P pn = R::get(at, x.dnormed, row, D, i, lane), ps = R::get(at + kTensor, x.stream, row, D, i, lane);
+        for (int c = 0; c < C::kChunks; ++c) {
+            if (C::any(c, lane, D)) {
+                Pairs n, s;
+                C::get(at, x.dnormed, row, D, c, lane, n);
+                C::get(at + kTensor, x.stream, row, D, c, lane, s);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const int n = i * kVec + e;
-                    const float t = to_float(pn.v[e]) * (to_float(ps.v[e]) * pre_rstd);
-                    dpre[n] += t;
-                    s[0] = fmaf(t, pre[n], s[0]);
+                for (int i = 0; i < kP; ++i) {
+                    const float2 t = __fmul2_rn(n[i], __fmul2_rn(s[i], pre_rstd));
+                    dpre[c * kP + i] = __fadd2_rn(dpre[c * kP + i], t);
+                    part = __ffma2_rn(t, pre[c * kP + i], part);
                 }
             }
         }
+        float s[1] = {part.x + part.y};
         sum(s);
-        const float m1 = s[0] * inv_d;
-        float gb[kN];
-        s[0] = 0.0f;
+        const float2 m1 = both(-s[0] * inv_d);
+        float2 gb[kN / 2];
+        part = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = R::index(i, lane);
-            if (j < D) {
-                const P pn = R::get(at, x.dnormed, row, D, i, lane), ps = R::get(at + kTensor, x.stream, row, D, i, lane);
-                P pd, pb, pg, pr, pdg;
-                if (x.dstream) pd = R::get(at + at_ds, x.dstream, row, D, i, lane);
-                if (x.block) pb = R::get(at + at_b, x.block, row, D, i, lane);
-                if (x.gate) pg = R::get(at + at_g, x.gate, row, D, i, lane);
+        for (int c = 0; c < C::kChunks; ++c) {
+            if (C::any(c, lane, D)) {
+                Pairs n, s, d, b, g, out;
+                C::get(at, x.dnormed, row, D, c, lane, n);
+                C::get(at + kTensor, x.stream, row, D, c, lane, s);
+                if (x.dstream) C::get(at + kStreamGradAt, x.dstream, row, D, c, lane, d);
+                if constexpr (kSide != kNoBlock) C::get(at + kBlockAt, x.block, row, D, c, lane, b);
+                if constexpr (kSide == kTokenGate) C::get(at + kGateAt, x.gate, row, D, c, lane, g);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const int n = i * kVec + e;
-                    const float hat = to_float(ps.v[e]) * pre_rstd;
-                    const float da = fmaf(pre_rstd, fmaf(-hat, m1, to_float(pn.v[e]) * pre[n]),
-                                          x.dstream ? to_float(pd.v[e]) : 0.0f);
-                    pr.v[e] = from_float<T>(a.scale * da);
-                    float g = da;
-                    const float bh = x.block ? to_float(pb.v[e]) * post_rstd : 0.0f;
-                    if (x.gate) {
-                        pdg.v[e] = from_float<T>(da * (bh * post[n]));
-                        g *= to_float(pg.v[e]);
+                for (int i = 0; i < kP; ++i) {
+                    const int k = c * kP + i;
+                    float2 da = __ffma2_rn(__fmul2_rn(s[i], pre_rstd), m1, __fmul2_rn(n[i], pre[k]));
+                    da = x.dstream ? __ffma2_rn(pre_rstd, da, d[i]) : __fmul2_rn(pre_rstd, da);
+                    out[i] = __fmul2_rn(both(a.scale), da);
+                    if constexpr (kSide != kNoBlock) {
+                        const float2 bh = __fmul2_rn(b[i], post_rstd);
+                        if constexpr (kSide == kTokenGate) {
+                            b[i] = __fmul2_rn(da, __fmul2_rn(bh, post[k]));  // the gate's gradient
+                            da = __fmul2_rn(da, g[i]);
+                        }
+                        dpost[k] = __ffma2_rn(da, bh, dpost[k]);
+                        gb[k] = __fmul2_rn(da, post[k]);
+                        part = __ffma2_rn(gb[k], bh, part);
+                    } else {
+                        gb[k] = da;
                     }
-                    dpost[n] = fmaf(g, bh, dpost[n]);
-                    gb[n] = g * post[n];
-                    s[0] = fmaf(gb[n], bh, s[0]);
                 }
-                *reinterpret_cast<P*>(x.dresidual + row * D + j) = pr;
-                if (x.gate && x.dgate) *reinterpret_cast<P*>(x.dgate + row * D + j) = pdg;
+                C::put(x.dresidual, row, D, c, lane, out);
+                if constexpr (kSide == kTokenGate)
+                    if (x.dgate) C::put(x.dgate, row, D, c, lane, b);
+                if constexpr (kSide == kNoBlock) {
+                    Pairs da;
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) da[i] = gb[c * kP + i];
+                    C::put(x.dblock, row, D, c, lane, da);
+                }
             }
         }
-        float m2 = 0.0f;
-        if (a.post_rstd) {
-            sum(s);
-            m2 = s[0] * inv_d;
-        }
+        if constexpr (kSide != kNoBlock) {
+            float2 m2 = both(0.0f);
+            if (a.post_rstd) {
+                s[0] = part.x + part.y;
+                sum(s);
+                m2 = both(-s[0] * inv_d);
+            }
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int j = R::index(i, lane);
-            if (j < D) {
-                P pb, pd;
-                if (x.block) pb = R::get(at + at_b, x.block, row, D, i, lane);
+            for (int c = 0; c < C::kChunks; ++c) {
+                if (C::any(c, lane, D)) {
+                    Pairs b, out;
+                    C::get(at + kBlockAt, x.block, row, D, c, lane, b);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float bh = x.block ? to_float(pb.v[e]) * post_rstd : 0.0f;
-                    pd.v[e] = from_float<T>(post_rstd * fmaf(-bh, m2, gb[i * kVec + e]));
+                    for (int i = 0; i < kP; ++i)
+                        out[i] = __fmul2_rn(post_rstd, __ffma2_rn(__fmul2_rn(b[i], post_rstd), m2, gb[c * kP + i]));
+                    C::put(x.dblock, row, D, c, lane, out);
                 }
-                *reinterpret_cast<P*>(x.dblock + row * D + j) = pd;
             }
         }
         slot = slot + 1 == stages ? 0 : slot + 1;
@@ -179,11 +199,12 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
     constexpr int kCols = kGroup * kN;
     float* own = acc + (threadIdx.x / kGroup) * 2 * kCols;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < R::kVecs; ++i) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            own[R::index(i, lane) + e] = dpre[i * kVec + e];
-            own[kCols + R::index(i, lane) + e] = dpost[i * kVec + e];
+        for (int e = 0; e < R::kVec; ++e) {
+            const int n = i * R::kVec + e;
+            own[R::index(i, lane) + e] = n % 2 ? dpre[n / 2].y : dpre[n / 2].x;
+            own[kCols + R::index(i, lane) + e] = n % 2 ? dpost[n / 2].y : dpost[n / 2].x;
         }
     }
     __syncthreads();
@@ -332,12 +353,19 @@ __global__ void __launch_bounds__(32 * kGradWarps) k_bn_param_grads(const GradAr
     if (a.dgate) store_param(a.dgate, a.param_dtype, j, s * g[0]);
 }
 
-template <typename T, int kGroup, bool kAligned>
-cudaError_t run(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<&k_bn_bwd<T, kGroup, kAligned>>(kBwdSmem<T>);
+template <typename T, int kGroup, bool kAligned, Side kSide>
+cudaError_t run_side(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
+    const cudaError_t e = allow_smem<&k_bn_bwd<T, kGroup, kAligned, kSide>>(kBwdSmem<T>);
     if (e != cudaSuccess) return e;
     *blocks = static_cast<int>(std::min<int64_t>({ceil_div(p.T, kLnThreads / kGroup), p.sm_count, kBnMaxBlocks}));
-    return launch_pdl(k_bn_bwd<T, kGroup, kAligned>, dim3(*blocks), dim3(kLnThreads), kBwdSmem<T>, stream, x, a);
+    return launch_pdl(k_bn_bwd<T, kGroup, kAligned, kSide>, dim3(*blocks), dim3(kLnThreads), kBwdSmem<T>, stream, x, a);
+}
+
+template <typename T, int kGroup, bool kAligned>
+cudaError_t run(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
+    if (x.gate) return run_side<T, kGroup, kAligned, kTokenGate>(p, x, a, blocks, stream);
+    if (x.block) return run_side<T, kGroup, kAligned, kBlock>(p, x, a, blocks, stream);
+    return run_side<T, kGroup, kAligned, kNoBlock>(p, x, a, blocks, stream);
 }
 
 template <typename T, bool kAligned>

@@ -204,6 +204,59 @@ constexpr int kBnN = sizeof(T) == 4 ? 8 : 16;
 template <typename T>
 constexpr int kBnMaxHeldD = kLnThreads * kBnN<T>;
 
+template <typename T>
+__device__ __forceinline__ void store_two(T* to, float2 v) {
+    to[0] = from_float<T>(v.x);
+    to[1] = from_float<T>(v.y);
+}
+template <>
+__device__ __forceinline__ void store_two<__nv_bfloat16>(__nv_bfloat16* to, float2 v) {
+    *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(v);
+}
+template <>
+__device__ __forceinline__ void store_two<__half>(__half* to, float2 v) {
+    *reinterpret_cast<__half2*>(to) = __float22half2_rn(v);
+}
+
+// A thread's share of a row in chunks of 16 bytes, as pairs of floats for the instructions that take two. Element e
+// of chunk c is the thread's element c kC + e, in the order of load_params. Elements past the row's end are 0.
+template <typename T, int kGroup, bool kAligned, int kN>
+struct Chunk {
+    using R = Row<T, kGroup, kAligned, kN>;
+    static constexpr int kC = 16 / static_cast<int>(sizeof(T)), kPairs = kC / 2, kChunks = kN / kC;
+    using Pairs = float2[kPairs];
+
+    __device__ static bool any(int c, int lane, int32_t D) { return R::index(kAligned ? c : c * kC, lane) < D; }
+    __device__ static void get(const uint8_t* part, const T* base, int64_t row, int32_t D, int c, int lane, Pairs& v) {
+        if constexpr (kAligned) {
+            const auto p = R::get(part, base, row, D, c, lane);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) v[i] = make_float2(to_float(p.v[2 * i]), to_float(p.v[2 * i + 1]));
+        } else {
+            float t[kC];
+#pragma unroll
+            for (int e = 0; e < kC; ++e)
+                t[e] = R::index(c * kC + e, lane) < D ? to_float(R::get(part, base, row, D, c * kC + e, lane).v[0]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
+        }
+    }
+    __device__ static void put(T* base, int64_t row, int32_t D, int c, int lane, const Pairs& v) {
+        if constexpr (kAligned) {
+            Pack<T, kC> p;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) store_two(p.v + 2 * i, v[i]);
+            *reinterpret_cast<Pack<T, kC>*>(base + row * D + R::index(c, lane)) = p;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kC; ++e) {
+                const int j = R::index(c * kC + e, lane);
+                if (j < D) base[row * D + j] = from_float<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
+            }
+        }
+    }
+};
+
 bool rows_aligned16(const void* p, int64_t row_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0;
 }
