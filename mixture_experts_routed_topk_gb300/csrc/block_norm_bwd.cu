@@ -27,6 +27,7 @@ struct BwdArgs {
     int64_t rows;
     int32_t D;
     float scale;
+    int tensor, stages;  // the ring: bytes of a tensor's row, and stages
 };
 
 template <typename T>
@@ -35,23 +36,24 @@ struct BwdRows {
     T *dblock, *dresidual, *dgate;                       // dgate: per token, or null
 };
 
-// Twelve tensors' rows in the ring: four stages of the three that there always may be, three of four, two of five.
-constexpr int kBwdTensors = 12;
-template <typename T>
-constexpr int kBwdSmem = kBwdTensors * kTensorBytes<T, kBnN<T>>;
+// The ring: up to four stages of the three to five tensors, at least two.
+constexpr int kBwdSmem = 224 * 1024;
+
+// As plain stores under the condition below, nvcc 13.0 sends a first lane's elements of every group to the first
+// group's place; the tests of short odd rows show it.
+__device__ __forceinline__ void store_shared(float* to, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem_addr(to)), "f"(v) : "memory");
+}
 
 // What there is of the block's side: nothing (its gradient is da alone), the block, the block and a gate per token.
 enum Side { kNoBlock, kBlock, kTokenGate };
 
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-template <typename T, int kGroup, bool kAligned, Side kSide>
+template <typename T, int kGroup, bool kWhole, Side kSide>
 __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, const BwdArgs a) {
     constexpr int kN = kBnN<T>;
-    using R = Row<T, kGroup, kAligned, kN>;
-    using C = Chunk<T, kGroup, kAligned, kN>;
+    using C = Cells<T, kGroup, kWhole, kN>;
     using Pairs = typename C::Pairs;
-    constexpr int kP = C::kPairs, kRows = kLnThreads / kGroup, kTensor = kTensorBytes<T, kN>;
+    constexpr int kP = C::kPairs, kRows = kLnThreads / kGroup;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][1][kLnThreads / 32];
     GroupSum<kGroup, 1> sum{buf};
@@ -59,68 +61,62 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
     const int32_t D = a.D;
     const int64_t rows = a.rows, stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
+    const C cells(x.dnormed, row, D, lane);
     // the tensors' places in a stage: dnormed, stream, block, gate, dstream
-    constexpr int kBlockAt = 2 * kTensor, kGateAt = 3 * kTensor;
-    constexpr int kStreamGradAt = (kSide == kNoBlock ? 2 : kSide == kBlock ? 3 : 4) * kTensor;
-    const int stage = kStreamGradAt + (x.dstream ? kTensor : 0);
-    const int stages = stage <= 3 * kTensor ? 4 : stage <= 4 * kTensor ? 3 : 2;
-    griddep_wait();
-    griddep_launch_dependents();
+    const int stream_at = a.tensor, block_at = 2 * a.tensor, gate_at = 3 * a.tensor;
+    const int dstream_at = (kSide == kNoBlock ? 2 : kSide == kBlock ? 3 : 4) * a.tensor;
+    const int stage = dstream_at + (x.dstream ? a.tensor : 0);
     auto fetch = [&](int slot, int64_t r) {
         if (r < rows) {
             uint8_t* to = ring + slot * stage;
-            R::fetch(to, x.dnormed, r, rows, D, lane);
-            R::fetch(to + kTensor, x.stream, r, rows, D, lane);
-            if constexpr (kSide != kNoBlock) R::fetch(to + kBlockAt, x.block, r, rows, D, lane);
-            if constexpr (kSide == kTokenGate) R::fetch(to + kGateAt, x.gate, r, rows, D, lane);
-            if (x.dstream) R::fetch(to + kStreamGradAt, x.dstream, r, rows, D, lane);
+            cells.fetch(to, x.dnormed, r, rows);
+            cells.fetch(to + stream_at, x.stream, r, rows);
+            if constexpr (kSide != kNoBlock) cells.fetch(to + block_at, x.block, r, rows);
+            if constexpr (kSide == kTokenGate) cells.fetch(to + gate_at, x.gate, r, rows);
+            if (x.dstream) cells.fetch(to + dstream_at, x.dstream, r, rows);
         }
         copy_commit();
     };
+    griddep_wait();
+    griddep_launch_dependents();
 #pragma unroll 1
-    for (int s = 0; s < stages - 1; ++s) fetch(s, row + s * stride);
+    for (int s = 0; s < a.stages - 1; ++s) fetch(s, row + s * stride);
     float2 pre[kN / 2], post[kN / 2], dpre[kN / 2], dpost[kN / 2];
-    {
-        float t[kN], u[kN];
-        load_params<R>(a.pre_gamma, D, lane, 1.0f, t);
+    cells.params(a.pre_gamma, 1.0f, pre);
+    cells.params(a.post_gamma, 1.0f, post);
+    cells.params(a.channel_gate, 1.0f, dpost);
 #pragma unroll
-        for (int i = 0; i < kN / 2; ++i) pre[i] = make_float2(t[2 * i], t[2 * i + 1]), dpre[i] = dpost[i] = both(0.0f);
-        load_params<R>(a.post_gamma, D, lane, 1.0f, t);
-        load_params<R>(a.channel_gate, D, lane, 1.0f, u);
-#pragma unroll
-        for (int i = 0; i < kN / 2; ++i) post[i] = make_float2(t[2 * i] * u[2 * i], t[2 * i + 1] * u[2 * i + 1]);
+    for (int i = 0; i < kN / 2; ++i) {
+        post[i] = __fmul2_rn(post[i], dpost[i]);
+        dpre[i] = dpost[i] = both(0.0f);
     }
     const float inv_d = 1.0f / static_cast<float>(D);
-    float next_pre = row < rows ? __ldg(a.pre_rstd + row) : 0.0f;
-    float next_post = row < rows && a.post_rstd ? __ldg(a.post_rstd + row) : 1.0f;
+    auto rstd_of = [&](const float* p, int64_t r) { return p && r < rows ? __ldg(p + r) : 1.0f; };
+    float pre_next = rstd_of(a.pre_rstd, row), post_next = rstd_of(a.post_rstd, row);
     int slot = 0;
     for (; row < rows; row += stride) {
-        const float2 pre_rstd = both(next_pre), post_rstd = both(next_post);
-        if (row + stride < rows) {
-            next_pre = __ldg(a.pre_rstd + row + stride);
-            if (a.post_rstd) next_post = __ldg(a.post_rstd + row + stride);
-        }
-        if (stages == 4) copy_wait<2>();
-        else if (stages == 3) copy_wait<1>();
+        const float2 pre_rstd = both(pre_next), post_rstd = both(post_next);
+        pre_next = rstd_of(a.pre_rstd, row + stride);
+        post_next = rstd_of(a.post_rstd, row + stride);
+        if (a.stages == 4) copy_wait<2>();
+        else if (a.stages == 3) copy_wait<1>();
         else copy_wait<0>();
-        if constexpr (!kAligned) {  // the rows were copied by the whole group
-            if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
-            else __syncwarp();
-        }
-        fetch(slot == 0 ? stages - 1 : slot - 1, row + (stages - 1) * stride);  // the place read in the last round
-        const uint8_t* at = ring + slot * stage;
+        uint8_t* at = ring + slot * stage;
+        if constexpr (!kWhole)
+            for (int t = 0; t < stage; t += a.tensor) cells.trim(at + t);
+        fetch(slot == 0 ? a.stages - 1 : slot - 1, row + (a.stages - 1) * stride);  // the place read in the last round
         float2 part = both(0.0f);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
-            if (C::any(c, lane, D)) {
-                Pairs n, s;
-                C::get(at, x.dnormed, row, D, c, lane, n);
-                C::get(at + kTensor, x.stream, row, D, c, lane, s);
+            if (cells.any(c)) {
+                Pairs n, t;
+                cells.get(at, c, n);
+                cells.get(at + stream_at, c, t);
 #pragma unroll
                 for (int i = 0; i < kP; ++i) {
-                    const float2 t = __fmul2_rn(n[i], __fmul2_rn(s[i], pre_rstd));
-                    dpre[c * kP + i] = __fadd2_rn(dpre[c * kP + i], t);
-                    part = __ffma2_rn(t, pre[c * kP + i], part);
+                    const float2 v = __fmul2_rn(n[i], __fmul2_rn(t[i], pre_rstd));
+                    dpre[c * kP + i] = __fadd2_rn(dpre[c * kP + i], v);
+                    part = __ffma2_rn(v, pre[c * kP + i], part);
                 }
             }
         }
@@ -131,17 +127,17 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
         part = both(0.0f);
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c) {
-            if (C::any(c, lane, D)) {
-                Pairs n, s, d, b, g, out;
-                C::get(at, x.dnormed, row, D, c, lane, n);
-                C::get(at + kTensor, x.stream, row, D, c, lane, s);
-                if (x.dstream) C::get(at + kStreamGradAt, x.dstream, row, D, c, lane, d);
-                if constexpr (kSide != kNoBlock) C::get(at + kBlockAt, x.block, row, D, c, lane, b);
-                if constexpr (kSide == kTokenGate) C::get(at + kGateAt, x.gate, row, D, c, lane, g);
+            if (cells.any(c)) {
+                Pairs n, t, d, b, g, out;
+                cells.get(at, c, n);
+                cells.get(at + stream_at, c, t);
+                if (x.dstream) cells.get(at + dstream_at, c, d);
+                if constexpr (kSide != kNoBlock) cells.get(at + block_at, c, b);
+                if constexpr (kSide == kTokenGate) cells.get(at + gate_at, c, g);
 #pragma unroll
                 for (int i = 0; i < kP; ++i) {
                     const int k = c * kP + i;
-                    float2 da = __ffma2_rn(__fmul2_rn(s[i], pre_rstd), m1, __fmul2_rn(n[i], pre[k]));
+                    float2 da = __ffma2_rn(__fmul2_rn(t[i], pre_rstd), m1, __fmul2_rn(n[i], pre[k]));
                     da = x.dstream ? __ffma2_rn(pre_rstd, da, d[i]) : __fmul2_rn(pre_rstd, da);
                     out[i] = __fmul2_rn(both(a.scale), da);
                     if constexpr (kSide != kNoBlock) {
@@ -154,18 +150,13 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
                         gb[k] = __fmul2_rn(da, post[k]);
                         part = __ffma2_rn(gb[k], bh, part);
                     } else {
-                        gb[k] = da;
+                        n[i] = da;
                     }
                 }
-                C::put(x.dresidual, row, D, c, lane, out);
+                cells.put(x.dresidual, row, c, out);
                 if constexpr (kSide == kTokenGate)
-                    if (x.dgate) C::put(x.dgate, row, D, c, lane, b);
-                if constexpr (kSide == kNoBlock) {
-                    Pairs da;
-#pragma unroll
-                    for (int i = 0; i < kP; ++i) da[i] = gb[c * kP + i];
-                    C::put(x.dblock, row, D, c, lane, da);
-                }
+                    if (x.dgate) cells.put(x.dgate, row, c, b);
+                if constexpr (kSide == kNoBlock) cells.put(x.dblock, row, c, n);
             }
         }
         if constexpr (kSide != kNoBlock) {
@@ -177,17 +168,17 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
             }
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
-                if (C::any(c, lane, D)) {
+                if (cells.any(c)) {
                     Pairs b, out;
-                    C::get(at + kBlockAt, x.block, row, D, c, lane, b);
+                    cells.get(at + block_at, c, b);
 #pragma unroll
                     for (int i = 0; i < kP; ++i)
                         out[i] = __fmul2_rn(post_rstd, __ffma2_rn(__fmul2_rn(b[i], post_rstd), m2, gb[c * kP + i]));
-                    C::put(x.dblock, row, D, c, lane, out);
+                    cells.put(x.dblock, row, c, out);
                 }
             }
         }
-        slot = slot + 1 == stages ? 0 : slot + 1;
+        slot = slot + 1 == a.stages ? 0 : slot + 1;
     }
     if (a.partial == nullptr) return;
     // the block's row of partial sums: its groups own the same columns, and meet in the ring in group order
@@ -195,16 +186,18 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
     copy_wait<0>();
     __syncthreads();
     float* acc = reinterpret_cast<float*>(ring);  // [kRows][2][kGroup * kN]
-    static_assert(kBwdSmem<T> >= 2 * kLnThreads * kN * 4, "the sums fit the ring");
+    static_assert(kBwdSmem >= 2 * kLnThreads * kN * 4, "the sums fit the ring");
     constexpr int kCols = kGroup * kN;
     float* own = acc + (threadIdx.x / kGroup) * 2 * kCols;
 #pragma unroll
-    for (int i = 0; i < R::kVecs; ++i) {
+    for (int c = 0; c < C::kChunks; ++c) {
 #pragma unroll
-        for (int e = 0; e < R::kVec; ++e) {
-            const int n = i * R::kVec + e;
-            own[R::index(i, lane) + e] = n % 2 ? dpre[n / 2].y : dpre[n / 2].x;
-            own[kCols + R::index(i, lane) + e] = n % 2 ? dpost[n / 2].y : dpost[n / 2].x;
+        for (int e = 0; e < C::kC; ++e) {
+            const int n = c * C::kC + e;
+            if (cells.has(c, e)) {
+                store_shared(own + cells.index(c, e), n % 2 ? dpre[n / 2].y : dpre[n / 2].x);
+                store_shared(own + kCols + cells.index(c, e), n % 2 ? dpost[n / 2].y : dpost[n / 2].x);
+            }
         }
     }
     __syncthreads();
@@ -217,7 +210,8 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
     }
 }
 
-// Rows longer than a group holds: three passes over each of a block's rows, the second and third mostly from L2.
+// Rows longer than a group holds, and tensors that lie differently to 16-byte pieces: three passes over each of a
+// block's rows, the second and third mostly from L2.
 // The columns' sums are in shared memory where they fit, else in the block's row of partial sums; a column belongs
 // to one thread.
 constexpr int kLongSums = 96 * 1024;  // bytes of them in shared memory: two blocks share an SM
@@ -353,40 +347,39 @@ __global__ void __launch_bounds__(32 * kGradWarps) k_bn_param_grads(const GradAr
     if (a.dgate) store_param(a.dgate, a.param_dtype, j, s * g[0]);
 }
 
-template <typename T, int kGroup, bool kAligned, Side kSide>
-cudaError_t run_side(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<&k_bn_bwd<T, kGroup, kAligned, kSide>>(kBwdSmem<T>);
+template <typename T, int kGroup, bool kWhole, Side kSide>
+cudaError_t run_side(const BlockNormProblem& p, const BwdRows<T>& x, BwdArgs a, int* blocks, cudaStream_t stream) {
+    const cudaError_t e = allow_smem<&k_bn_bwd<T, kGroup, kWhole, kSide>>(kBwdSmem);
     if (e != cudaSuccess) return e;
-    *blocks = static_cast<int>(std::min<int64_t>({ceil_div(p.T, kLnThreads / kGroup), p.sm_count, kBnMaxBlocks}));
-    return launch_pdl(k_bn_bwd<T, kGroup, kAligned, kSide>, dim3(*blocks), dim3(kLnThreads), kBwdSmem<T>, stream, x, a);
+    *blocks = static_cast<int>(row_blocks(p.T, kLnThreads / kGroup, std::min(p.sm_count, kBnMaxBlocks)));
+    const int tensors = (kSide == kNoBlock ? 2 : kSide == kBlock ? 3 : 4) + (x.dstream ? 1 : 0);
+    a.tensor = tensor_stride<T, kGroup>(p.D);
+    a.stages = std::min(4, kBwdSmem / (tensors * a.tensor));
+    static_assert(2 * 5 * kTensorBytes<T, kBnN<T>> <= kBwdSmem, "two stages of everything");
+    return launch_pdl(k_bn_bwd<T, kGroup, kWhole, kSide>, dim3(*blocks), dim3(kLnThreads), kBwdSmem, stream, x, a);
 }
 
-template <typename T, int kGroup, bool kAligned>
+template <typename T, int kGroup, bool kWhole>
 cudaError_t run(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
-    if (x.gate) return run_side<T, kGroup, kAligned, kTokenGate>(p, x, a, blocks, stream);
-    if (x.block) return run_side<T, kGroup, kAligned, kBlock>(p, x, a, blocks, stream);
-    return run_side<T, kGroup, kAligned, kNoBlock>(p, x, a, blocks, stream);
+    if (x.gate) return run_side<T, kGroup, kWhole, kTokenGate>(p, x, a, blocks, stream);
+    if (x.block) return run_side<T, kGroup, kWhole, kBlock>(p, x, a, blocks, stream);
+    return run_side<T, kGroup, kWhole, kNoBlock>(p, x, a, blocks, stream);
 }
 
-template <typename T, bool kAligned>
+template <typename T, bool kWhole>
 cudaError_t dispatch(const BlockNormProblem& p, const BwdRows<T>& x, const BwdArgs& a, int* blocks, cudaStream_t stream) {
     constexpr int kN = kBnN<T>;
-    if (p.D <= 32 * kN) return run<T, 32, kAligned>(p, x, a, blocks, stream);
-    if (p.D <= 64 * kN) return run<T, 64, kAligned>(p, x, a, blocks, stream);
-    if (p.D <= 128 * kN) return run<T, 128, kAligned>(p, x, a, blocks, stream);
-    if (p.D <= 256 * kN) return run<T, 256, kAligned>(p, x, a, blocks, stream);
-    if (p.D <= 512 * kN) return run<T, 512, kAligned>(p, x, a, blocks, stream);
-    constexpr int kVec = kAligned ? 16 / static_cast<int>(sizeof(T)) : 1;
-    const cudaError_t e = allow_smem<&k_bn_bwd_long<T, kVec>>(kLongSums);
-    if (e != cudaSuccess) return e;
-    const int64_t sums = 8 * static_cast<int64_t>(p.D);
-    *blocks = static_cast<int>(std::min<int64_t>({p.T, 2 * p.sm_count, kBnMaxBlocks}));
-    return launch_pdl(k_bn_bwd_long<T, kVec>, dim3(*blocks), dim3(kLnThreads),
-                      static_cast<size_t>(a.partial && sums <= kLongSums ? sums : 0), stream, x, a);
+    const int32_t held = kWhole ? p.D : p.D + 16 / static_cast<int>(sizeof(T)) - 1;  // with what comes before the row
+    if (held <= 32 * kN) return run<T, 32, kWhole>(p, x, a, blocks, stream);
+    if (held <= 64 * kN) return run<T, 64, kWhole>(p, x, a, blocks, stream);
+    if (held <= 128 * kN) return run<T, 128, kWhole>(p, x, a, blocks, stream);
+    if (held <= 256 * kN) return run<T, 256, kWhole>(p, x, a, blocks, stream);
+    return run<T, 512, kWhole>(p, x, a, blocks, stream);
 }
 
 template <typename T>
 cudaError_t of_type(const BlockNormProblem& p, int* blocks, cudaStream_t stream) {
+    constexpr int kC = 16 / static_cast<int>(sizeof(T));
     const T* gate = p.gate_per_token ? static_cast<const T*>(p.gate) : nullptr;
     const bool needs_block = p.post_rstd_in || p.gate;
     const BwdRows<T> x{static_cast<const T*>(p.dstream), static_cast<const T*>(p.dnormed),
@@ -395,15 +388,20 @@ cudaError_t of_type(const BlockNormProblem& p, int* blocks, cudaStream_t stream)
                        gate ? static_cast<T*>(p.dgate) : nullptr};
     const BwdArgs a{param(p.post_gamma, p.param_dtype), param(gate ? nullptr : p.gate, p.param_dtype),
                     param(p.pre_gamma, p.param_dtype), p.post_rstd_in, p.pre_rstd_in, p.partial, p.T, p.D,
-                    p.residual_scale};
-    const int64_t bytes = static_cast<int64_t>(p.D) * sizeof(T);
-    bool whole = true;
-    for (const void* t : {static_cast<const void*>(x.dstream), static_cast<const void*>(x.dnormed),
-                          static_cast<const void*>(x.block), static_cast<const void*>(x.stream),
-                          static_cast<const void*>(x.gate), static_cast<const void*>(x.dblock),
-                          static_cast<const void*>(x.dresidual), static_cast<const void*>(x.dgate)})
-        whole = whole && rows_aligned16(t, bytes);
-    return whole ? dispatch<T, true>(p, x, a, blocks, stream) : dispatch<T, false>(p, x, a, blocks, stream);
+                    p.residual_scale, 0, 0};
+    const bool alike = lie_alike({x.dstream, x.dnormed, x.block, x.stream, x.gate, x.dblock, x.dresidual, x.dgate});
+    const bool whole = alike && rows_aligned16(x.dnormed, static_cast<int64_t>(p.D) * sizeof(T));
+    if (whole && p.D <= kBnMaxHeldD<T>) return dispatch<T, true>(p, x, a, blocks, stream);
+    if (alike && !whole && p.D + kC - 1 <= kBnMaxHeldD<T>) return dispatch<T, false>(p, x, a, blocks, stream);
+    const int64_t sums = 8 * static_cast<int64_t>(p.D);
+    *blocks = static_cast<int>(std::min<int64_t>({p.T, 2 * p.sm_count, kBnMaxBlocks}));
+    auto go = [&](auto kernel, cudaError_t allowed) {
+        if (allowed != cudaSuccess) return allowed;
+        return launch_pdl(kernel, dim3(*blocks), dim3(kLnThreads),
+                          static_cast<size_t>(a.partial && sums <= kLongSums ? sums : 0), stream, x, a);
+    };
+    return whole ? go(k_bn_bwd_long<T, kC>, allow_smem<&k_bn_bwd_long<T, kC>>(kLongSums))
+                 : go(k_bn_bwd_long<T, 1>, allow_smem<&k_bn_bwd_long<T, 1>>(kLongSums));
 }
 
 }  // namespace

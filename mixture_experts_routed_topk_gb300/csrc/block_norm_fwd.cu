@@ -26,18 +26,19 @@ struct FwdArgs {
     float scale, eps;
 };
 
+// Two rows at a time; the ring has six stages of two tensors, or four of three: 200 KB.
 constexpr int kBatch = 2;
-// Two tensors in six stages, or three in four: 200 KB.
 template <typename T>
 constexpr int kFwdSmem = 12 * kTensorBytes<T, kBnN<T>>;
 
 // The pointers are not declared restrict: stream may be residual or block, normed too.
-template <typename T, int kGroup, bool kAligned>
+template <typename T, int kGroup, bool kWhole>
 __global__ void __launch_bounds__(kLnThreads, 1)
     k_bn_fwd(const T* block, const T* residual, const T* gate, T* stream, T* normed, const FwdArgs a) {
     constexpr int kN = kBnN<T>;
-    using R = Row<T, kGroup, kAligned, kN>;
-    constexpr int kVec = R::kVec, kVecs = R::kVecs, kRows = kLnThreads / kGroup, kTensor = kTensorBytes<T, kN>;
+    using C = Cells<T, kGroup, kWhole, kN>;
+    using Pairs = typename C::Pairs;
+    constexpr int kP = C::kPairs, kRows = kLnThreads / kGroup, kTensor = kTensorBytes<T, kN>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][kBatch][kLnThreads / 32];
     GroupSum<kGroup, kBatch> sum{buf};
@@ -45,60 +46,62 @@ __global__ void __launch_bounds__(kLnThreads, 1)
     const int32_t D = a.D;
     const int64_t rows = a.rows, stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kGroup;
+    const C cells(block, row, D, lane);
     const int tensors = gate ? 3 : 2, stages = gate ? 4 : 6, stage = tensors * kTensor;
     griddep_wait();
     griddep_launch_dependents();
     auto fetch = [&](int slot, int64_t r) {
         if (r < rows) {
             uint8_t* to = ring + slot * stage;
-            R::fetch(to, block, r, rows, D, lane);
-            R::fetch(to + kTensor, residual, r, rows, D, lane);
-            if (gate) R::fetch(to + 2 * kTensor, gate, r, rows, D, lane);
+            cells.fetch(to, block, r, rows);
+            cells.fetch(to + kTensor, residual, r, rows);
+            if (gate) cells.fetch(to + 2 * kTensor, gate, r, rows);
         }
         copy_commit();
     };
 #pragma unroll 1
     for (int s = 0; s < stages - kBatch; ++s) fetch(s, row + s * stride);
-    float post[kN], pre[kN];
-    {
-        float t[kN];
-        load_params<R>(a.post_gamma, D, lane, 1.0f, post);
-        load_params<R>(a.channel_gate, D, lane, 1.0f, t);
+    float2 post[kN / 2], pre[kN / 2];
+    cells.params(a.post_gamma, 1.0f, post);
+    cells.params(a.channel_gate, 1.0f, pre);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) post[i] *= t[i];
-        load_params<R>(a.pre_gamma, D, lane, 1.0f, pre);
-    }
+    for (int i = 0; i < kN / 2; ++i) post[i] = __fmul2_rn(post[i], pre[i]);
+    cells.params(a.pre_gamma, 1.0f, pre);
     const float inv_d = 1.0f / static_cast<float>(D);
     int slot = 0;
     for (; row < rows; row += kBatch * stride) {
         if (gate) copy_wait<0>();
         else copy_wait<2>();
-        if constexpr (!kAligned) {  // the rows were copied by the whole group
-            if constexpr (kGroup > 32) group_barrier(1 + threadIdx.x / kGroup, kGroup);
-            else __syncwarp();
+        if constexpr (!kWhole) {
+            for (int t = 0; t < tensors; ++t)
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) cells.trim(ring + (slot + k) * stage + t * kTensor);
         }
         const int last = slot == 0 ? stages - kBatch : slot - kBatch;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) fetch(last + k, row + (stages - kBatch + k) * stride);
-        float v[kBatch][kN], s[kBatch], rstd[kBatch];
+        float2 v[kBatch][kN / 2], part[kBatch];
+        float s[kBatch], rstd[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const bool live = row + k * stride < rows;
-            s[k] = 0.0f;
+            part[k] = both(0.0f);
+            rstd[k] = 1.0f;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
+            for (int c = 0; c < C::kChunks; ++c) {
+                Pairs b;
+                if (row + k * stride < rows && cells.any(c)) {
+                    cells.get(ring + (slot + k) * stage, c, b);
+                } else {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) v[k][i * kVec + e] = 0.0f;
-                if (live && R::index(i, lane) < D) {
-                    const auto p = R::get(ring + (slot + k) * stage, block, row + k * stride, D, i, lane);
+                    for (int i = 0; i < kP; ++i) b[i] = both(0.0f);
+                }
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        v[k][i * kVec + e] = to_float(p.v[e]);
-                        s[k] = fmaf(v[k][i * kVec + e], v[k][i * kVec + e], s[k]);
-                    }
+                for (int i = 0; i < kP; ++i) {
+                    v[k][c * kP + i] = b[i];
+                    part[k] = __ffma2_rn(b[i], b[i], part[k]);
                 }
             }
-            rstd[k] = 1.0f;
+            s[k] = part[k].x + part[k].y;
         }
         if (a.post_rstd) {
             sum(s);
@@ -112,24 +115,24 @@ __global__ void __launch_bounds__(kLnThreads, 1)
         for (int k = 0; k < kBatch; ++k) {
             const int64_t r = row + k * stride;
             const uint8_t* at = ring + (slot + k) * stage;
-            s[k] = 0.0f;
+            part[k] = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                if (r < rows && R::index(i, lane) < D) {
-                    const auto pr = R::get(at + kTensor, residual, r, D, i, lane);
-                    Pack<T, kVec> pg;
-                    if (gate) pg = R::get(at + 2 * kTensor, gate, r, D, i, lane);
+            for (int c = 0; c < C::kChunks; ++c) {
+                if (r < rows && cells.any(c)) {
+                    Pairs t, g;
+                    cells.get(at + kTensor, c, t);
+                    if (gate) cells.get(at + 2 * kTensor, c, g);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        const int n = i * kVec + e;
-                        float u = v[k][n] * rstd[k] * post[n];
-                        if (gate) u *= to_float(pg.v[e]);
-                        u = fmaf(a.scale, to_float(pr.v[e]), u);
-                        v[k][n] = u;
-                        s[k] = fmaf(u, u, s[k]);
+                    for (int i = 0; i < kP; ++i) {
+                        const int n = c * kP + i;
+                        float2 u = __fmul2_rn(__fmul2_rn(v[k][n], both(rstd[k])), post[n]);
+                        if (gate) u = __fmul2_rn(u, g[i]);
+                        v[k][n] = __ffma2_rn(both(a.scale), t[i], u);
+                        part[k] = __ffma2_rn(v[k][n], v[k][n], part[k]);
                     }
                 }
             }
+            s[k] = part[k].x + part[k].y;
         }
         sum(s);
 #pragma unroll
@@ -138,18 +141,16 @@ __global__ void __launch_bounds__(kLnThreads, 1)
             if (r >= rows) break;
             const float pre_rstd = 1.0f / sqrtf(s[k] * inv_d + a.eps);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int j = R::index(i, lane);
-                if (j < D) {
-                    Pack<T, kVec> ps, pn;
+            for (int c = 0; c < C::kChunks; ++c) {
+                if (cells.any(c)) {
+                    Pairs t, n;
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        const int n = i * kVec + e;
-                        ps.v[e] = from_float<T>(v[k][n]);
-                        pn.v[e] = from_float<T>(v[k][n] * pre_rstd * pre[n]);
+                    for (int i = 0; i < kP; ++i) {
+                        t[i] = v[k][c * kP + i];
+                        n[i] = __fmul2_rn(__fmul2_rn(t[i], both(pre_rstd)), pre[c * kP + i]);
                     }
-                    *reinterpret_cast<Pack<T, kVec>*>(stream + r * D + j) = ps;
-                    *reinterpret_cast<Pack<T, kVec>*>(normed + r * D + j) = pn;
+                    cells.put(stream, r, c, t);
+                    cells.put(normed, r, c, n);
                 }
             }
             if (lane == 0) a.pre_rstd[r] = pre_rstd;
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(kLnThreads, 1)
     }
 }
 
-// Rows longer than a group holds: a block to each, three passes.
+// Rows longer than a group holds, and tensors that lie differently to 16-byte pieces: a block to each row, three
+// passes.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kLnThreads)
     k_bn_fwd_long(const T* block, const T* residual, const T* gate, T* stream, T* normed, const FwdArgs a) {
@@ -222,39 +224,43 @@ __global__ void __launch_bounds__(kLnThreads)
     }
 }
 
-template <typename T, int kGroup, bool kAligned>
+template <typename T, int kGroup, bool kWhole>
 cudaError_t run(const BlockNormProblem& p, const FwdArgs& a, const T* gate, cudaStream_t stream) {
-    const cudaError_t e = allow_smem<&k_bn_fwd<T, kGroup, kAligned>>(kFwdSmem<T>);
+    const cudaError_t e = allow_smem<&k_bn_fwd<T, kGroup, kWhole>>(kFwdSmem<T>);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = std::min<int64_t>(ceil_div(p.T, kLnThreads / kGroup), p.sm_count);
-    return launch_pdl(k_bn_fwd<T, kGroup, kAligned>, dim3(static_cast<unsigned>(blocks)), dim3(kLnThreads), kFwdSmem<T>,
+    const int64_t blocks = row_blocks(p.T, kLnThreads / kGroup, p.sm_count);
+    return launch_pdl(k_bn_fwd<T, kGroup, kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(kLnThreads), kFwdSmem<T>,
                       stream, static_cast<const T*>(p.block), static_cast<const T*>(p.residual), gate,
                       static_cast<T*>(p.stream), static_cast<T*>(p.normed), a);
 }
 
-template <typename T, bool kAligned>
+template <typename T, bool kWhole>
 cudaError_t dispatch(const BlockNormProblem& p, const FwdArgs& a, const T* gate, cudaStream_t stream) {
     constexpr int kN = kBnN<T>;
-    if (p.D <= 32 * kN) return run<T, 32, kAligned>(p, a, gate, stream);
-    if (p.D <= 64 * kN) return run<T, 64, kAligned>(p, a, gate, stream);
-    if (p.D <= 128 * kN) return run<T, 128, kAligned>(p, a, gate, stream);
-    if (p.D <= 256 * kN) return run<T, 256, kAligned>(p, a, gate, stream);
-    if (p.D <= 512 * kN) return run<T, 512, kAligned>(p, a, gate, stream);
-    constexpr int kVec = kAligned ? 16 / static_cast<int>(sizeof(T)) : 1;
-    return launch_pdl(k_bn_fwd_long<T, kVec>, dim3(static_cast<unsigned>(p.T)), dim3(kLnThreads), 0, stream,
-                      static_cast<const T*>(p.block), static_cast<const T*>(p.residual), gate,
-                      static_cast<T*>(p.stream), static_cast<T*>(p.normed), a);
+    const int32_t held = kWhole ? p.D : p.D + 16 / static_cast<int>(sizeof(T)) - 1;  // with what comes before the row
+    if (held <= 32 * kN) return run<T, 32, kWhole>(p, a, gate, stream);
+    if (held <= 64 * kN) return run<T, 64, kWhole>(p, a, gate, stream);
+    if (held <= 128 * kN) return run<T, 128, kWhole>(p, a, gate, stream);
+    if (held <= 256 * kN) return run<T, 256, kWhole>(p, a, gate, stream);
+    return run<T, 512, kWhole>(p, a, gate, stream);
 }
 
 template <typename T>
 cudaError_t of_type(const BlockNormProblem& p, cudaStream_t stream) {
     const FwdArgs a{param(p.post_gamma, p.param_dtype), param(p.gate_per_token ? nullptr : p.gate, p.param_dtype),
                     param(p.pre_gamma, p.param_dtype), p.post_rstd, p.pre_rstd, p.T, p.D, p.residual_scale, p.eps};
+    constexpr int kC = 16 / static_cast<int>(sizeof(T));
     const T* gate = p.gate_per_token ? static_cast<const T*>(p.gate) : nullptr;
-    const int64_t bytes = static_cast<int64_t>(p.D) * sizeof(T);
-    const bool whole = rows_aligned16(p.block, bytes) && rows_aligned16(p.residual, bytes) &&
-                       rows_aligned16(p.stream, bytes) && rows_aligned16(p.normed, bytes) && rows_aligned16(gate, bytes);
-    return whole ? dispatch<T, true>(p, a, gate, stream) : dispatch<T, false>(p, a, gate, stream);
+    const bool alike = lie_alike({p.block, p.residual, p.stream, p.normed, gate});
+    const bool whole = alike && rows_aligned16(p.block, static_cast<int64_t>(p.D) * sizeof(T));
+    if (whole && p.D <= kBnMaxHeldD<T>) return dispatch<T, true>(p, a, gate, stream);
+    if (alike && !whole && p.D + kC - 1 <= kBnMaxHeldD<T>) return dispatch<T, false>(p, a, gate, stream);
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(p.T)), dim3(kLnThreads), 0, stream,
+                          static_cast<const T*>(p.block), static_cast<const T*>(p.residual), gate,
+                          static_cast<T*>(p.stream), static_cast<T*>(p.normed), a);
+    };
+    return whole ? go(k_bn_fwd_long<T, kC>) : go(k_bn_fwd_long<T, 1>);
 }
 
 }  // namespace

@@ -2,7 +2,9 @@
 // shared memory that asynchronous copies fill, and the parameters in registers.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "ptx_sm103.cuh"
 #include "train_internal.cuh"
@@ -218,44 +220,134 @@ __device__ __forceinline__ void store_two<__half>(__half* to, float2 v) {
     *reinterpret_cast<__half2*>(to) = __float22half2_rn(v);
 }
 
-// A thread's share of a row in chunks of 16 bytes, as pairs of floats for the instructions that take two. Element e
-// of chunk c is the thread's element c kC + e, in the order of load_params. Elements past the row's end are 0.
-template <typename T, int kGroup, bool kAligned, int kN>
-struct Chunk {
-    using R = Row<T, kGroup, kAligned, kN>;
+// A thread's share of a row in chunks of 16 bytes, as pairs of floats for the instructions that take two. A lane
+// copies and reads only its own chunks.
+//
+// kWhole: every row starts and ends on 16-byte boundaries. Otherwise the chunks are the 16-byte pieces of memory that
+// cover the row, so that rows of any length come and go in 16-byte accesses: the first and last may hold neighbours'
+// elements, which count as 0 and are not written. All tensors have to lie the same way to those pieces, and a
+// group's rows too: `lead` is how many elements of the first piece come before the row.
+template <typename T, int kGroup, bool kWhole, int kN>
+struct Cells {
     static constexpr int kC = 16 / static_cast<int>(sizeof(T)), kPairs = kC / 2, kChunks = kN / kC;
     using Pairs = float2[kPairs];
+    int lane, lead;
+    int32_t D;
 
-    __device__ static bool any(int c, int lane, int32_t D) { return R::index(kAligned ? c : c * kC, lane) < D; }
-    __device__ static void get(const uint8_t* part, const T* base, int64_t row, int32_t D, int c, int lane, Pairs& v) {
-        if constexpr (kAligned) {
-            const auto p = R::get(part, base, row, D, c, lane);
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) v[i] = make_float2(to_float(p.v[2 * i]), to_float(p.v[2 * i + 1]));
-        } else {
-            float t[kC];
-#pragma unroll
-            for (int e = 0; e < kC; ++e)
-                t[e] = R::index(c * kC + e, lane) < D ? to_float(R::get(part, base, row, D, c * kC + e, lane).v[0]) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
-        }
+    // base: any of the tensors; row: any of the group's rows.
+    __device__ Cells(const T* base, int64_t row, int32_t d, int l) : lane(l), lead(0), D(d) {
+        if constexpr (!kWhole)
+            lead = static_cast<int>((reinterpret_cast<uintptr_t>(base) / sizeof(T) + static_cast<uintptr_t>(row) * d) % kC);
     }
-    __device__ static void put(T* base, int64_t row, int32_t D, int c, int lane, const Pairs& v) {
-        if constexpr (kAligned) {
-            Pack<T, kC> p;
+    // The element of the row that is element e of chunk c.
+    __device__ int index(int c, int e) const { return (c * kGroup + lane) * kC + e - (kWhole ? 0 : lead); }
+    __device__ bool any(int c) const { return index(c, 0) < D; }
+    __device__ bool has(int c, int e) const { return index(c, e) >= 0 && index(c, e) < D; }
+    __device__ bool whole(int c) const { return kWhole || (index(c, 0) >= 0 && index(c, kC - 1) < D); }
+
+    __device__ void fetch(uint8_t* part, const T* base, int64_t row, int64_t rows) const {
+        uint8_t* dst = part + 16 * static_cast<int>(threadIdx.x);
+        const T* src = base + row * D;
+        if (kWhole || (row > 0 && row < rows - 1)) {
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) store_two(p.v + 2 * i, v[i]);
-            *reinterpret_cast<Pack<T, kC>*>(base + row * D + R::index(c, lane)) = p;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kC; ++e) {
-                const int j = R::index(c * kC + e, lane);
-                if (j < D) base[row * D + j] = from_float<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
+            for (int c = 0; c < kChunks; ++c)
+                if (any(c)) copy_async16(dst + c * kLnThreads * 16, src + index(c, 0));
+        } else {  // before the tensor's first element and after its last there is nothing to read
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+                if (!any(c)) continue;
+                if ((row > 0 || index(c, 0) >= 0) && (row < rows - 1 || index(c, kC - 1) < D)) {
+                    copy_async16(dst + c * kLnThreads * 16, src + index(c, 0));
+                } else {
+                    for (int e = 0; e < kC; ++e)
+                        if (has(c, e)) reinterpret_cast<T*>(dst + c * kLnThreads * 16)[e] = src[index(c, e)];
+                }
             }
         }
     }
+    // Once the row is there: zeros for the neighbours' elements in the lane's chunks.
+    __device__ void trim(uint8_t* part) const {
+        if constexpr (!kWhole) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!any(c) || whole(c)) continue;
+                auto* at = reinterpret_cast<Pack<T, kC>*>(part + 16 * (c * kLnThreads + static_cast<int>(threadIdx.x)));
+                auto p = *at;
+#pragma unroll
+                for (int e = 0; e < kC; ++e)
+                    if (!has(c, e)) p.v[e] = from_float<T>(0.0f);
+                *at = p;
+            }
+        }
+    }
+    // The lane's chunk c (any(c)) of a row that has been trimmed.
+    __device__ void get(const uint8_t* part, int c, Pairs& v) const {
+        const auto p = *reinterpret_cast<const Pack<T, kC>*>(part + 16 * (c * kLnThreads + static_cast<int>(threadIdx.x)));
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[i] = make_float2(to_float(p.v[2 * i]), to_float(p.v[2 * i + 1]));
+    }
+    __device__ void put(T* base, int64_t row, int c, const Pairs& v) const {
+        T* to = base + row * D;
+        if (kWhole || whole(c)) {
+            Pack<T, kC> p;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) store_two(p.v + 2 * i, v[i]);
+            *reinterpret_cast<Pack<T, kC>*>(to + index(c, 0)) = p;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kC; ++e)
+                if (has(c, e)) to[index(c, e)] = from_float<T>(e % 2 ? v[e / 2].y : v[e / 2].x);
+        }
+    }
+    // The lane's parameters, in the order of its elements.
+    __device__ void params(const Param& a, float none, float2 (&out)[kN / 2]) const {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            float t[kC];
+            if (kWhole) {
+#pragma unroll
+                for (int e = 0; e < kC; ++e) t[e] = none;
+                if (any(c)) load_param<kC>(a, index(c, 0), none, t);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kC; ++e) {
+                    float one[1] = {none};
+                    if (has(c, e)) load_param<1>(a, index(c, e), none, one);
+                    t[e] = one[0];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) out[c * kPairs + i] = make_float2(t[2 * i], t[2 * i + 1]);
+        }
+    }
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Bytes of a tensor's row in a stage of the ring: what a group of all threads needs, or all groups' together.
+template <typename T, int kGroup>
+int tensor_stride(int32_t D) {
+    constexpr int kC = 16 / static_cast<int>(sizeof(T));
+    const int full = kTensorBytes<T, kBnN<T>>;
+    return kGroup < kLnThreads ? full : std::min(full, (static_cast<int>(ceil_div(D, kC)) + 2) * 16);
+}
+
+// Blocks of a grid whose groups keep their rows' way of lying to 16-byte pieces: the stride between a group's rows is
+// a multiple of eight, or each has but one.
+inline int64_t row_blocks(int64_t rows, int rows_per_block, int64_t most) {
+    const int64_t need = ceil_div(rows, rows_per_block);
+    return need <= most ? need : most / 8 * 8;
+}
+
+// Whether the tensors lie the same way to 16-byte pieces of memory (null ones lie any way).
+inline bool lie_alike(std::initializer_list<const void*> tensors) {
+    const void* first = nullptr;
+    for (const void* t : tensors) {
+        if (t && !first) first = t;
+        if (t && (reinterpret_cast<uintptr_t>(t) ^ reinterpret_cast<uintptr_t>(first)) % 16 != 0) return false;
+    }
+    return true;
+}
 
 bool rows_aligned16(const void* p, int64_t row_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0;
