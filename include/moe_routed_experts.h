@@ -773,6 +773,32 @@ moe_status_t moe_layer_fwd_few(const void *x, const void *logits, int32_t dtype,
                                moe_stream_t stream);
 
 /*
+ * The choice of the next token of each row of logits [T,V], from a given number in [0, 1):
+ *   1. The tokens are ordered by logit, largest first, equal ones by the lowest number.
+ *   2. top_k: the first top_k of them are kept.
+ *   3. top_p: of these, the shortest run from the start whose share of the weights of those kept so far,
+ *      w = exp((logit - largest) / temperature), is top_p or more.
+ *   4. min_p: of these, the ones with w >= min_p. The first of the order is always kept.
+ *   5. token[t] is the first token, by number, at which the running sum of the kept weights exceeds uniform[t] times
+ *      their sum; logprob[t] the logarithm of its share of that sum.
+ *   logits       device [T,V] of `dtype` (MOE_DTYPE_*), element-aligned
+ *   uniform      device fp32 [T]; below 0 or not a number counts as 0, 1 or above as the largest number below 1
+ *   temperature  device fp32 [T], or NULL = 1. Not above 2^-60 (0, negative, not a number): the largest logit's first
+ *                token, with logprob 0
+ *   top_k        device int32 [T], or NULL; 0 or less, or V or more: off
+ *   top_p        device fp32 [T], or NULL; 1 or more, or not a number: off; 0 or less keeps one token
+ *   min_p        device fp32 [T], or NULL; 0 or less, or not a number: off
+ *   token        device int32 [T];  logprob  device fp32 [T], or NULL
+ * 1 <= V <= 2^24, T < 2^31. A logit of -inf is never chosen; where there are logits of +inf they share the choice
+ * equally. A row of nothing but -inf, or with a logit that is not a number, gets token -1 and a logprob that is not a
+ * number. Weights are integers in units of 2^-44 (2^-(62 - log2 V) for V above 2^17), good to about 2^-32 of
+ * themselves: their sums are exact, so the choice does not depend on the order of additions.
+ */
+moe_status_t moe_sample(const void *logits, int32_t dtype, const float *uniform, const float *temperature,
+                        const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,
+                        int64_t T, int32_t V, moe_stream_t stream);
+
+/*
  * Reads the device status word at the start of `workspace` (a forward, backward, routing or
  * vocabulary-loss workspace) into *device_bits (host memory): 0, or an OR of MOE_DEV_* bits raised
  * since the last moe_fwd_dispatch / moe_routed_experts_fwd / moe_routing / moe_lm_* / moe_*_fwd_few on

@@ -52,6 +52,7 @@ __all__ = [
     "moe_few_workspace_bytes",
     "moe_routed_experts_fwd_few",
     "moe_layer_fwd_few",
+    "moe_sample",
     "MOE_WEIGHT_W13",
     "MOE_WEIGHT_W2",
     "moe_get_status",

@@ -137,6 +137,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 [vp, vp, vp, i32, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
             "moe_layer_fwd_few": (
                 [vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp], ctypes.c_int),
+            "moe_sample": ([vp, i32, vp, vp, vp, vp, vp, vp, vp, i64, i32, vp], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -936,3 +937,19 @@ def moe_layer_fwd_few(x, logits, w13, w2, topk_ids, topk_scores, out, workspace,
         px, pz, 1 if bf16 else 0, 1 if normalize else 0, p13, p2, pi,
         _operand(topk_scores, "topk_scores", torch.float32, (T, K), dev), _operand(out, "out", torch.bfloat16, (T, D), dev),
         T, D, F, E, K, _workspace(workspace, dev), workspace.numel(), _stream_of(stream, dev)))
+
+
+def moe_sample(logits, uniform, token, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None,
+               stream=None) -> None:
+    """The next token [T] int32 of each row of logits [T,V] (fp32, bf16 or fp16) for the numbers uniform [T] fp32 in
+    [0, 1), and the logarithm [T] fp32 of its probability among the tokens that were kept (None: not wanted).
+    temperature, top_p and min_p [T] fp32 and top_k [T] int32 hold each row's own (None: 1, and off); a temperature of 0
+    takes the largest logit. A row without a choice (nothing but -inf, or a NaN) gets token -1."""
+    T, V, dev, pz = _rows(logits, "logits", MOE_DTYPE)
+    f32, one = torch.float32, (T,)
+    _check("moe_sample", load().moe_sample(
+        pz, MOE_DTYPE[logits.dtype], _operand(uniform, "uniform", f32, one, dev),
+        _optional(temperature, "temperature", f32, one, dev), _optional(top_k, "top_k", torch.int32, one, dev),
+        _optional(top_p, "top_p", f32, one, dev), _optional(min_p, "min_p", f32, one, dev),
+        _operand(token, "token", torch.int32, one, dev), _optional(logprob, "logprob", f32, one, dev), T, V,
+        _stream_of(stream, dev)))

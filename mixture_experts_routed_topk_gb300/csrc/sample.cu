@@ -1,0 +1,583 @@
+// sample.cu -- the choice of the next token of each row of logits, from a given uniform number.
+//
+//   order      tokens by logit, largest first, equal ones by the lowest number
+//   kept       the first top_k of them; of these the shortest run whose share of the probabilities
+//              softmax(z / temperature) of those top_k reaches top_p; of these the ones with at least min_p times the
+//              largest probability: always a run from the start of the order, cut at one (logit, number)
+//   token      the first, by number, whose running sum of kept probabilities exceeds u times their sum
+//
+// Where many small probabilities are added up, two ways of adding disagree about which token a number falls to. So
+// a weight exp((z - max) / temperature) is an integer in units of 2^-shift (44 bits for usual vocabularies), made
+// from a logarithm in two floats, a table of 2^(j/256) and a cubic, to about 2^-32 of itself; sums of them are exact
+// and in any order the same, and cuts and choice are integer comparisons. A row gives the same token whatever the
+// grid, and the one that 64-bit arithmetic gives but for numbers within some 2^-32 of a border.
+//
+// A row is shared by a cluster of one to eight blocks, each of which owns a run of it. Filters need one histogram of
+// the row: 16 bins to each halving of the weight, with counts and weights, merged over the cluster. The cut lies in
+// one bin; its tokens (some hundreds) go to the first block, which sorts them. Bins with more tokens than the
+// list holds are split again by the logits' bits, down to a single logit, whose ties are cut by number. Bound by
+// latency for a few rows (a handful of cluster barriers), by instruction issue for many: some 30 instructions to a
+// weight, where reading the logits alone takes a quarter of that time.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "exp2_table.cuh"
+#include "ptx_sm103.cuh"
+#include "serve_internal.cuh"
+#include "train_internal.cuh"
+
+namespace moe {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr int kList = 2048;  // tokens of a bin that are sorted
+constexpr int kPerOctave = 16;
+
+struct SampleArgs {
+    const float *uniform, *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    int32_t* token;
+    float* logprob;
+    int32_t V;
+    int shift;  // weights are in units of 2^-shift
+};
+
+struct Histogram {
+    uint32_t count[kBins], lo[kBins], hi[kBins];
+};
+struct Totals {
+    uint64_t weight[kBins];
+    uint32_t count[kBins];
+};
+// Where a cut lies: kept are the tokens of larger keys, and of this key those up to this number.
+struct Cut {
+    uint32_t key;
+    int32_t last;
+};
+
+struct SampleSmem {
+    uint64_t table[256];
+    Histogram hist;
+    Totals merged;     // this block's share of the cluster's histogram
+    Totals first;      // the whole cluster's, by weight
+    Totals split;      // of one bin, by key
+    uint64_t list[kList];
+    uint64_t sums[kWarps + 1];
+    uint32_t counts[kWarps + 1];
+    uint32_t listed;
+    uint64_t best;     // this block's largest key and its first token
+    uint64_t total;    // this block's kept weight
+    Cut cut;           // the first block's answer
+    uint64_t cut_weight;
+    int32_t found_bin;
+    uint32_t before_count;
+    uint64_t before_weight;
+    int32_t chosen;    // the block's answer in a search by number, or -1
+    float c_hi, c_lo;  // 256 log2(e) / temperature
+};
+
+template <typename T>
+struct Row {
+    static constexpr int kC = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kStep = 32 * kC;  // tokens that a warp takes at once
+    const T* z;
+    int32_t V;
+    int lead;               // elements of the first 16-byte piece that come before the row
+    int32_t begin, end;     // this warp's steps
+
+    // The keys of a lane's tokens in a step, in order of their numbers; 0 for none. Returns the first one's number.
+    __device__ int32_t load(int32_t step, int lane, uint32_t (&key)[kC]) const {
+        const int32_t j = (step * 32 + lane) * kC - lead;
+        if (j >= 0 && j + kC <= V) {
+            T v[kC];
+            *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(z + j));
+#pragma unroll
+            for (int e = 0; e < kC; ++e) key[e] = order_key(to_float(v[e]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < kC; ++e) key[e] = j + e >= 0 && j + e < V ? order_key(to_float(z[j + e])) : 0u;
+        }
+        return j;
+    }
+};
+
+// A weight from a logit, the row's largest and 256 log2(e) / temperature in two floats.
+struct Weigh {
+    const uint64_t* table;
+    float max, c_hi, c_lo;
+    int shift;
+
+    // 256 log2 of the weight; the part that a float does not hold in `rest`.
+    __device__ float exponent(float z, float* rest) const {
+        const float d = z - max, b = z - d;
+        const float lost = (z - (d + b)) + (b - max);  // z - max is d + lost
+        const float p = d * c_hi;
+        *rest = fmaf(d, c_lo, fmaf(lost, c_hi, fmaf(d, c_hi, -p)));
+        return p;
+    }
+    __device__ uint64_t operator()(float z) const {
+        if (z == max) return uint64_t{1} << shift;  // also where both are infinite
+        float rest;
+        const float p = exponent(z, &rest);
+        if (!(p > -256.0f * (shift + 1))) return 0u;
+        const int k = __float2int_rd(p);
+        const float x = ((p - static_cast<float>(k)) + rest) * (0.69314718056f / 256.0f);
+        const float f = x * fmaf(x, fmaf(x, 1.0f / 6.0f, 0.5f), 1.0f);  // 2^(..) - 1
+        const uint64_t t = table[k & 255];
+        const int64_t add = static_cast<int64_t>(__float2int_rn(f * 4294967296.0f)) * static_cast<int64_t>(t >> 32);
+        const int by = 62 - shift - (k >> 8);
+        return by > 63 ? 0u : (t + static_cast<uint64_t>(add)) >> by;
+    }
+    // Bins go down by weight; the last holds all that is left.
+    __device__ int bin(float z) const {
+        if (z == max) return 0;
+        const float t = (z - max) * c_hi * (-kPerOctave / 256.0f);
+        return t < kBins - 1 ? static_cast<int>(t) : kBins - 1;
+    }
+};
+
+__device__ __forceinline__ uint64_t warp_upto(uint64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint64_t warp_total(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <typename T>
+struct Sampler {
+    SampleSmem& sm;
+    cg::cluster_group cluster;
+    Row<T> row;
+    Weigh weigh;
+    int rank, ranks, lane, warp, tid;
+
+    // f(number of the first, keys) for each of the warp's steps.
+    template <class F>
+    __device__ void each(F f) const {
+        for (int32_t s = row.begin; s < row.end; ++s) {
+            uint32_t key[Row<T>::kC];
+            const int32_t j = row.load(s, lane, key);
+            f(j, key);
+        }
+    }
+
+    __device__ void clear_histogram() {
+        for (int b = tid; b < kBins; b += kThreads) sm.hist.count[b] = sm.hist.lo[b] = sm.hist.hi[b] = 0u;
+        __syncthreads();
+    }
+    __device__ void put(int b, uint64_t w) {
+        atomicAdd(&sm.hist.count[b], 1u);
+        if (w == 0u) return;
+        const uint32_t lo = static_cast<uint32_t>(w);
+        const uint32_t old = atomicAdd(&sm.hist.lo[b], lo);
+        const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
+        if (hi) atomicAdd(&sm.hist.hi[b], hi);
+    }
+    // The cluster's histogram into `out` of every block: each block adds up a share of the bins, then all read them.
+    __device__ void merge(Totals& out) {
+        const int share = kBins / ranks;
+        cluster.sync();
+        for (int b = tid; b < share; b += kThreads) {
+            uint64_t w = 0u;
+            uint32_t n = 0u;
+            for (int r = 0; r < ranks; ++r) {
+                const Histogram* h = cluster.map_shared_rank(&sm.hist, r);
+                const int at = rank * share + b;
+                n += h->count[at];
+                w += (static_cast<uint64_t>(h->hi[at]) << 32) + h->lo[at];
+            }
+            sm.merged.count[b] = n;
+            sm.merged.weight[b] = w;
+        }
+        cluster.sync();
+        for (int b = tid; b < kBins; b += kThreads) {
+            const Totals* m = cluster.map_shared_rank(&sm.merged, b / share);
+            out.count[b] = m->count[b % share];
+            out.weight[b] = m->weight[b % share];
+        }
+        __syncthreads();
+    }
+    // The first bin at which the running count, or weight, reaches the target: found_bin, and what comes before it.
+    // kBins - 1 where none does.
+    __device__ void find_bin(const Totals& t, bool by_count, uint64_t target) {
+        constexpr int kEach = kBins / kThreads;
+        uint32_t n = 0u;
+        uint64_t w = 0u;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) n += t.count[tid * kEach + i], w += t.weight[tid * kEach + i];
+        uint64_t n_upto = warp_upto(n, lane), w_upto = warp_upto(w, lane);
+        if (lane == 31) sm.sums[warp] = w_upto, sm.counts[warp] = static_cast<uint32_t>(n_upto);
+        if (tid == 0) sm.found_bin = -1;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) n_upto += sm.counts[i], w_upto += sm.sums[i];
+        uint64_t n_before = n_upto - n, w_before = w_upto - w;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int b = tid * kEach + i;
+            const uint64_t n_to = n_before + t.count[b], w_to = w_before + t.weight[b];
+            const bool reached = by_count ? n_to >= target : w_to >= target;
+            const bool already = by_count ? n_before >= target : w_before >= target;
+            if (b == kBins - 1 ? !already : reached && !already) {
+                sm.found_bin = b;
+                sm.before_count = static_cast<uint32_t>(n_before);
+                sm.before_weight = w_before;
+            }
+            n_before = n_to;
+            w_before = w_to;
+        }
+        __syncthreads();
+    }
+    // Sorts the first block's list of n tokens by key, then number, and cuts it where the target is reached.
+    __device__ void cut_list(int n, bool by_count, uint64_t target, uint32_t before_count, uint64_t before_weight) {
+        int size = 32;
+        while (size < n) size <<= 1;
+        for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~uint64_t{0};
+        __syncthreads();
+        for (int k = 2; k <= size; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                for (int i = tid; i < size / 2; i += kThreads) {
+                    const int a = (i / j) * 2 * j + i % j, b = a + j;
+                    const uint64_t x = sm.list[a], y = sm.list[b];
+                    if ((x > y) == ((a & k) == 0)) sm.list[a] = y, sm.list[b] = x;
+                }
+                __syncthreads();
+            }
+        constexpr int kEach = kList / kThreads;
+        uint64_t w[kEach], own = 0u;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = tid * kEach + i;
+            w[i] = at < n ? weigh(key_value(~static_cast<uint32_t>(sm.list[at] >> 32))) : 0u;
+            own += w[i];
+        }
+        uint64_t upto = warp_upto(own, lane);
+        if (lane == 31) sm.sums[warp] = upto;
+        __syncthreads();
+        uint64_t before = before_weight + upto - own;
+        for (int i = 0; i < warp; ++i) before += sm.sums[i];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = tid * kEach + i;
+            const bool last = at == n - 1;
+            const bool here = by_count ? before_count + at + 1 == target || (last && before_count + n < target)
+                                       : before < target && (before + w[i] >= target || last);
+            if (at < n && here) {
+                sm.cut.key = ~static_cast<uint32_t>(sm.list[at] >> 32);
+                sm.cut.last = static_cast<int32_t>(sm.list[at]);
+                sm.cut_weight = before + w[i];
+            }
+            before += w[i];
+        }
+        __syncthreads();
+    }
+    // The first token, by number, at which the running sum of weight(key, number) over the row exceeds the target;
+    // `own` is this warp's sum of it. Every block gets it (-1 where the sum never does).
+    template <class F>
+    __device__ int32_t search(uint64_t own, uint64_t target, F weight) {
+        if (lane == 0) sm.sums[warp] = own;
+        __syncthreads();
+        uint64_t before = 0u;
+        if (tid == 0) {
+            for (int i = 0; i < kWarps; ++i) before += sm.sums[i];
+            sm.total = before;
+            sm.chosen = -1;
+        }
+        cluster.sync();
+        before = 0u;
+        for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&sm.total, r);
+        for (int i = 0; i < warp; ++i) before += sm.sums[i];
+        if (before <= target && target < before + own) {  // one warp of the cluster
+            for (int32_t s = row.begin; s < row.end; ++s) {
+                uint32_t key[Row<T>::kC];
+                const int32_t j = row.load(s, lane, key);
+                uint64_t w[Row<T>::kC], mine = 0u;
+#pragma unroll
+                for (int e = 0; e < Row<T>::kC; ++e) mine += w[e] = weight(key[e], j + e);
+                const uint64_t upto = warp_upto(mine, lane);
+                const uint64_t step = __shfl_sync(0xffffffffu, upto, 31);
+                if (target < before + step) {
+                    before += upto - mine;
+                    if (before <= target && target < before + mine) {
+#pragma unroll
+                        for (int e = 0; e < Row<T>::kC; ++e) {
+                            if (before <= target && target < before + w[e]) sm.chosen = j + e;
+                            before += w[e];
+                        }
+                    }
+                    break;
+                }
+                before += step;
+            }
+        }
+        cluster.sync();
+        int32_t chosen = -1;
+        for (int r = 0; r < ranks; ++r) chosen = max(chosen, *cluster.map_shared_rank(&sm.chosen, r));
+        return chosen;
+    }
+    template <class F>
+    __device__ uint64_t warp_sum_of(F weight) const {
+        uint64_t own = 0u;
+        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+            for (int e = 0; e < Row<T>::kC; ++e) own += weight(key[e], j + e);
+        });
+        return warp_total(own);
+    }
+    // The cut at which the running count (or weight) of the order reaches the target, and the weight up to it.
+    __device__ Cut select(bool by_count, uint64_t target, uint64_t* upto) {
+        find_bin(sm.first, by_count, target);
+        const int bin = sm.found_bin;
+        uint32_t before_count = sm.before_count;
+        uint64_t before_weight = sm.before_weight;
+        // the last bin was not counted: it holds what is left of the row
+        uint32_t n = bin == kBins - 1 ? static_cast<uint32_t>(row.V) - before_count : sm.first.count[bin];
+        uint32_t lo = 1u, hi = 0xffffffffu;  // the keys that are still in question
+        auto within = [&](uint32_t key) { return key >= lo && key <= hi && weigh.bin(key_value(key)) == bin; };
+        while (n > kList && lo < hi) {
+            const int by = max(0, 22 - __clz(hi - lo));
+            clear_histogram();
+            each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+                for (int e = 0; e < Row<T>::kC; ++e)
+                    if (within(key[e])) put(kBins - 1 - static_cast<int>((key[e] - lo) >> by), weigh(key_value(key[e])));
+            });
+            merge(sm.split);
+            find_bin(sm.split, by_count, by_count ? target - before_count : target - before_weight);
+            const uint32_t part = static_cast<uint32_t>(kBins - 1 - sm.found_bin);
+            n = sm.split.count[sm.found_bin];
+            before_count += sm.before_count;
+            before_weight += sm.before_weight;
+            const uint64_t top = lo + ((static_cast<uint64_t>(part) + 1u) << by) - 1u;
+            lo += part << by;
+            hi = top < hi ? static_cast<uint32_t>(top) : hi;
+        }
+        if (n > kList) {  // equal logits: the first of them by number
+            const uint64_t each_weight = weigh(key_value(lo));
+            uint64_t take = n;
+            if (by_count) take = min(take, target - before_count);
+            else if (each_weight > 0u) take = min(take, (target - before_weight + each_weight - 1u) / each_weight);
+            auto one = [&](uint32_t key, int32_t) { return key == lo ? uint64_t{1} : uint64_t{0}; };
+            *upto = before_weight + take * each_weight;
+            return Cut{lo, search(warp_sum_of(one), take - 1u, one)};
+        }
+        if (rank == 0 && tid == 0) sm.listed = 0u;
+        cluster.sync();
+        uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
+        uint64_t* list = cluster.map_shared_rank(sm.list, 0);
+        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+            for (int e = 0; e < Row<T>::kC; ++e)
+                if (within(key[e])) {
+                    const uint32_t at = atomicAdd(listed, 1u);
+                    if (at < kList) list[at] = (static_cast<uint64_t>(~key[e]) << 32) | static_cast<uint32_t>(j + e);
+                }
+        });
+        cluster.sync();
+        if (rank == 0) cut_list(static_cast<int>(n), by_count, target, before_count, before_weight);
+        cluster.sync();
+        *upto = *cluster.map_shared_rank(&sm.cut_weight, 0);
+        const Cut cut = *cluster.map_shared_rank(&sm.cut, 0);
+        cluster.sync();  // read by all before it is written again
+        return cut;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logits, const SampleArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    SampleSmem& sm = *reinterpret_cast<SampleSmem*>(raw);
+    Sampler<T> s{sm, cg::this_cluster()};
+    s.rank = static_cast<int>(s.cluster.block_rank());
+    s.ranks = static_cast<int>(s.cluster.num_blocks());
+    s.tid = threadIdx.x;
+    s.lane = s.tid & 31;
+    s.warp = s.tid >> 5;
+    const int64_t t = blockIdx.x / s.ranks;
+    if (s.tid < 256) sm.table[s.tid] = kExp2Table[s.tid];
+    Row<T>& row = s.row;
+    row.z = logits + t * a.V;
+    row.V = a.V;
+    row.lead = static_cast<int>(reinterpret_cast<uintptr_t>(row.z) / sizeof(T) % Row<T>::kC);
+    {  // steps in equal runs over the blocks, and over a block's warps
+        const int32_t steps = static_cast<int32_t>((static_cast<int64_t>(a.V) + row.lead + Row<T>::kStep - 1) / Row<T>::kStep);
+        const int32_t per_block = (steps + s.ranks - 1) / s.ranks, per_warp = (per_block + kWarps - 1) / kWarps;
+        const int32_t block_end = min(steps, (s.rank + 1) * per_block);
+        row.begin = min(block_end, s.rank * per_block + s.warp * per_warp);
+        row.end = min(block_end, row.begin + per_warp);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const float tau = a.temperature ? a.temperature[t] : 1.0f;
+    // the largest logit, the first of equals
+    uint64_t best = 0u;
+    s.each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+        for (int e = 0; e < Row<T>::kC; ++e) {
+            const uint64_t v = (static_cast<uint64_t>(key[e]) << 32) | (0xffffffffu - static_cast<uint32_t>(j + e));
+            best = key[e] != 0u && v > best ? v : best;
+        }
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (s.lane == 0) sm.sums[s.warp] = best;
+    __syncthreads();
+    if (s.tid == 0) {
+        for (int i = 1; i < kWarps; ++i) best = max(best, sm.sums[i]);
+        sm.best = best;
+        const double c = 256.0 * 1.4426950408889634 / static_cast<double>(tau);
+        sm.c_hi = static_cast<float>(c);
+        sm.c_lo = static_cast<float>(c - static_cast<double>(sm.c_hi));
+    }
+    s.cluster.sync();
+    for (int r = 0; r < s.ranks; ++r) best = max(best, *s.cluster.map_shared_rank(&sm.best, r));
+    best = max(best, sm.best);
+    const uint32_t top = static_cast<uint32_t>(best >> 32);
+    const float largest = key_value(top);
+    const bool speaks = s.rank == 0 && s.tid == 0;
+    // nothing to choose: a logit that is not a number, or nothing but -inf
+    const bool none = top == 0xffffffffu || largest == -INFINITY;
+    if (none || !(tau > 0x1p-60f)) {
+        if (speaks) {
+            a.token[t] = none ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+            if (a.logprob) a.logprob[t] = none ? NAN : 0.0f;
+        }
+        s.cluster.sync();  // nobody leaves while another may read its memory
+        return;
+    }
+    s.weigh = Weigh{sm.table, largest, sm.c_hi, sm.c_lo, a.shift};
+    const Weigh& weigh = s.weigh;
+    const int32_t k = a.top_k ? a.top_k[t] : 0;
+    const float p = a.top_p ? a.top_p[t] : 1.0f, least = a.min_p ? a.min_p[t] : 0.0f;
+    const bool by_k = k > 0 && k < a.V, by_p = p < 1.0f;
+    Cut cut{1u, 0x7fffffff};  // keeps everything
+    if (by_k || by_p) {
+        s.clear_histogram();
+        s.each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+            for (int e = 0; e < Row<T>::kC; ++e) {
+                const float z = key_value(key[e]);
+                const int b = key[e] == 0u ? kBins - 1 : weigh.bin(z);
+                if (b < kBins - 1) s.put(b, weigh(z));  // the last bin's weights are 0, its count is what is left
+            }
+        });
+        s.merge(sm.first);
+        uint64_t kept = 0u;
+        if (by_k) {
+            cut = s.select(true, static_cast<uint64_t>(k), &kept);
+        } else {
+            uint64_t w = 0u;
+            for (int b = s.tid; b < kBins; b += kThreads) w += sm.first.weight[b];
+            w = warp_total(w);
+            __syncthreads();
+            if (s.lane == 0) sm.sums[s.warp] = w;
+            __syncthreads();
+            for (int i = 0; i < kWarps; ++i) kept += sm.sums[i];
+            __syncthreads();
+        }
+        if (by_p) {
+            const uint64_t share = p > 0.0f ? static_cast<uint64_t>(static_cast<double>(p) * 0x1p64) : 0u;
+            uint64_t need = __umul64hi(share, kept) + (share * kept != 0u ? 1u : 0u);
+            need = max(need, uint64_t{1});
+            const Cut at = s.select(false, need, &kept);
+            if (at.key > cut.key || (at.key == cut.key && at.last < cut.last)) cut = at;
+        }
+    }
+    if (least > 0.0f && !isinf(tau)) {  // the logit at which a weight is min_p of the largest; the largest always stays
+        const double at = static_cast<double>(largest) + static_cast<double>(tau) * log(static_cast<double>(least));
+        const float z = at < static_cast<double>(largest) ? __double2float_ru(at) : largest;
+        const uint32_t key = order_key(z);
+        if (key > cut.key) cut = Cut{key, 0x7fffffff};
+    }
+    auto kept_weight = [&](uint32_t key, int32_t j) -> uint64_t {
+        return key > cut.key || (key == cut.key && j <= cut.last) ? weigh(key_value(key)) : 0u;
+    };
+    const uint64_t own = s.warp_sum_of(kept_weight);
+    // the sum over the cluster, then the number's place in it
+    if (s.lane == 0) sm.sums[s.warp] = own;
+    __syncthreads();
+    if (s.tid == 0) {
+        uint64_t total = 0u;
+        for (int i = 0; i < kWarps; ++i) total += sm.sums[i];
+        sm.total = total;
+    }
+    s.cluster.sync();
+    uint64_t total = 0u;
+    for (int r = 0; r < s.ranks; ++r) total += *s.cluster.map_shared_rank(&sm.total, r);
+    s.cluster.sync();
+    float u = a.uniform[t];
+    u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
+    const uint64_t place = __umul64hi(static_cast<uint64_t>(static_cast<double>(u) * 0x1p64), total);
+    const int32_t token = s.search(own, place, kept_weight);
+    if (speaks) {
+        a.token[t] = token;
+        if (a.logprob) {
+            const double z = static_cast<double>(to_float(row.z[token])), all = ldexp(static_cast<double>(total), -a.shift);
+            const double x = to_float(row.z[token]) == largest ? 0.0 : (z - static_cast<double>(largest)) / static_cast<double>(tau);
+            a.logprob[t] = static_cast<float>(x - log(all));
+        }
+    }
+    s.cluster.sync();
+}
+
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <typename T>
+cudaError_t run(const SampleProblem& p, const SampleArgs& a, cudaStream_t stream) {
+    cudaError_t e = allow_smem<&k_sample<T>>(sizeof(SampleSmem));
+    if (e != cudaSuccess) return e;
+    // blocks to a row: two to an SM in all, each with at least 2048 tokens
+    int ranks = 8;
+    while (ranks > 1 && (p.T * ranks > 2 * static_cast<int64_t>(p.sm_count) || p.V / ranks < 2048)) ranks /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.T * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(SampleSmem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_sample<T>, static_cast<const T*>(p.logits), a);
+}
+
+}  // namespace
+
+moe_status_t launch_sample(const SampleProblem& p, cudaStream_t stream) {
+    SampleArgs a{p.uniform, p.temperature, p.top_p, p.min_p, p.top_k, p.token, p.logprob, p.V, 44};
+    while (a.shift + 1 > 62 || (static_cast<int64_t>(p.V) >> (62 - a.shift)) > 0) --a.shift;  // V weights fit 62 bits
+    const cudaError_t e = p.dtype == MOE_DTYPE_F32    ? run<float>(p, a, stream)
+                          : p.dtype == MOE_DTYPE_BF16 ? run<__nv_bfloat16>(p, a, stream)
+                                                      : run<__half>(p, a, stream);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace moe

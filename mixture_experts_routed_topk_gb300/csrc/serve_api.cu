@@ -108,4 +108,23 @@ moe_status_t moe_layer_fwd_few(const void* x, const void* logits, int32_t dtype,
     return run_few(p, T, workspace, workspace_bytes, stream);
 }
 
+moe_status_t moe_sample(const void* logits, int32_t dtype, const float* uniform, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token, float* logprob,
+                        int64_t T, int32_t V, moe_stream_t stream) {
+    if ((dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) || T < 0 || V <= 0)
+        return MOE_ERR_INVALID_ARG;
+    if (T >= (int64_t{1} << 31) || V > kSampleMaxV) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!logits || !uniform || !token) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype == MOE_DTYPE_F32 ? 4 : 2) || !aligned(uniform, 4) || !aligned(temperature, 4) ||
+        !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(token, 4) || !aligned(logprob, 4))
+        return MOE_ERR_MISALIGNED;
+    DeviceInfo dev;
+    const moe_status_t st = device_info(&dev);
+    if (st != MOE_OK) return st;
+    if (!dev.supported) return MOE_ERR_UNSUPPORTED_DEVICE;
+    const SampleProblem p{logits, dtype, uniform, temperature, top_k, top_p, min_p, token, logprob, T, V, dev.sm_count};
+    return launch_sample(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -37,4 +37,22 @@ struct FewProblem {
 };
 moe_status_t launch_few(const FewProblem& p, cudaStream_t stream);
 
+// The choice of the next token (sample.cu).
+constexpr int32_t kSampleMaxV = 1 << 24;
+struct SampleProblem {
+    const void* logits;        // [T, V] of dtype
+    int32_t dtype;
+    const float* uniform;      // [T]
+    const float* temperature;  // [T] each, or null
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* token;            // [T]
+    float* logprob;            // [T] or null
+    int64_t T;
+    int32_t V;
+    int sm_count;
+};
+moe_status_t launch_sample(const SampleProblem& p, cudaStream_t stream);
+
 }  // namespace moe

@@ -1,10 +1,11 @@
 """64-bit values of the operators of a decoding step, from their definitions, and the error bounds the kernels
 are held to. No package code here. Runs on the tensors' device."""
 
+import math
+
 import torch
 
-import train_ops_ref as R
-from train_ops_ref import ACC, U32, half_step, round_bound
+from train_ops_ref import ACC, U32, round_bound
 
 BF16 = torch.bfloat16
 
@@ -41,3 +42,39 @@ def few(x, ids, scores, w13, w2):
         mag.index_add_(0, t, s.abs() * (h.abs() @ wd.abs().T))
     err = err + (ids.shape[1] + 10) * U32 * mag
     return out, err * 1.01 + round_bound(out, BF16)
+
+
+# ------------------------------------------------------------------------ the choice of the next token
+
+def sample_row(z, u, tau=1.0, k=0, p=1.0, least=0.0):
+    """(token, log of its probability, distance to the nearest border) of one row in 64 bits, step by step. The distance
+    says how far the choice is from another one, as a share of the weights: of the number to the borders of its token,
+    and of the cut by share to the next tokens' running sums."""
+    z = z.double()
+    V = z.numel()
+    if torch.isnan(z).any() or bool((z == -math.inf).all()):
+        return -1, math.nan, math.inf
+    order = torch.sort(z, descending=True, stable=True)[1]
+    if not tau > 2.0 ** -60:
+        return int(order[0]), 0.0, math.inf
+    top = z[order[0]]
+    w = torch.where(z == top, 1.0, torch.exp((z - top) / tau))
+    w = torch.where(z == -math.inf, 0.0, w)
+    kept, near = order, math.inf
+    if 0 < k < V:
+        kept = kept[:k]
+    if p < 1.0:
+        run = w[kept].cumsum(0) / w[kept].sum()
+        n = int((run < p).sum()) + 1 if p > 0 else 1
+        near = float((run[max(0, n - 2):n + 1] - p).abs().min()) if p > 0 else math.inf
+        kept = kept[:n]
+    if least > 0:
+        kept = kept[w[kept] >= min(least, 1.0)]
+    kept = torch.sort(kept)[0]
+    u = min(max(u, 0.0), 1.0 - 2.0 ** -24) if u == u else 0.0
+    run = w[kept].cumsum(0)
+    at = min(int((run <= u * run[-1]).sum()), kept.numel() - 1)
+    share = run / run[-1]
+    if u > 0:
+        near = min(near, float((share - u).abs().min()))
+    return int(kept[at]), math.log(float(w[kept[at]] / run[-1])), near

@@ -129,6 +129,23 @@ def test_few_refusals(lib):
         assert binding.moe_few_workspace_bytes(*sizes) == 0
 
 
+# ---------------------------------------------------------------------- the choice of the next token
+
+def test_sample_refusals(lib):
+    go = lambda **k: lib.moe_sample(
+        v(k.get("z", FAKE)), k.get("dt", 1), v(k.get("u", FAKE)), v(k.get("tau", 0)), v(k.get("k", 0)), v(k.get("p", FAKE)),
+        v(0), v(k.get("token", FAKE)), v(k.get("lp", 0)), k.get("T", 4), k.get("V", 100), None)
+    assert go(T=0) == OK
+    assert go(T=0, z=0) == OK
+    for bad in (dict(T=-1), dict(V=0), dict(dt=3), dict(dt=-1), dict(z=0), dict(u=0), dict(token=0)):
+        assert go(**bad) == INVALID, bad
+    assert go(T=1 << 31) == SHAPE
+    assert go(V=(1 << 24) + 1) == SHAPE
+    for bad in (dict(z=FAKE + 1), dict(dt=0, z=FAKE + 2), dict(u=FAKE + 2), dict(tau=FAKE + 1), dict(k=FAKE + 2),
+                dict(p=FAKE + 2), dict(token=FAKE + 2), dict(lp=FAKE + 1)):
+        assert go(**bad) == MISALIGNED, bad
+
+
 # ---------------------------------------------------------------------- the binding's own checks
 
 def calls(T, D, F, E, K):
@@ -137,11 +154,13 @@ def calls(T, D, F, E, K):
     x, row, ws, p = tensor(T, D), tensor(T, dtype=f32), tensor(1 << 20, dtype=u8), tensor(D)
     w13, w2 = tensor(E, 2, F, D), tensor(E, D, F)
     ids, scores, z = tensor(T, K, dtype=i32), tensor(T, K, dtype=f32), tensor(T, E)
+    number = tensor(T, dtype=i32)
     return {
         "moe_block_norm_fwd": lambda **k: binding.moe_block_norm_fwd(x, x, p, p, p, x, x, row, row, **k),
         "moe_block_norm_bwd": lambda **k: binding.moe_block_norm_bwd(x, x, x, x, p, p, p, row, row, x, x, p, p, p, ws, **k),
         "moe_routed_experts_fwd_few": lambda **k: binding.moe_routed_experts_fwd_few(x, ids, scores, w13, w2, x, ws, **k),
         "moe_layer_fwd_few": lambda **k: binding.moe_layer_fwd_few(x, z, w13, w2, ids, scores, x, ws, **k),
+        "moe_sample": lambda **k: binding.moe_sample(z, row, number, row, row, number, row, row, **k),
     }
 
 
@@ -179,7 +198,7 @@ def test_devices_and_streams(called, name):
 
 @pytest.mark.parametrize("name,size", [("moe_block_norm_fwd", "D"), ("moe_block_norm_bwd", "D"),
                                        ("moe_routed_experts_fwd_few", "F"), ("moe_routed_experts_fwd_few", "K"),
-                                       ("moe_layer_fwd_few", "E"), ("moe_layer_fwd_few", "D")])
+                                       ("moe_layer_fwd_few", "E"), ("moe_layer_fwd_few", "D"), ("moe_sample", "E")])
 def test_sizes_past_32_bits(called, name, size):
     with pytest.raises(ValueError, match="32"):
         calls(**{**SMALL, size: WRAP + SMALL[size]})[name]()
