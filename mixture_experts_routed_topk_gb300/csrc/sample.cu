@@ -91,14 +91,20 @@ struct Row {
     int lead;               // elements of the first 16-byte piece that come before the row
     int32_t begin, end;     // this warp's steps
 
+    __device__ int32_t number(int32_t step, int lane) const { return (step * 32 + lane) * kC - lead; }
+    // Whether all lanes' pieces of the step are the row's.
+    __device__ bool inside(int32_t step) const { return step * kStep >= lead && (step + 1) * kStep - lead <= V; }
+    __device__ static void keys_of(const uint4& piece, uint32_t (&key)[kC]) {
+        T v[kC];
+        *reinterpret_cast<uint4*>(v) = piece;
+#pragma unroll
+        for (int e = 0; e < kC; ++e) key[e] = order_key(to_float(v[e]));
+    }
     // The keys of a lane's tokens in a step, in order of their numbers; 0 for none. Returns the first one's number.
     __device__ int32_t load(int32_t step, int lane, uint32_t (&key)[kC]) const {
-        const int32_t j = (step * 32 + lane) * kC - lead;
+        const int32_t j = number(step, lane);
         if (j >= 0 && j + kC <= V) {
-            T v[kC];
-            *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(z + j));
-#pragma unroll
-            for (int e = 0; e < kC; ++e) key[e] = order_key(to_float(v[e]));
+            keys_of(__ldg(reinterpret_cast<const uint4*>(z + j)), key);
         } else {
 #pragma unroll
             for (int e = 0; e < kC; ++e) key[e] = j + e >= 0 && j + e < V ? order_key(to_float(z[j + e])) : 0u;
@@ -157,6 +163,12 @@ __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
     return v;
 }
 
+// The least weight, 1 or more, that is a share (in units of 2^-64) of a sum.
+__device__ __forceinline__ uint64_t share_of(uint64_t share, uint64_t sum) {
+    const uint64_t need = __umul64hi(share, sum) + (share * sum != 0u ? 1u : 0u);
+    return need > 0u ? need : 1u;
+}
+
 template <typename T>
 struct Sampler {
     SampleSmem& sm;
@@ -165,13 +177,28 @@ struct Sampler {
     Weigh weigh;
     int rank, ranks, lane, warp, tid;
 
-    // f(number of the first, keys) for each of the warp's steps.
+    // f(number of the first, keys) for each of the warp's steps, kAhead of whose loads are on their way at once.
     template <class F>
     __device__ void each(F f) const {
-        for (int32_t s = row.begin; s < row.end; ++s) {
-            uint32_t key[Row<T>::kC];
-            const int32_t j = row.load(s, lane, key);
-            f(j, key);
+        constexpr int kAhead = 4;
+        uint32_t key[Row<T>::kC];
+        for (int32_t first = row.begin; first < row.end; first += kAhead) {
+            if (first + kAhead <= row.end && row.inside(first) && row.inside(first + kAhead - 1)) {
+                uint4 piece[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    piece[i] = __ldg(reinterpret_cast<const uint4*>(row.z + row.number(first + i, lane)));
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    Row<T>::keys_of(piece[i], key);
+                    f(row.number(first + i, lane), key);
+                }
+            } else {
+                for (int32_t s = first; s < min(first + kAhead, row.end); ++s) {
+                    const int32_t j = row.load(s, lane, key);
+                    f(j, key);
+                }
+            }
         }
     }
 
@@ -241,21 +268,52 @@ struct Sampler {
         }
         __syncthreads();
     }
-    // Sorts the first block's list of n tokens by key, then number, and cuts it where the target is reached.
-    __device__ void cut_list(int n, bool by_count, uint64_t target, uint32_t before_count, uint64_t before_weight) {
-        int size = 32;
+    // Sorts the block's list of n numbers.
+    __device__ void sort_list(int n) {
+        int size = 2;
         while (size < n) size <<= 1;
         for (int i = n + tid; i < size; i += kThreads) sm.list[i] = ~uint64_t{0};
         __syncthreads();
         for (int k = 2; k <= size; k <<= 1)
             for (int j = k >> 1; j > 0; j >>= 1) {
                 for (int i = tid; i < size / 2; i += kThreads) {
-                    const int a = (i / j) * 2 * j + i % j, b = a + j;
+                    const int a = (i & ~(j - 1)) * 2 + (i & (j - 1)), b = a + j;
                     const uint64_t x = sm.list[a], y = sm.list[b];
                     if ((x > y) == ((a & k) == 0)) sm.list[a] = y, sm.list[b] = x;
                 }
                 __syncthreads();
             }
+    }
+    // What comes before `own` in the order of the block's threads.
+    __device__ uint64_t before_of(uint64_t own) {
+        const uint64_t upto = warp_upto(own, lane);
+        if (lane == 31) sm.sums[warp] = upto;
+        __syncthreads();
+        uint64_t before = upto - own;
+        for (int i = 0; i < warp; ++i) before += sm.sums[i];
+        __syncthreads();
+        return before;
+    }
+    // The tokens for which which(key) holds go to the first block's list, as keys from the largest and numbers.
+    template <class F>
+    __device__ void gather(F which) {
+        if (rank == 0 && tid == 0) sm.listed = 0u;
+        cluster.sync();
+        uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
+        uint64_t* list = cluster.map_shared_rank(sm.list, 0);
+        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+            for (int e = 0; e < Row<T>::kC; ++e)
+                if (which(key[e])) {
+                    const uint32_t at = atomicAdd(listed, 1u);
+                    if (at < kList) list[at] = (static_cast<uint64_t>(~key[e]) << 32) | static_cast<uint32_t>(j + e);
+                }
+        });
+        cluster.sync();
+    }
+    // Sorts the first block's list of n tokens by key, then number, and cuts it where the target is reached.
+    __device__ void cut_list(int n, bool by_count, uint64_t target, uint32_t before_count, uint64_t before_weight) {
+        sort_list(n);
         constexpr int kEach = kList / kThreads;
         uint64_t w[kEach], own = 0u;
 #pragma unroll
@@ -264,11 +322,7 @@ struct Sampler {
             w[i] = at < n ? weigh(key_value(~static_cast<uint32_t>(sm.list[at] >> 32))) : 0u;
             own += w[i];
         }
-        uint64_t upto = warp_upto(own, lane);
-        if (lane == 31) sm.sums[warp] = upto;
-        __syncthreads();
-        uint64_t before = before_weight + upto - own;
-        for (int i = 0; i < warp; ++i) before += sm.sums[i];
+        uint64_t before = before_weight + before_of(own);
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             const int at = tid * kEach + i;
@@ -284,10 +338,10 @@ struct Sampler {
         }
         __syncthreads();
     }
-    // The first token, by number, at which the running sum of weight(key, number) over the row exceeds the target;
-    // `own` is this warp's sum of it. Every block gets it (-1 where the sum never does).
-    template <class F>
-    __device__ int32_t search(uint64_t own, uint64_t target, F weight) {
+    // The first token, by number, at which the running sum of weight(key, number) over the row exceeds target(the
+    // whole sum); `own` is this warp's part of the sum. Every block gets it (-1 where the sum never does), and the sum.
+    template <class G, class F>
+    __device__ int32_t search(uint64_t own, G target_of, F weight, uint64_t* whole) {
         if (lane == 0) sm.sums[warp] = own;
         __syncthreads();
         uint64_t before = 0u;
@@ -297,8 +351,13 @@ struct Sampler {
             sm.chosen = -1;
         }
         cluster.sync();
-        before = 0u;
-        for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&sm.total, r);
+        before = *whole = 0u;
+        for (int r = 0; r < ranks; ++r) {
+            const uint64_t part = *cluster.map_shared_rank(&sm.total, r);
+            *whole += part;
+            if (r < rank) before += part;
+        }
+        const uint64_t target = target_of(*whole);
         for (int i = 0; i < warp; ++i) before += sm.sums[i];
         if (before <= target && target < before + own) {  // one warp of the cluster
             for (int32_t s = row.begin; s < row.end; ++s) {
@@ -337,6 +396,90 @@ struct Sampler {
         });
         return warp_total(own);
     }
+    // All of the choice by the first block, from its list of the n tokens that come first in the order.
+    struct Filters {
+        uint64_t top_k;   // n or less
+        uint64_t share;   // top_p in units of 2^-64, of `all` or of the first top_k's weight; 0 with !by_p
+        uint64_t all;
+        uint32_t least;   // the smallest key that min_p keeps
+        bool by_k, by_p;
+    };
+    __device__ void choose_from_list(int n, const Filters& f, float u, uint64_t* total, int32_t* token) {
+        constexpr int kEach = kList / kThreads;
+        sort_list(n);
+        if (tid == 0) sm.listed = static_cast<uint32_t>(min(static_cast<uint64_t>(n), f.top_k));
+        uint64_t w[kEach], own = 0u;
+        uint32_t key[kEach];
+        int32_t number[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = tid * kEach + i;
+            key[i] = at < n ? ~static_cast<uint32_t>(sm.list[at] >> 32) : 0u;
+            number[i] = at < n ? static_cast<int32_t>(sm.list[at]) : 0;
+            w[i] = at < n ? weigh(key_value(key[i])) : 0u;
+            own += w[i];
+        }
+        const uint64_t before = before_of(own);
+        // the weight of the first `listed` of them, to everyone
+        auto weight_upto_listed = [&] {
+            const int m = static_cast<int>(sm.listed);
+            uint64_t run = before;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                run += w[i];
+                if (tid * kEach + i == m - 1) sm.cut_weight = run;
+            }
+            __syncthreads();
+            return sm.cut_weight;
+        };
+        if (f.by_p) {
+            const uint64_t base = f.by_k ? weight_upto_listed() : f.all;
+            const uint64_t need = share_of(f.share, base);
+            uint64_t run = before;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (run < need && run + w[i] >= need) atomicMin(&sm.listed, static_cast<uint32_t>(tid * kEach + i + 1));
+                run += w[i];
+            }
+            __syncthreads();
+        }
+        if (f.least > 1u) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (tid * kEach + i > 0 && key[i] < f.least) atomicMin(&sm.listed, static_cast<uint32_t>(tid * kEach + i));
+            __syncthreads();
+        }
+        *total = weight_upto_listed();
+        const int m = static_cast<int>(sm.listed);
+        // the kept ones by number
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (tid * kEach + i < m) sm.list[tid * kEach + i] = (static_cast<uint64_t>(number[i]) << 32) | key[i];
+        __syncthreads();
+        sort_list(m);
+        own = 0u;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = tid * kEach + i;
+            w[i] = at < m ? weigh(key_value(static_cast<uint32_t>(sm.list[at]))) : 0u;
+            own += w[i];
+        }
+        const uint64_t place = place_of(u, *total);
+        uint64_t run = before_of(own);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (run <= place && place < run + w[i]) sm.chosen = static_cast<int32_t>(sm.list[tid * kEach + i] >> 32);
+            run += w[i];
+        }
+        __syncthreads();
+        *token = sm.chosen;
+    }
+    // A number in [0, 1) as a place in a sum.
+    __device__ static uint64_t place_of(float u, uint64_t total) {
+        u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
+        return __umul64hi(static_cast<uint64_t>(static_cast<double>(u) * 0x1p64), total);
+    }
     // The cut at which the running count (or weight) of the order reaches the target, and the weight up to it.
     __device__ Cut select(bool by_count, uint64_t target, uint64_t* upto) {
         find_bin(sm.first, by_count, target);
@@ -372,21 +515,10 @@ struct Sampler {
             else if (each_weight > 0u) take = min(take, (target - before_weight + each_weight - 1u) / each_weight);
             auto one = [&](uint32_t key, int32_t) { return key == lo ? uint64_t{1} : uint64_t{0}; };
             *upto = before_weight + take * each_weight;
-            return Cut{lo, search(warp_sum_of(one), take - 1u, one)};
+            uint64_t ties;
+            return Cut{lo, search(warp_sum_of(one), [&](uint64_t) { return take - 1u; }, one, &ties)};
         }
-        if (rank == 0 && tid == 0) sm.listed = 0u;
-        cluster.sync();
-        uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
-        uint64_t* list = cluster.map_shared_rank(sm.list, 0);
-        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
-#pragma unroll
-            for (int e = 0; e < Row<T>::kC; ++e)
-                if (within(key[e])) {
-                    const uint32_t at = atomicAdd(listed, 1u);
-                    if (at < kList) list[at] = (static_cast<uint64_t>(~key[e]) << 32) | static_cast<uint32_t>(j + e);
-                }
-        });
-        cluster.sync();
+        gather(within);
         if (rank == 0) cut_list(static_cast<int>(n), by_count, target, before_count, before_weight);
         cluster.sync();
         *upto = *cluster.map_shared_rank(&sm.cut_weight, 0);
@@ -463,74 +595,86 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     const int32_t k = a.top_k ? a.top_k[t] : 0;
     const float p = a.top_p ? a.top_p[t] : 1.0f, least = a.min_p ? a.min_p[t] : 0.0f;
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.0f;
-    Cut cut{1u, 0x7fffffff};  // keeps everything
+    // the smallest key that min_p keeps: of the logit at which a weight is min_p of the largest, which always stays
+    uint32_t least_key = 1u;
+    if (least > 0.0f && !isinf(tau)) {
+        const double at = static_cast<double>(largest) + static_cast<double>(tau) * log(static_cast<double>(least));
+        least_key = order_key(at < static_cast<double>(largest) ? __double2float_ru(at) : largest);
+    }
+    const uint64_t share = by_p && p > 0.0f ? static_cast<uint64_t>(static_cast<double>(p) * 0x1p64) : 0u;
+    const float u = a.uniform[t];
+    Cut cut{least_key, 0x7fffffff};
+    uint64_t total = 0u;
+    int32_t token = -1;
+    bool done = false;
     if (by_k || by_p) {
-        s.clear_histogram();
-        s.each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
+        // Counts are enough to find the first top_k; shares need the weights too.
+        auto count = [&](bool weights) {
+            s.clear_histogram();
+            s.each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
-            for (int e = 0; e < Row<T>::kC; ++e) {
-                const float z = key_value(key[e]);
-                const int b = key[e] == 0u ? kBins - 1 : weigh.bin(z);
-                if (b < kBins - 1) s.put(b, weigh(z));  // the last bin's weights are 0, its count is what is left
-            }
-        });
-        s.merge(sm.first);
-        uint64_t kept = 0u;
-        if (by_k) {
-            cut = s.select(true, static_cast<uint64_t>(k), &kept);
-        } else {
+                for (int e = 0; e < Row<T>::kC; ++e) {
+                    const float z = key_value(key[e]);
+                    const int b = key[e] == 0u ? kBins - 1 : weigh.bin(z);
+                    // the last bin's weights are 0, its count is what is left
+                    if (b < kBins - 1) s.put(b, weights ? weigh(z) : 0u);
+                }
+            });
+            s.merge(sm.first);
+        };
+        auto all_weights = [&] {
             uint64_t w = 0u;
             for (int b = s.tid; b < kBins; b += kThreads) w += sm.first.weight[b];
             w = warp_total(w);
             __syncthreads();
             if (s.lane == 0) sm.sums[s.warp] = w;
             __syncthreads();
-            for (int i = 0; i < kWarps; ++i) kept += sm.sums[i];
+            w = 0u;
+            for (int i = 0; i < kWarps; ++i) w += sm.sums[i];
             __syncthreads();
+            return w;
+        };
+        count(!by_k);
+        uint64_t kept = by_k ? 0u : all_weights();
+        const uint64_t need = share_of(share, kept);
+        s.find_bin(sm.first, by_k, by_k ? static_cast<uint64_t>(k) : need);
+        const int bin = sm.found_bin;
+        const uint32_t upto = sm.before_count + (bin < kBins - 1 ? sm.first.count[bin] : kList + 1u);
+        if (upto <= kList) {  // the tokens up to the cut's bin fit the list: the first block does the rest
+            s.gather([&](uint32_t key) { return key != 0u && weigh.bin(key_value(key)) <= bin; });
+            if (s.rank == 0)
+                s.choose_from_list(static_cast<int>(upto),
+                                   {by_k ? static_cast<uint64_t>(k) : ~uint64_t{0}, share, kept, least_key, by_k, by_p}, u,
+                                   &total, &token);
+            done = true;
+        } else {
+            if (by_k) {
+                if (by_p) count(true);  // find_bin's answer for the counts stays the same
+                const Cut at = s.select(true, static_cast<uint64_t>(k), &kept);
+                if (at.key >= cut.key) cut = at;
+            }
+            if (by_p) {
+                const Cut at = s.select(false, share_of(share, kept), &kept);
+                if (at.key > cut.key || (at.key == cut.key && at.last < cut.last)) cut = at;
+            }
         }
-        if (by_p) {
-            const uint64_t share = p > 0.0f ? static_cast<uint64_t>(static_cast<double>(p) * 0x1p64) : 0u;
-            uint64_t need = __umul64hi(share, kept) + (share * kept != 0u ? 1u : 0u);
-            need = max(need, uint64_t{1});
-            const Cut at = s.select(false, need, &kept);
-            if (at.key > cut.key || (at.key == cut.key && at.last < cut.last)) cut = at;
-        }
     }
-    if (least > 0.0f && !isinf(tau)) {  // the logit at which a weight is min_p of the largest; the largest always stays
-        const double at = static_cast<double>(largest) + static_cast<double>(tau) * log(static_cast<double>(least));
-        const float z = at < static_cast<double>(largest) ? __double2float_ru(at) : largest;
-        const uint32_t key = order_key(z);
-        if (key > cut.key) cut = Cut{key, 0x7fffffff};
+    if (!done) {
+        auto kept_weight = [&](uint32_t key, int32_t j) -> uint64_t {
+            return key > cut.key || (key == cut.key && j <= cut.last) ? weigh(key_value(key)) : 0u;
+        };
+        token = s.search(s.warp_sum_of(kept_weight), [&](uint64_t all) { return Sampler<T>::place_of(u, all); },
+                         kept_weight, &total);
     }
-    auto kept_weight = [&](uint32_t key, int32_t j) -> uint64_t {
-        return key > cut.key || (key == cut.key && j <= cut.last) ? weigh(key_value(key)) : 0u;
-    };
-    const uint64_t own = s.warp_sum_of(kept_weight);
-    // the sum over the cluster, then the number's place in it
-    if (s.lane == 0) sm.sums[s.warp] = own;
-    __syncthreads();
-    if (s.tid == 0) {
-        uint64_t total = 0u;
-        for (int i = 0; i < kWarps; ++i) total += sm.sums[i];
-        sm.total = total;
-    }
-    s.cluster.sync();
-    uint64_t total = 0u;
-    for (int r = 0; r < s.ranks; ++r) total += *s.cluster.map_shared_rank(&sm.total, r);
-    s.cluster.sync();
-    float u = a.uniform[t];
-    u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-    const uint64_t place = __umul64hi(static_cast<uint64_t>(static_cast<double>(u) * 0x1p64), total);
-    const int32_t token = s.search(own, place, kept_weight);
     if (speaks) {
         a.token[t] = token;
         if (a.logprob) {
-            const double z = static_cast<double>(to_float(row.z[token])), all = ldexp(static_cast<double>(total), -a.shift);
-            const double x = to_float(row.z[token]) == largest ? 0.0 : (z - static_cast<double>(largest)) / static_cast<double>(tau);
-            a.logprob[t] = static_cast<float>(x - log(all));
+            const float z = to_float(row.z[token]);
+            const double x = z == largest ? 0.0 : (static_cast<double>(z) - static_cast<double>(largest)) / static_cast<double>(tau);
+            a.logprob[t] = static_cast<float>(x - log(ldexp(static_cast<double>(total), -a.shift)));
         }
     }
-    s.cluster.sync();
+    s.cluster.sync();  // nobody leaves while another may read its memory
 }
 
 template <auto kKernel>
