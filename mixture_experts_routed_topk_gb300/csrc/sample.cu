@@ -68,8 +68,9 @@ struct SampleSmem {
     Totals first;      // the whole cluster's, by weight
     Totals split;      // of one bin, by key
     uint64_t list[kList];
-    uint64_t sums[kWarps + 1];
-    uint32_t counts[kWarps + 1];
+    uint64_t runs[kWarps][32];  // a warp's sums over its runs of steps
+    uint64_t sums[kWarps];
+    uint32_t counts[kWarps];
     uint32_t listed;
     uint64_t best;     // this block's largest key and its first token
     uint64_t total;    // this block's kept weight
@@ -80,6 +81,8 @@ struct SampleSmem {
     uint64_t before_weight;
     int32_t chosen;    // the block's answer in a search by number, or -1
     float c_hi, c_lo;  // 256 log2(e) / temperature
+    uint64_t share;    // top_p in units of 2^-64
+    uint32_t least;    // the smallest key that min_p keeps
 };
 
 template <typename T>
@@ -90,6 +93,7 @@ struct Row {
     int32_t V;
     int lead;               // elements of the first 16-byte piece that come before the row
     int32_t begin, end;     // this warp's steps
+    int32_t run;            // steps in a run, of which a warp has up to 32
 
     __device__ int32_t number(int32_t step, int lane) const { return (step * 32 + lane) * kC - lead; }
     // Whether all lanes' pieces of the step are the row's.
@@ -180,10 +184,14 @@ struct Sampler {
     // f(number of the first, keys) for each of the warp's steps, kAhead of whose loads are on their way at once.
     template <class F>
     __device__ void each(F f) const {
+        each_of(row.begin, row.end, f);
+    }
+    template <class F>
+    __device__ void each_of(int32_t begin, int32_t end, F f) const {
         constexpr int kAhead = 4;
         uint32_t key[Row<T>::kC];
-        for (int32_t first = row.begin; first < row.end; first += kAhead) {
-            if (first + kAhead <= row.end && row.inside(first) && row.inside(first + kAhead - 1)) {
+        for (int32_t first = begin; first < end; first += kAhead) {
+            if (first + kAhead <= end && row.inside(first) && row.inside(first + kAhead - 1)) {
                 uint4 piece[kAhead];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
@@ -191,12 +199,12 @@ struct Sampler {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     Row<T>::keys_of(piece[i], key);
-                    f(row.number(first + i, lane), key);
+                    f(first + i, row.number(first + i, lane), key);
                 }
             } else {
-                for (int32_t s = first; s < min(first + kAhead, row.end); ++s) {
+                for (int32_t s = first; s < min(first + kAhead, end); ++s) {
                     const int32_t j = row.load(s, lane, key);
-                    f(j, key);
+                    f(s, j, key);
                 }
             }
         }
@@ -301,7 +309,7 @@ struct Sampler {
         cluster.sync();
         uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
         uint64_t* list = cluster.map_shared_rank(sm.list, 0);
-        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+        each([&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
             for (int e = 0; e < Row<T>::kC; ++e)
                 if (which(key[e])) {
@@ -360,7 +368,12 @@ struct Sampler {
         const uint64_t target = target_of(*whole);
         for (int i = 0; i < warp; ++i) before += sm.sums[i];
         if (before <= target && target < before + own) {  // one warp of the cluster
-            for (int32_t s = row.begin; s < row.end; ++s) {
+            // the run of steps, then the step
+            const uint64_t run = sm.runs[warp][lane];
+            const uint64_t run_upto = before + warp_upto(run, lane);
+            const int at = __ffs(__ballot_sync(0xffffffffu, target < run_upto)) - 1;
+            before = __shfl_sync(0xffffffffu, run_upto - run, at);
+            for (int32_t s = row.begin + at * row.run; s < row.end; ++s) {
                 uint32_t key[Row<T>::kC];
                 const int32_t j = row.load(s, lane, key);
                 uint64_t w[Row<T>::kC], mine = 0u;
@@ -387,14 +400,27 @@ struct Sampler {
         for (int r = 0; r < ranks; ++r) chosen = max(chosen, *cluster.map_shared_rank(&sm.chosen, r));
         return chosen;
     }
+    // The sum of weight(key, number) over the warp's tokens, and over each of its runs of steps.
     template <class F>
     __device__ uint64_t warp_sum_of(F weight) const {
-        uint64_t own = 0u;
-        each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+        uint64_t mine = 0u, whole = 0u;
+        sm.runs[warp][lane] = 0u;
+        __syncwarp();
+        each([&](int32_t s, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
-            for (int e = 0; e < Row<T>::kC; ++e) own += weight(key[e], j + e);
+            for (int e = 0; e < Row<T>::kC; ++e) mine += weight(key[e], j + e);
+            const int32_t n = s - row.begin;
+            if (n % row.run == row.run - 1 || s == row.end - 1) {
+                if (__any_sync(0xffffffffu, mine != 0u)) {
+                    mine = warp_total(mine);
+                    if (lane == 0) sm.runs[warp][n / row.run] = mine;
+                    whole += mine;
+                }
+                mine = 0u;
+            }
         });
-        return warp_total(own);
+        __syncwarp();
+        return whole;
     }
     // All of the choice by the first block, from its list of the n tokens that come first in the order.
     struct Filters {
@@ -477,8 +503,12 @@ struct Sampler {
     }
     // A number in [0, 1) as a place in a sum.
     __device__ static uint64_t place_of(float u, uint64_t total) {
+        // u is m 2^(e - 150) with a 24-bit m; as a 64-bit fraction, cut off below 2^-64
         u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-        return __umul64hi(static_cast<uint64_t>(static_cast<double>(u) * 0x1p64), total);
+        const int e = static_cast<int>(__float_as_uint(u) >> 23);
+        const uint64_t m = (__float_as_uint(u) & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
+        const int up = (e > 0 ? e : 1) - 150 + 64;
+        return __umul64hi(up >= 0 ? m << up : up > -24 ? m >> -up : 0u, total);
     }
     // The cut at which the running count (or weight) of the order reaches the target, and the weight up to it.
     __device__ Cut select(bool by_count, uint64_t target, uint64_t* upto) {
@@ -493,7 +523,7 @@ struct Sampler {
         while (n > kList && lo < hi) {
             const int by = max(0, 22 - __clz(hi - lo));
             clear_histogram();
-            each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
+            each([&](int32_t, int32_t, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
                 for (int e = 0; e < Row<T>::kC; ++e)
                     if (within(key[e])) put(kBins - 1 - static_cast<int>((key[e] - lo) >> by), weigh(key_value(key[e])));
@@ -550,13 +580,14 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         const int32_t block_end = min(steps, (s.rank + 1) * per_block);
         row.begin = min(block_end, s.rank * per_block + s.warp * per_warp);
         row.end = min(block_end, row.begin + per_warp);
+        row.run = (per_warp + 31) / 32;
     }
     griddep_wait();
     griddep_launch_dependents();
     const float tau = a.temperature ? a.temperature[t] : 1.0f;
     // the largest logit, the first of equals
     uint64_t best = 0u;
-    s.each([&](int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+    s.each([&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
         for (int e = 0; e < Row<T>::kC; ++e) {
             const uint64_t v = (static_cast<uint64_t>(key[e]) << 32) | (0xffffffffu - static_cast<uint32_t>(j + e));
@@ -570,9 +601,6 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     if (s.tid == 0) {
         for (int i = 1; i < kWarps; ++i) best = max(best, sm.sums[i]);
         sm.best = best;
-        const double c = 256.0 * 1.4426950408889634 / static_cast<double>(tau);
-        sm.c_hi = static_cast<float>(c);
-        sm.c_lo = static_cast<float>(c - static_cast<double>(sm.c_hi));
     }
     s.cluster.sync();
     for (int r = 0; r < s.ranks; ++r) best = max(best, *s.cluster.map_shared_rank(&sm.best, r));
@@ -590,18 +618,26 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         s.cluster.sync();  // nobody leaves while another may read its memory
         return;
     }
-    s.weigh = Weigh{sm.table, largest, sm.c_hi, sm.c_lo, a.shift};
-    const Weigh& weigh = s.weigh;
     const int32_t k = a.top_k ? a.top_k[t] : 0;
     const float p = a.top_p ? a.top_p[t] : 1.0f, least = a.min_p ? a.min_p[t] : 0.0f;
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.0f;
-    // the smallest key that min_p keeps: of the logit at which a weight is min_p of the largest, which always stays
-    uint32_t least_key = 1u;
-    if (least > 0.0f && !isinf(tau)) {
-        const double at = static_cast<double>(largest) + static_cast<double>(tau) * log(static_cast<double>(least));
-        least_key = order_key(at < static_cast<double>(largest) ? __double2float_ru(at) : largest);
+    if (s.tid == 0) {  // the 64-bit arithmetic, of which an SM has little
+        const double c = 256.0 * 1.4426950408889634 / static_cast<double>(tau);
+        sm.c_hi = static_cast<float>(c);
+        sm.c_lo = static_cast<float>(c - static_cast<double>(sm.c_hi));
+        sm.share = by_p && p > 0.0f ? static_cast<uint64_t>(static_cast<double>(p) * 0x1p64) : 0u;
+        // min_p keeps the logits whose weight is min_p of the largest; the largest always stays
+        sm.least = 1u;
+        if (least > 0.0f && !isinf(tau)) {
+            const double at = static_cast<double>(largest) + static_cast<double>(tau) * log(static_cast<double>(least));
+            sm.least = order_key(at < static_cast<double>(largest) ? __double2float_ru(at) : largest);
+        }
     }
-    const uint64_t share = by_p && p > 0.0f ? static_cast<uint64_t>(static_cast<double>(p) * 0x1p64) : 0u;
+    __syncthreads();
+    s.weigh = Weigh{sm.table, largest, sm.c_hi, sm.c_lo, a.shift};
+    const Weigh& weigh = s.weigh;
+    const uint32_t least_key = sm.least;
+    const uint64_t share = sm.share;
     const float u = a.uniform[t];
     Cut cut{least_key, 0x7fffffff};
     uint64_t total = 0u;
@@ -611,7 +647,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         // Counts are enough to find the first top_k; shares need the weights too.
         auto count = [&](bool weights) {
             s.clear_histogram();
-            s.each([&](int32_t, const uint32_t (&key)[Row<T>::kC]) {
+            s.each([&](int32_t, int32_t, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
                 for (int e = 0; e < Row<T>::kC; ++e) {
                     const float z = key_value(key[e]);
