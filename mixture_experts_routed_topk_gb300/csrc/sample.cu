@@ -19,6 +19,8 @@
 // latency for a few rows (a handful of cluster barriers), by instruction issue for many: some 30 instructions to a
 // weight, where reading the logits alone takes a quarter of that time.
 #include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <atomic>
@@ -72,7 +74,7 @@ struct SampleSmem {
     uint64_t sums[kWarps];
     uint32_t counts[kWarps];
     uint32_t listed;
-    uint64_t best;     // this block's largest key and its first token
+    uint32_t best;     // this block's largest
     uint64_t total;    // this block's kept weight
     Cut cut;           // the first block's answer
     uint64_t cut_weight;
@@ -84,6 +86,31 @@ struct SampleSmem {
     uint64_t share;    // top_p in units of 2^-64
     uint32_t least;    // the smallest key that min_p keeps
 };
+
+// The largest of a piece's elements; not a number where one of them is none.
+__device__ __forceinline__ float larger(float a, float b) {
+    float v;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4& piece);
+template <>
+__device__ __forceinline__ float largest_of<float>(const uint4& p) {
+    return larger(larger(__uint_as_float(p.x), __uint_as_float(p.y)), larger(__uint_as_float(p.z), __uint_as_float(p.w)));
+}
+template <>
+__device__ __forceinline__ float largest_of<__nv_bfloat16>(const uint4& p) {
+    const auto* v = reinterpret_cast<const __nv_bfloat162*>(&p);
+    const float2 m = __bfloat1622float2(__hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3])));
+    return larger(m.x, m.y);
+}
+template <>
+__device__ __forceinline__ float largest_of<__half>(const uint4& p) {
+    const auto* v = reinterpret_cast<const __half2*>(&p);
+    const float2 m = __half22float2(__hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3])));
+    return larger(m.x, m.y);
+}
 
 template <typename T>
 struct Row {
@@ -181,33 +208,37 @@ struct Sampler {
     Weigh weigh;
     int rank, ranks, lane, warp, tid;
 
-    // f(number of the first, keys) for each of the warp's steps, kAhead of whose loads are on their way at once.
-    template <class F>
-    __device__ void each(F f) const {
-        each_of(row.begin, row.end, f);
-    }
-    template <class F>
-    __device__ void each_of(int32_t begin, int32_t end, F f) const {
+    // piece_f(its largest) for each of the lane's pieces that are all the row's; f(step, number of the first, keys) for
+    // the steps in which that was true for some lane, and for the steps at the row's ends, whose pieces are never asked
+    // for their largest. kAhead loads of a warp are on their way at once.
+    template <class P, class F>
+    __device__ void each_where(P piece_f, F f) const {
         constexpr int kAhead = 4;
         uint32_t key[Row<T>::kC];
-        for (int32_t first = begin; first < end; first += kAhead) {
-            if (first + kAhead <= end && row.inside(first) && row.inside(first + kAhead - 1)) {
+        for (int32_t first = row.begin; first < row.end; first += kAhead) {
+            if (first + kAhead <= row.end && row.inside(first) && row.inside(first + kAhead - 1)) {
                 uint4 piece[kAhead];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
                     piece[i] = __ldg(reinterpret_cast<const uint4*>(row.z + row.number(first + i, lane)));
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
+                    if (!__any_sync(0xffffffffu, piece_f(largest_of<T>(piece[i])))) continue;
                     Row<T>::keys_of(piece[i], key);
                     f(first + i, row.number(first + i, lane), key);
                 }
             } else {
-                for (int32_t s = first; s < min(first + kAhead, end); ++s) {
+                for (int32_t s = first; s < min(first + kAhead, row.end); ++s) {
                     const int32_t j = row.load(s, lane, key);
                     f(s, j, key);
                 }
             }
         }
+    }
+    // f for every step.
+    template <class F>
+    __device__ void each(F f) const {
+        each_where([](float) { return true; }, f);
     }
 
     __device__ void clear_histogram() {
@@ -302,14 +333,16 @@ struct Sampler {
         __syncthreads();
         return before;
     }
-    // The tokens for which which(key) holds go to the first block's list, as keys from the largest and numbers.
-    template <class F>
-    __device__ void gather(F which) {
+    // The tokens for which which(key) holds go to the first block's list, as keys from the largest and numbers; listed
+    // is their number, which may be more than the list holds. piece_may: of a piece's largest logit, whether it may have
+    // one.
+    template <class P, class F>
+    __device__ void gather(P piece_may, F which) {
         if (rank == 0 && tid == 0) sm.listed = 0u;
         cluster.sync();
         uint32_t* listed = cluster.map_shared_rank(&sm.listed, 0);
         uint64_t* list = cluster.map_shared_rank(sm.list, 0);
-        each([&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+        each_where(piece_may, [&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
             for (int e = 0; e < Row<T>::kC; ++e)
                 if (which(key[e])) {
@@ -401,24 +434,27 @@ struct Sampler {
         return chosen;
     }
     // The sum of weight(key, number) over the warp's tokens, and over each of its runs of steps.
-    template <class F>
-    __device__ uint64_t warp_sum_of(F weight) const {
+    template <class P, class F>
+    __device__ uint64_t warp_sum_of(P piece_may, F weight) const {
         uint64_t mine = 0u, whole = 0u;
+        int32_t run = 0, run_end = row.begin + row.run;
         sm.runs[warp][lane] = 0u;
         __syncwarp();
-        each([&](int32_t s, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+        auto close = [&] {
+            mine = warp_total(mine);
+            if (lane == 0) sm.runs[warp][run] = mine;
+            whole += mine;
+            mine = 0u;
+        };
+        each_where(piece_may, [&](int32_t s, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+            if (s >= run_end) {
+                close();
+                while (s >= run_end) run_end += row.run, ++run;
+            }
 #pragma unroll
             for (int e = 0; e < Row<T>::kC; ++e) mine += weight(key[e], j + e);
-            const int32_t n = s - row.begin;
-            if (n % row.run == row.run - 1 || s == row.end - 1) {
-                if (__any_sync(0xffffffffu, mine != 0u)) {
-                    mine = warp_total(mine);
-                    if (lane == 0) sm.runs[warp][n / row.run] = mine;
-                    whole += mine;
-                }
-                mine = 0u;
-            }
         });
+        close();
         __syncwarp();
         return whole;
     }
@@ -546,9 +582,9 @@ struct Sampler {
             auto one = [&](uint32_t key, int32_t) { return key == lo ? uint64_t{1} : uint64_t{0}; };
             *upto = before_weight + take * each_weight;
             uint64_t ties;
-            return Cut{lo, search(warp_sum_of(one), [&](uint64_t) { return take - 1u; }, one, &ties)};
+            return Cut{lo, search(warp_sum_of([](float) { return true; }, one), [&](uint64_t) { return take - 1u; }, one, &ties)};
         }
-        gather(within);
+        gather([&](float z) { return weigh.bin(z) <= bin; }, within);
         if (rank == 0) cut_list(static_cast<int>(n), by_count, target, before_count, before_weight);
         cluster.sync();
         *upto = *cluster.map_shared_rank(&sm.cut_weight, 0);
@@ -585,34 +621,49 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     griddep_wait();
     griddep_launch_dependents();
     const float tau = a.temperature ? a.temperature[t] : 1.0f;
-    // the largest logit, the first of equals
-    uint64_t best = 0u;
-    s.each([&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+    // the largest logit
+    uint32_t top = 0u;
+    s.each_where(
+        [&](float z) {
+            top = max(top, order_key(z));
+            return false;
+        },
+        [&](int32_t, int32_t, const uint32_t (&key)[Row<T>::kC]) {
 #pragma unroll
-        for (int e = 0; e < Row<T>::kC; ++e) {
-            const uint64_t v = (static_cast<uint64_t>(key[e]) << 32) | (0xffffffffu - static_cast<uint32_t>(j + e));
-            best = key[e] != 0u && v > best ? v : best;
+            for (int e = 0; e < Row<T>::kC; ++e) top = max(top, key[e]);
+        });
+    // of the cluster's, the largest of every block's v
+    auto cluster_max = [&](uint32_t v) {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (s.lane == 0) sm.counts[s.warp] = v;
+        __syncthreads();
+        if (s.tid == 0) {
+            for (int i = 1; i < kWarps; ++i) v = max(v, sm.counts[i]);
+            sm.best = v;
         }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if (s.lane == 0) sm.sums[s.warp] = best;
-    __syncthreads();
-    if (s.tid == 0) {
-        for (int i = 1; i < kWarps; ++i) best = max(best, sm.sums[i]);
-        sm.best = best;
-    }
-    s.cluster.sync();
-    for (int r = 0; r < s.ranks; ++r) best = max(best, *s.cluster.map_shared_rank(&sm.best, r));
-    best = max(best, sm.best);
-    const uint32_t top = static_cast<uint32_t>(best >> 32);
+        s.cluster.sync();
+        for (int r = 0; r < s.ranks; ++r) v = max(v, *s.cluster.map_shared_rank(&sm.best, r));
+        return v;
+    };
+    top = cluster_max(top);
     const float largest = key_value(top);
     const bool speaks = s.rank == 0 && s.tid == 0;
     // nothing to choose: a logit that is not a number, or nothing but -inf
     const bool none = top == 0xffffffffu || largest == -INFINITY;
     if (none || !(tau > 0x1p-60f)) {
+        uint32_t first = 0u;  // the largest's first token, counted down from 2^32 - 1
+        if (!none) {
+            s.each_where([&](float z) { return order_key(z) == top; },
+                         [&](int32_t, int32_t j, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+                             for (int e = 0; e < Row<T>::kC; ++e)
+                                 if (key[e] == top) first = max(first, 0xffffffffu - static_cast<uint32_t>(j + e));
+                         });
+            s.cluster.sync();  // the last maximum has been read
+            first = cluster_max(first);
+        }
         if (speaks) {
-            a.token[t] = none ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best));
+            a.token[t] = none ? -1 : static_cast<int32_t>(0xffffffffu - first);
             if (a.logprob) a.logprob[t] = none ? NAN : 0.0f;
         }
         s.cluster.sync();  // nobody leaves while another may read its memory
@@ -644,7 +695,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     int32_t token = -1;
     bool done = false;
     if (by_k || by_p) {
-        // Counts are enough to find the first top_k; shares need the weights too.
+        // Counts are enough to find the first top_k, shares need the weights too.
         auto count = [&](bool weights) {
             s.clear_histogram();
             s.each([&](int32_t, int32_t, const uint32_t (&key)[Row<T>::kC]) {
@@ -670,14 +721,45 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
             __syncthreads();
             return w;
         };
-        count(!by_k);
-        uint64_t kept = by_k ? 0u : all_weights();
-        const uint64_t need = share_of(share, kept);
-        s.find_bin(sm.first, by_k, by_k ? static_cast<uint64_t>(k) : need);
-        const int bin = sm.found_bin;
-        const uint32_t upto = sm.before_count + (bin < kBins - 1 ? sm.first.count[bin] : kList + 1u);
-        if (upto <= kList) {  // the tokens up to the cut's bin fit the list: the first block does the rest
-            s.gather([&](uint32_t key) { return key != 0u && weigh.bin(key_value(key)) <= bin; });
+        // The first top_k tokens have logits of at least the top_k'th largest of the pieces' largest ones: enough to
+        // list them, with few others, at an eighth (a quarter) of the counting.
+        int bin = kBins - 1;
+        uint32_t upto = 0u;
+        uint64_t kept = 0u;
+        bool listed = false;
+        if (by_k) {
+            s.clear_histogram();
+            s.each_where(
+                [&](float z) {
+                    const int b = weigh.bin(z);
+                    if (b < kBins - 1) s.put(b, 0u);
+                    return false;
+                },
+                [&](int32_t, int32_t, const uint32_t (&key)[Row<T>::kC]) {
+#pragma unroll
+                    for (int e = 0; e < Row<T>::kC; ++e) {
+                        const int b = key[e] == 0u ? kBins - 1 : weigh.bin(key_value(key[e]));
+                        if (b < kBins - 1) s.put(b, 0u);
+                    }
+                });
+            s.merge(sm.first);
+            s.find_bin(sm.first, true, static_cast<uint64_t>(k));
+            bin = sm.found_bin;
+        } else {
+            count(true);
+            kept = all_weights();
+            s.find_bin(sm.first, false, share_of(share, kept));
+            bin = sm.found_bin;
+            if (sm.before_count + sm.first.count[bin] > kList) bin = kBins - 1;
+        }
+        if (bin < kBins - 1) {
+            s.gather([&](float z) { return weigh.bin(z) <= bin; },
+                     [&](uint32_t key) { return key != 0u && weigh.bin(key_value(key)) <= bin; });
+            upto = *s.cluster.map_shared_rank(&sm.listed, 0);
+            listed = upto <= kList;
+            s.cluster.sync();  // read before the first block counts in it again
+        }
+        if (listed) {  // the first block does the rest
             if (s.rank == 0)
                 s.choose_from_list(static_cast<int>(upto),
                                    {by_k ? static_cast<uint64_t>(k) : ~uint64_t{0}, share, kept, least_key, by_k, by_p}, u,
@@ -685,7 +767,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
             done = true;
         } else {
             if (by_k) {
-                if (by_p) count(true);  // find_bin's answer for the counts stays the same
+                count(by_p);
                 const Cut at = s.select(true, static_cast<uint64_t>(k), &kept);
                 if (at.key >= cut.key) cut = at;
             }
@@ -699,8 +781,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         auto kept_weight = [&](uint32_t key, int32_t j) -> uint64_t {
             return key > cut.key || (key == cut.key && j <= cut.last) ? weigh(key_value(key)) : 0u;
         };
-        token = s.search(s.warp_sum_of(kept_weight), [&](uint64_t all) { return Sampler<T>::place_of(u, all); },
-                         kept_weight, &total);
+        const uint64_t own = s.warp_sum_of([&](float z) { return order_key(z) >= cut.key; }, kept_weight);
+        token = s.search(own, [&](uint64_t all) { return Sampler<T>::place_of(u, all); }, kept_weight, &total);
     }
     if (speaks) {
         a.token[t] = token;
