@@ -14,10 +14,11 @@
 // a lane's wait for its own copies, and no warp waits for another until a tile's sums meet. Measured on the way
 // (1 token, D = 7168, F = 2048, 8 experts; the weights alone take 104 us at the copy rate): a loading warp with TMA
 // boxes of 2 KB 152 us and a ring filled by TMA for each warp 189 us (issue of small boxes and the chain of barrier,
-// products and refill), loads into three sets of registers 143 us, this 109 us.
+// products and refill), loads into three sets of registers 143 us, this 109 us
+// (115 us since H has two parts).
 //
 //   k_few_gate_up   a tile is 8 gate rows and the same 8 up rows of one expert, over all of D:
-//                   the warps' sums meet in shared memory, SiLU(g) u is written to H (bf16)
+//                   the warps' sums meet in shared memory, SiLU(g) u is written to H (in two bf16 parts)
 //   k_few_down      a tile is up to 16 rows of the output, over all experts and all of F: each warp adds an
 //                   expert's sums, scaled by the tokens' scores in fp32, to its own 16 rows x T in shared
 //                   memory; the warps' sums meet at the end, and out is rounded once
@@ -29,10 +30,10 @@
 //
 // A pair whose score is 0 is passed over: it costs no weights. All sums are fp32, in a fixed order.
 //
-// Measured (calls in a graph, other experts in each): 1 x 2048 x 1408, 6 experts 23 us (15.3 at the copy rate);
-// 1 x 7168 x 2048, 8 experts 109 us (104); 16 tokens there 723 us (724); 32 x 4096 x 1536, 8 of 128 experts 697 us
+// Measured (calls in a graph, other experts in each): 1 x 2048 x 1408, 6 experts 24 us (15.3 at the copy rate);
+// 1 x 7168 x 2048, 8 experts 115 us (104); 16 tokens there 777 us (724); 32 x 4096 x 1536, 8 of 128 experts 707 us
 // (622). Furthest from the weights' time are few experts with many tokens, whose columns cost as much as the weights
-// they meet: 32 x 2048 x 1408, 4 of 8 experts 52 us (20).
+// they meet: 32 x 2048 x 1408, 4 of 8 experts 65 us (20).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,7 +52,8 @@ constexpr int kFewK = 64;                           // elements of K in a piece
 constexpr int kFewF = kFewRows / 2;                 // f values of a gate/up tile
 
 // How a launch is laid out: the most column tiles, warps of a block, blocks that share an SM. A warp's ring has
-// 12 KB: four pieces with one column tile, three with two, two with three or four.
+// 12 KB: of the gate/up kernel four pieces with one column tile, three with two, two with more; of the down kernel,
+// whose columns have two parts, three, two and one.
 template <int kTiles_, int kWarps_, int kBlocks_>
 struct Shape {
     static constexpr int kTiles = kTiles_, kWarps = kWarps_, kBlocks = kBlocks_;
@@ -349,19 +351,22 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there
 __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // A lane's own ring of pieces in shared memory: what it copies there it alone reads, so a wait for its own copies
-// is all the order there is to keep. Unit i of all lanes lies together, without bank conflicts.
+// is all the order there is to keep. Unit i of all lanes lies together, without bank conflicts: the weights', then
+// those of each column tile's parts (x has one, H two).
+template <int kParts>
 struct Ring {
     uint8_t* mine;  // this lane's first unit of place 0
     int slot;       // bytes of a piece: the weights' units, then those of its column tiles
     int depth;      // pieces
     int at = 0;
     __device__ Ring(uint8_t* ring, int tiles, int warp, int lane)
-        : mine(ring + warp * kFewRing + 16 * lane), slot(2048 + 1024 * tiles), depth(tiles == 1 ? 4 : tiles == 2 ? 3 : 2) {}
+        : mine(ring + warp * kFewRing + 16 * lane), slot(2048 + 1024 * kParts * tiles), depth(kFewRing / slot) {}
     __device__ uint32_t place(int i) const { return smem_addr(mine + i * slot); }
     __device__ void get(Weights& w) const {
         if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
         else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
         const uint8_t* p = mine + at * slot;
         w.top.take(p, p + 512);
         w.bottom.take(p + 1024, p + 1536);
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_gate_up(const F
         }
         copy_group();
     };
-    Ring ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
+    Ring<1> ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
     aim();
 #pragma unroll 1
     for (int i = 0; i < ring.depth; ++i) load(ring.place(i));
@@ -526,9 +531,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_gate_up(const F
         for (int o = threadIdx.x; o < kFewF * count; o += S::kThreads) {
             const int f = o & 7, col = o >> 3;
             const float g = sum_of_warps<S>(sm.red, f, col), v = sum_of_warps<S>(sm.red, f + 8, col);
-            // H is rounded to bf16 here, as the large forward's
-            a.h[static_cast<int64_t>(base + col) * a.F + (tile - u * per_expert) * kFewF + f] =
-                __float2bfloat16_rn(g / (1.0f + __expf(-g)) * v);
+            // H goes on in two bf16 parts, which together are good to 2^-17. Rounded to one, as the large forward's, it
+            // made up half of the output's error (2.3e-3 against 1.6e-3 of rounding the output alone), and 5 % less time.
+            const float h = g / (1.0f + __expf(-g)) * v;
+            const __nv_bfloat16 part = __float2bfloat16_rn(h);
+            __nv_bfloat16* to = a.h + static_cast<int64_t>(base + col) * a.F + (tile - u * per_expert) * kFewF + f;
+            to[0] = part;
+            to[static_cast<int64_t>(a.T) * a.K * a.F] = __float2bfloat16_rn(h - __bfloat162float(part));
         }
     }
 }
@@ -573,6 +582,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
         copy16(to + 1024, q, has_bottom);
         copy16(to + 1536, q + 32, has_bottom);
     };
+    const int64_t second = static_cast<int64_t>(a.T) * a.K * a.F;  // from a first part of H to its second
     auto load_columns = [&](uint32_t to) {
         if (ahead.row < rows) {
 #pragma unroll
@@ -581,8 +591,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
                     const int col = 8 * j + (lane >> 2);
                     const bool on = col < coming;
                     const __nv_bfloat16* p = column + (on ? static_cast<int64_t>(col) * a.F : 0) + ahead.p * kFewK;
-                    copy16(to + 2048 + 1024 * j, p, on);
-                    copy16(to + 2560 + 1024 * j, p + 32, on);
+                    copy16(to + 2048 + 2048 * j, p, on);
+                    copy16(to + 2560 + 2048 * j, p + 32, on);
+                    copy16(to + 3072 + 2048 * j, p + second, on);
+                    copy16(to + 3584 + 2048 * j, p + second + 32, on);
                 }
         }
         copy_group();
@@ -591,7 +603,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
         ahead.p += S::kWarps;
         if (ahead.settle(pieces, step, experts)) aim();
     };
-    Ring ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
+    Ring<2> ring(sm.ring, kTiles == 1 ? 1 : most_tiles(plan, experts, lane), warp, lane);
     const Walk begin = ahead;
     aim();
 #pragma unroll 1
@@ -625,7 +637,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
                 for (int j = 0; j < kTiles; ++j)
                     if (j == 0 || 8 * j < count) {
                         Units b;
-                        ring.column(j, b);
+                        ring.column(2 * j, b);
+                        acc.add(j, w, b);
+                        ring.column(2 * j + 1, b);
                         acc.add(j, w, b);
                     }
                 const uint32_t to = ring.place(ring.at);
@@ -722,7 +736,7 @@ moe_status_t launch_few(const FewProblem& p, cudaStream_t stream) {
     // to an SM where the down kernel has no more than one full tile for each (D <= 16 SMs): its tiles would be cut
     // in half for two, and with one block of each kernel on an SM the down kernel is there and has its first
     // weights before the gate/up kernel ends (1 x 2048 x 1408, 6 experts: 24.1 us, against 26.2 with two; 4 x 2048:
-    // 65.7 and 71.2).
+    // 65.7 and 71.2; all with H in one part).
     const int blocks = (p.D <= kFewRows * p.sm_count ? 1 : 2) * p.sm_count;
     if (p.T <= 8) return run<Shape<1, 8, 2>>(a, blocks, stream);
     if (p.T <= 16) return run<Shape<2, 8, 2>>(a, blocks, stream);

@@ -23,8 +23,9 @@ moe_status_t check_few(int64_t T, int32_t D, int32_t F, int32_t E, int32_t K) {
     return MOE_OK;
 }
 
+// The status word, and H [T K, F] in two bf16 parts.
 size_t few_workspace(int64_t T, int32_t F, int32_t K) {
-    return kAlign + (2 * static_cast<size_t>(T) * K * F + kAlign - 1) / kAlign * kAlign;
+    return kAlign + (4 * static_cast<size_t>(T) * K * F + kAlign - 1) / kAlign * kAlign;
 }
 
 // The checks that both entry points share; T = 0 returns before anything is looked at.

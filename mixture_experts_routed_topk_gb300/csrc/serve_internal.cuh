@@ -31,7 +31,7 @@ struct FewProblem {
     const void* w2;       // bf16 [E, D, F]
     void* out;            // bf16 [T, D]
     uint32_t* status;
-    void* h;              // bf16 [T*K, F]
+    void* h;              // bf16 [2, T*K, F]: H in two parts
     int32_t T, D, F, E, K;
     int sm_count;
 };

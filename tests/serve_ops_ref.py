@@ -5,7 +5,7 @@ import math
 
 import torch
 
-from train_ops_ref import ACC, U32, round_bound
+from train_ops_ref import ACC, U32, half_step, round_bound
 
 BF16 = torch.bfloat16
 
@@ -17,7 +17,7 @@ def few(x, ids, scores, w13, w2):
     weights hold.
 
     The bound: an fp32 sum of n products in steps of 16, each cut off, and then 8 warps' sums; H's rounding
-    to bf16; the exponential (2 + 1.2 |g| units); the pairs one after another."""
+    to two bf16 parts; the exponential (2 + 1.2 |g| units); the pairs one after another."""
     T, D = x.shape
     E, _, F, _ = w13.shape
     out = torch.zeros(T, D, dtype=torch.double, device=x.device)
@@ -34,9 +34,9 @@ def few(x, ids, scores, w13, w2):
         silu = g / (1 + torch.exp(-g))
         h = silu * u
         dh = 1.11 * dg * (u.abs() + du) + silu.abs() * du + (6 + 2 * g.abs()) * ACC * h.abs()
-        dh = dh * 1.01 + round_bound(h, BF16)
+        dh = dh * 1.01 + h.abs() * half_step(BF16) ** 2 + 2.0 ** -130
         y = h @ wd.T
-        dy = dh @ wd.abs().T + (F // 16 + 16) * ACC * (h.abs() @ wd.abs().T)
+        dy = dh @ wd.abs().T + 2 * (F // 16 + 16) * ACC * (h.abs() @ wd.abs().T)
         out.index_add_(0, t, s * y)
         err.index_add_(0, t, s.abs() * dy)
         mag.index_add_(0, t, s.abs() * (h.abs() @ wd.abs().T))
