@@ -749,7 +749,9 @@ size_t moe_few_workspace_bytes(int64_t T, int32_t D, int32_t F, int32_t E, int32
  * Arguments, types and alignment as for moe_routed_experts_fwd; a workspace of
  * moe_few_workspace_bytes(T, D, F, E, K), whose first 4 bytes are the status word. T > 32 or T K > 512:
  * MOE_ERR_UNSUPPORTED_SHAPE.
- * Unlike there, H = SiLU(g) u keeps 16 bits more than bf16 has, and the pairs' outputs are scaled and added
+ * Quicker than moe_routed_experts_fwd while an expert has up to about eight tokens; with more of them that
+ * call is (32 tokens with four of 8 experts each take 74 us here, 51 there).
+ * Unlike there, H = SiLU(g) u goes on in two bf16 parts (good to 2^-17), and the pairs' outputs are scaled and added
  * up in fp32: out alone is rounded, once. A pair with a score of 0 is passed over (its expert's weights are not read for
  * it, and need not be finite). An id outside [0, E) sets MOE_DEV_BAD_EXPERT_ID and contributes 0; ids may
  * repeat. A token without pairs gets a row of zeros. out may not overlap x or the weights.
