@@ -283,6 +283,7 @@ struct Sampler {
         constexpr int kEach = kBins / kThreads;
         uint32_t n = 0u;
         uint64_t w = 0u;
+        __syncthreads();  // the last answer has been read by all
 #pragma unroll
         for (int i = 0; i < kEach; ++i) n += t.count[tid * kEach + i], w += t.weight[tid * kEach + i];
         uint64_t n_upto = warp_upto(n, lane), w_upto = warp_upto(w, lane);
@@ -582,7 +583,10 @@ struct Sampler {
             auto one = [&](uint32_t key, int32_t) { return key == lo ? uint64_t{1} : uint64_t{0}; };
             *upto = before_weight + take * each_weight;
             uint64_t ties;
-            return Cut{lo, search(warp_sum_of([](float) { return true; }, one), [&](uint64_t) { return take - 1u; }, one, &ties)};
+            const int32_t last =
+                search(warp_sum_of([](float) { return true; }, one), [&](uint64_t) { return take - 1u; }, one, &ties);
+            cluster.sync();  // read by all before it is written again
+            return Cut{lo, last};
         }
         gather([&](float z) { return weigh.bin(z) <= bin; }, within);
         if (rank == 0) cut_list(static_cast<int>(n), by_count, target, before_count, before_weight);
