@@ -13,6 +13,11 @@
 // There are only two sums over the tokens, whatever is asked for: of dnormed hat, and of da bh (times a gate per
 // token), from which a channel gate's and post_gamma's gradients follow by a factor per channel. They stay in
 // registers; each block writes one row of them, and a second kernel adds the rows in block order.
+//
+// Measured (calls in a graph; in brackets the bytes at the copy rate): 16384 x 7168 bf16 273 us (208), with a gate per
+// token 335 us (277), 4096 x 2048 without a norm after the block 20 us (12), 16384 x 7001 353 us (203), 8192 x 7168 f32
+// 373 us (208). Bound by the two dependent sums of a row where it is not the memory: issue is 50 %, and 122 registers
+// leave no room for a second row. Blocks of 1024 threads took 325 us against 270, one reduction for both sums the same.
 #include <algorithm>
 
 #include "row_ring.cuh"

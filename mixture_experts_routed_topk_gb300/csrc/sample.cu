@@ -16,8 +16,14 @@
 // the row: 16 bins to each halving of the weight, with counts and weights, merged over the cluster. The cut lies in
 // one bin; its tokens (some hundreds) go to the first block, which sorts them. Bins with more tokens than the
 // list holds are split again by the logits' bits, down to a single logit, whose ties are cut by number. Bound by
-// latency for a few rows (a handful of cluster barriers), by instruction issue for many: some 30 instructions to a
-// weight, where reading the logits alone takes a quarter of that time.
+// latency for a few rows (a handful of cluster barriers), by instruction issue for many: a pass over the weights has
+// some 75 instructions for a warp's 32 tokens, one that only looks for the largest logit about 4.
+//
+// Measured (calls in a graph): 1 x 32000 f32 without a filter 10 us, with top-k 17, top-p 22, both 17, min-p 11;
+// 64 x 131072 bf16 33, 28, 99, 28 and 23 us; 256 x 131072 f32 with top-p 296 us, where reading the logits once takes
+// 20. Of the 99 us the histogram takes 24, the list 13 and its sort 13, the last sums 18. Tried without gain: weights
+// without branches and conversions, a histogram without counts; an estimate of the cut from every eighth token, with
+// finer bins around it, took 136 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
