@@ -17,7 +17,7 @@ moe_status_t check_few(int64_t T, int32_t D, int32_t F, int32_t E, int32_t K) {
     if (T < 0 || D <= 0 || F <= 0 || E <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || D % 64 != 0 || F % 64 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T > kFewMaxTokens || T * K > kFewMaxPairs) return MOE_ERR_UNSUPPORTED_SHAPE;
-    // TMA row coordinates and tile numbers are 32-bit
+    // rows of weights and tile numbers are 32-bit
     if (static_cast<int64_t>(E) * 2 * F >= (int64_t{1} << 31) || static_cast<int64_t>(E) * D >= (int64_t{1} << 31))
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
