@@ -52,6 +52,7 @@ namespace {
 constexpr int kFewRows = 16;                        // weight rows of a tile
 constexpr int kFewK = 64;                           // elements of K in a piece
 constexpr int kFewF = kFewRows / 2;                 // f values of a gate/up tile
+constexpr int kUnit = 512;                          // bytes of a 16-byte unit of every lane
 
 // How a launch is laid out: the most column tiles, and rings as deep as two blocks' shared memory holds. A piece in a
 // ring has 2 KB of weights and 1 KB of columns, or 2 KB of H's two parts.
@@ -60,7 +61,8 @@ struct Shape {
     static constexpr int kTiles = kTiles_, kWarps = 8, kBlocks = 2;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kUpDepth = kTiles == 4 ? 3 : 4, kDownDepth = kTiles == 4 ? 2 : 3;
-    static constexpr int kRing = kUpDepth * 3072 > kDownDepth * 4096 ? kUpDepth * 3072 : kDownDepth * 4096;  // a warp's
+    static constexpr int kUpBytes = kUpDepth * 6 * kUnit, kDownBytes = kDownDepth * 8 * kUnit;
+    static constexpr int kRing = kUpBytes > kDownBytes ? kUpBytes : kDownBytes;  // a warp's
 };
 
 struct FewArgs {
@@ -371,7 +373,7 @@ __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_gro
 // while the one before is multiplied made 16 x 7168 x 2048 slower (806 us against 765) and 32 tokens 1 to 6 % faster.
 template <class S, int kParts, int kDepth>
 struct Ring {
-    static constexpr int kSlot = 2048 + 1024 * kParts;
+    static constexpr int kSlot = (4 + 2 * kParts) * kUnit;
     static_assert(kDepth * kSlot <= S::kRing, "fits");
     uint8_t* mine;  // this lane's first unit of place 0
     int at = 0;
@@ -380,10 +382,10 @@ struct Ring {
     __device__ void get(Weights& w, Units (&column)[kParts]) const {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
         const uint8_t* p = mine + at * kSlot;
-        w.top.take(p, p + 512);
-        w.bottom.take(p + 1024, p + 1536);
+        w.top.take(p, p + kUnit);
+        w.bottom.take(p + 2 * kUnit, p + 3 * kUnit);
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) column[i].take(p + 2048 + 1024 * i, p + 2560 + 1024 * i);
+        for (int i = 0; i < kParts; ++i) column[i].take(p + (4 + 2 * i) * kUnit, p + (5 + 2 * i) * kUnit);
     }
     __device__ void next() { at = at + 1 == kDepth ? 0 : at + 1; }
 };
@@ -478,11 +480,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_gate_up(const F
         if (ahead.row < rows) {
             const int k = ahead.p * kFewK;
             copy16(to, gate + k);
-            copy16(to + 512, gate + k + 32);
-            copy16(to + 1024, gate + up + k);
-            copy16(to + 1536, gate + up + k + 32);
-            copy16(to + 2048, column + k, on);
-            copy16(to + 2560, column + k + 32, on);
+            copy16(to + kUnit, gate + k + 32);
+            copy16(to + 2 * kUnit, gate + up + k);
+            copy16(to + 3 * kUnit, gate + up + k + 32);
+            copy16(to + 4 * kUnit, column + k, on);
+            copy16(to + 5 * kUnit, column + k + 32, on);
             ahead.p += S::kWarps;
             if (ahead.settle(pieces, step, per_expert)) aim();
         }
@@ -573,18 +575,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
         const __nv_bfloat16* p = down + ahead.p * kFewK;
         const __nv_bfloat16* q = has_bottom ? p + 8 * static_cast<int64_t>(a.F) : p;
         copy16(to, p, has_top);
-        copy16(to + 512, p + 32, has_top);
-        copy16(to + 1024, q, has_bottom);
-        copy16(to + 1536, q + 32, has_bottom);
+        copy16(to + kUnit, p + 32, has_top);
+        copy16(to + 2 * kUnit, q, has_bottom);
+        copy16(to + 3 * kUnit, q + 32, has_bottom);
     };
     const int64_t second = static_cast<int64_t>(a.T) * a.K * a.F;  // from a first part of H to its second
     auto load_columns = [&](uint32_t to) {
         if (ahead.row < rows) {
             const __nv_bfloat16* p = column + ahead.p * kFewK;
-            copy16(to + 2048, p, on);
-            copy16(to + 2560, p + 32, on);
-            copy16(to + 3072, p + second, on);
-            copy16(to + 3584, p + second + 32, on);
+            copy16(to + 4 * kUnit, p, on);
+            copy16(to + 5 * kUnit, p + 32, on);
+            copy16(to + 6 * kUnit, p + second, on);
+            copy16(to + 7 * kUnit, p + second + 32, on);
         }
         copy_group();
     };
