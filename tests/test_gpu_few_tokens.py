@@ -248,3 +248,15 @@ def test_weights_past_32_bits():
     out, _ = run(x, at, scores, w13, w2)
     same = torch.tensor([[0, 1], [1, 0]], dtype=torch.int32, device="cuda")
     R.check(out, *S.few(x, same, scores, s13, s2), "out")
+
+
+@pytest.mark.parametrize("T,K", [(15, 8), (31, 16)])
+def test_experts_with_every_number_of_tokens(T, K):
+    x, _, scores, w13, w2, _ = make(T, 192, 128, T, K, seed=11)
+    chosen = [[] for _ in range(T)]
+    for count in range(T, 0, -1):  # expert count - 1 goes to the tokens with the fewest so far: T (T + 1) / 2 pairs
+        for t in sorted(range(T), key=lambda t: (len(chosen[t]), t))[:count]:
+            chosen[t].append(count - 1)
+    ids = torch.tensor(chosen, dtype=torch.int32, device="cuda")
+    assert ids.shape == (T, K)
+    compare(x, ids, scores, w13, w2)
