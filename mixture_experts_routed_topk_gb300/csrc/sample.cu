@@ -20,8 +20,8 @@
 // some 75 instructions for a warp's 32 tokens, one that only looks for the largest logit about 4.
 //
 // Measured (calls in a graph): 1 x 32000 f32 without a filter 10 us, with top-k 17, top-p 22, both 17, min-p 11;
-// 64 x 131072 bf16 33, 28, 99, 28 and 23 us; 256 x 131072 f32 with top-p 296 us, where reading the logits once takes
-// 20. Of the 99 us the histogram takes 24, the list 13 and its sort 13, the last sums 18. Tried without gain: weights
+// 64 x 131072 bf16 33, 25, 96, 25 and 23 us; 256 x 131072 f32 with top-p 274 us, where reading the logits once takes
+// 20. Of the 96 us the histogram takes 24, the list 10 and its sort 13, the last sums 18. Tried without gain: weights
 // without branches and conversions, a histogram without counts; an estimate of the cut from every eighth token, with
 // finer bins around it, took 136 us.
 #include <cooperative_groups.h>
@@ -381,6 +381,28 @@ struct Sampler {
         __syncthreads();
         return before;
     }
+    // The smallest key of the bins up to b, which is not the last one. Passes over the row compare keys with it, which
+    // takes a third of the instructions that a token's bin does (256 x 131072 f32, top-p: 276 us against 295). Each warp
+    // searches with 32 keys at a time, near the logit that the bin's number stands for (else seven steps of them took
+    // 1 us).
+    __device__ uint32_t least_key(int b) const {
+        uint32_t below = 0u, key = order_key(weigh.max);  // a key of a later bin, and one of these
+        const float at = weigh.max - static_cast<float>((b + 1) * (256 / kPerOctave)) / weigh.c_hi;
+        const float off = (fabsf(weigh.max) + fabsf(at)) * 0x1p-20f, z_below = at - off, z_key = at + off;
+        if (z_below < z_key && z_key < weigh.max && weigh.bin(z_below) > b && weigh.bin(z_key) <= b)
+            below = order_key(z_below), key = order_key(z_key);
+        while (key - below > 1u) {
+            const uint32_t step = (key - below + 31u) / 32u;
+            const uint32_t mine = min(static_cast<uint32_t>(lane + 1), (key - below) / step) * step + below;
+            const uint32_t in = __ballot_sync(0xffffffffu, weigh.bin(key_value(mine)) <= b);
+            const int first = in ? __ffs(in) - 1 : 31;
+            const uint32_t from = __shfl_sync(0xffffffffu, mine, first > 0 ? first - 1 : 0), to = __shfl_sync(0xffffffffu, mine, first);
+            if (first > 0) below = from;
+            if (in) key = to;
+            else below = to;
+        }
+        return key;
+    }
     // The tokens for which which(key) holds go to the first block's list, as keys from the largest and numbers; listed
     // is their number, which may be more than the list holds. piece_may: of a piece's largest logit, whether it may have
     // one.
@@ -609,8 +631,9 @@ struct Sampler {
         uint64_t before_weight = sm.before_weight;
         // the last bin was not counted: it holds what is left of the row
         uint32_t n = bin == kBins - 1 ? static_cast<uint32_t>(row.V) - before_count : sm.first.count[bin];
-        uint32_t lo = 1u, hi = 0xffffffffu;  // the keys that are still in question
-        auto within = [&](uint32_t key) { return key >= lo && key <= hi && weigh.bin(key_value(key)) == bin; };
+        // the keys that are still in question
+        uint32_t lo = bin == kBins - 1 ? 1u : least_key(bin), hi = bin == 0 ? order_key(weigh.max) : least_key(bin - 1) - 1u;
+        auto within = [&](uint32_t key) { return key >= lo && key <= hi; };
         while (n > kList && lo < hi) {
             const int by = max(0, 22 - __clz(hi - lo));
             clear_histogram();
@@ -642,7 +665,7 @@ struct Sampler {
             cluster.sync();  // read by all before it is written again
             return Cut{lo, last};
         }
-        gather([&](float z) { return weigh.bin(z) <= bin; }, within);
+        gather([&](float z) { return order_key(z) >= lo; }, within);
         if (rank == 0) cut_list(static_cast<int>(n), by_count, target, before_count, before_weight);
         cluster.sync();
         *upto = *cluster.map_shared_rank(&sm.cut_weight, 0);
@@ -811,8 +834,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
             if (sm.before_count + sm.first.count[bin] > kList) bin = kBins - 1;
         }
         if (bin < kBins - 1) {
-            s.gather([&](float z) { return weigh.bin(z) <= bin; },
-                     [&](uint32_t key) { return key != 0u && weigh.bin(key_value(key)) <= bin; });
+            const uint32_t from = s.least_key(bin);
+            s.gather([&](float z) { return order_key(z) >= from; }, [&](uint32_t key) { return key >= from; });
             upto = *s.cluster.map_shared_rank(&sm.listed, 0);
             listed = upto <= kList;
             s.cluster.sync();  // read before the first block counts in it again
