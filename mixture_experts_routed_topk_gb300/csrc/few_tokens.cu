@@ -120,6 +120,14 @@ struct FewSmem {
     }
 };
 
+// Reads of ids, scores and logits go to L2. The down kernel makes its plan before it waits (see there): by then their
+// writer has completed and L2 has what it wrote, but an SM on which no block has waited since may hold older lines in L1.
+__device__ __forceinline__ float from_l2(const float* p) { return __ldcg(p); }
+__device__ __forceinline__ float from_l2(const __nv_bfloat16* p) {
+    return __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(p))));
+}
+__device__ __forceinline__ int32_t from_l2(const int32_t* p) { return __ldcg(p); }
+
 // One token's choice as the router makes it: the K largest logits, equal ones by the lowest id, and their
 // scores. One warp; a round takes the largest key below the last one's, so nothing is marked as taken.
 template <typename L>
@@ -127,7 +135,7 @@ __device__ void choose(const L* row, int32_t E, int32_t K, bool normalize, int l
     constexpr int kHeld = 8;  // keys of a lane that stay in registers: up to 256 experts
     uint32_t key[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) key[i] = 32 * i + lane < E ? order_key(to_float(row[32 * i + lane])) : 0u;
+    for (int i = 0; i < kHeld; ++i) key[i] = 32 * i + lane < E ? order_key(from_l2(row + 32 * i + lane)) : 0u;
     uint32_t last = 0xffffffffu;
     int32_t last_id = -1;
     float m = 0.0f, part = 0.0f;
@@ -139,7 +147,7 @@ __device__ void choose(const L* row, int32_t E, int32_t K, bool normalize, int l
         };
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) look(key[i], 32 * i + lane);
-        for (int32_t e = 32 * kHeld + lane; e < E; e += 32) look(order_key(to_float(row[e])), e);
+        for (int32_t e = 32 * kHeld + lane; e < E; e += 32) look(order_key(from_l2(row + e)), e);
         last = __reduce_max_sync(0xffffffffu, best);
         last_id = static_cast<int32_t>(
             __reduce_min_sync(0xffffffffu, best == last ? static_cast<uint32_t>(at) : 0xffffffffu));
@@ -157,7 +165,7 @@ __device__ void choose(const L* row, int32_t E, int32_t K, bool normalize, int l
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
             if (key[i] != 0u) part += expf(key_value(key[i]) - m);
-        for (int32_t e = 32 * kHeld + lane; e < E; e += 32) part += expf(to_float(row[e]) - m);
+        for (int32_t e = 32 * kHeld + lane; e < E; e += 32) part += expf(from_l2(row + e) - m);
         part = warp_sum(part);
     }
     const float inv = 1.0f / part;
@@ -220,8 +228,8 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, i
     int32_t* ids = reinterpret_cast<int32_t*>(table + a.E);  // [pairs]
     float* scores = reinterpret_cast<float*>(ids + pairs);
     auto given_score = [&](int p) {
-        return a.scores_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.scores)[p])
-                             : static_cast<const float*>(a.scores)[p];
+        return a.scores_bf16 ? from_l2(static_cast<const __nv_bfloat16*>(a.scores) + p)
+                             : from_l2(static_cast<const float*>(a.scores) + p);
     };
     const bool speaks = kFirst && blockIdx.x == 0;  // writes what the caller gets to see
     if (a.logits != nullptr) {
@@ -248,7 +256,7 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, i
             int32_t id = 0;
             float score = 0.0f;
             if (lane < pairs) {
-                id = a.logits ? ids[lane] : a.ids[lane];
+                id = a.logits ? ids[lane] : from_l2(a.ids + lane);
                 score = a.logits ? scores[lane] : given_score(lane);
             }
             const bool bad = static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.E);
@@ -267,7 +275,7 @@ __device__ int make_plan(const FewArgs& a, uint8_t* scratch, const Plan& plan, i
     for (int e = tid; e < a.E; e += S::kThreads) table[e] = 0u;
     if (a.logits == nullptr)
         for (int p = tid; p < pairs; p += S::kThreads) {
-            ids[p] = a.ids[p];
+            ids[p] = from_l2(a.ids + p);
             scores[p] = given_score(p);
         }
     __syncthreads();
@@ -547,8 +555,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_down(const FewA
     FewSmem<S> sm(raw, a.T * a.K);
     const Plan& plan = sm.plan;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // Before griddep_wait(): ids, scores and logits were written by kernels that had completed when the gate/up
-    // kernel passed its own wait, and it lets this one start only after that; nobody writes the weights.
+    // Before griddep_wait(): what the call reads was written by kernels that had completed when the gate/up kernel passed
+    // its own wait, and every block of it lets this one start only after that. The reads here, of ids, scores, logits and
+    // the first weights, go to L2, where those kernels' writes are.
     const int experts = make_plan<S, false>(a, sm.ring, plan, sm.sums);
     const int tiles = (a.D + a.rows - 1) / a.rows, pieces = a.F / kFewK;
     const int first = blockIdx.x, stride = gridDim.x;
