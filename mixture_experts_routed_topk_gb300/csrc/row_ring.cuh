@@ -7,6 +7,7 @@
 #include <initializer_list>
 
 #include "ptx_sm103.cuh"
+#include "row_pieces.cuh"
 #include "train_internal.cuh"
 
 namespace moe {
@@ -230,6 +231,9 @@ __device__ __forceinline__ void store_two<__half>(__half* to, float2 v) {
 template <typename T, int kGroup, bool kWhole, int kN>
 struct Cells {
     static constexpr int kC = 16 / static_cast<int>(sizeof(T)), kPairs = kC / 2, kChunks = kN / kC;
+    // Whether rows may be shorter than a piece. A larger group has rows of more than half its elements.
+    static constexpr bool kShort = kGroup == 32;
+    static_assert(kGroup == 32 || kGroup * kN / 2 >= 2 * kC, "rows of a piece or more");
     using Pairs = float2[kPairs];
     int lane, lead;
     int32_t D;
@@ -248,7 +252,7 @@ struct Cells {
     __device__ void fetch(uint8_t* part, const T* base, int64_t row, int64_t rows) const {
         uint8_t* dst = part + 16 * static_cast<int>(threadIdx.x);
         const T* src = base + row * D;
-        if (kWhole || (row > 0 && row < rows - 1)) {
+        if (kWhole || (row > 0 && row < rows - 1 && neighbours_cover<kShort>(D, kC))) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 if (any(c)) copy_async16(dst + c * kLnThreads * 16, src + index(c, 0));
@@ -256,7 +260,7 @@ struct Cells {
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 if (!any(c)) continue;
-                if ((row > 0 || index(c, 0) >= 0) && (row < rows - 1 || index(c, kC - 1) < D)) {
+                if (piece_inside<kShort>(row, rows, D, index(c, 0), index(c, kC - 1))) {
                     copy_async16(dst + c * kLnThreads * 16, src + index(c, 0));
                 } else {
                     for (int e = 0; e < kC; ++e)
