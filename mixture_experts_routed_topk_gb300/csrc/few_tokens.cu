@@ -540,10 +540,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) k_few_gate_up(const F
             // H goes on in two bf16 parts, which together are good to 2^-17. Rounded to one, as the large forward's, it
             // made up half of the output's error (2.3e-3 against 1.6e-3 of rounding the output alone), and 5 % less time.
             const float h = g / (1.0f + __expf(-g)) * v;
-            const __nv_bfloat16 part = __float2bfloat16_rn(h);
+            // From 0x1.ffp127 on bf16 rounds to infinity: the first part is cut off instead, so that a finite H stays
+            // one; infinity has no second part (infinity less infinity is not a number).
+            const __nv_bfloat16 part = fabsf(h) < 0x1.ffp127f ? __float2bfloat16_rn(h) : __float2bfloat16_rz(h);
+            const float left = isinf(h) ? 0.0f : h - __bfloat162float(part);
             __nv_bfloat16* to = a.h + static_cast<int64_t>(base + col) * a.F + (tile - u * per_expert) * kFewF + f;
             to[0] = part;
-            to[static_cast<int64_t>(a.T) * a.K * a.F] = __float2bfloat16_rn(h - __bfloat162float(part));
+            to[static_cast<int64_t>(a.T) * a.K * a.F] = __float2bfloat16_rn(left);
         }
     }
 }

@@ -1,4 +1,5 @@
-"""The layer for a few tokens where its answer hangs on more than its sums: what the kernel just before wrote."""
+"""The layer for a few tokens where its answer hangs on more than its sums: what the kernel just before wrote, and H
+near the end of its type."""
 
 import pytest
 import torch
@@ -49,3 +50,29 @@ def test_each_call_plans_from_what_was_just_written(route):
             B.moe_routed_experts_fwd_few(x, *one, w13, w2, want[key], ws)
             torch.cuda.synchronize()
         assert torch.equal(outs[i], want[key]), i
+
+
+@pytest.mark.parametrize("tokens", [1, 9, 20])
+def test_h_near_the_end_of_bf16(tokens):
+    """H = g u past bf16's largest number and within fp32's stays finite, beyond fp32's it is infinite; not a number it
+    is only where a formula in any number of bits says so."""
+    D, F = 128, 64
+    x = torch.ones(tokens, D, dtype=BF16, device="cuda")
+    w13, w2 = torch.zeros(5, 2, F, D, dtype=BF16, device="cuda"), torch.zeros(5, D, F, dtype=BF16, device="cuda")
+    at = 11
+    # g = SiLU(g) = 2^64 (1 - 2^-k) in two products, u = 2^64 or -2^64, H = 2^128 (1 - 2^-k)
+    for e, (k, sign) in enumerate([(9, 1.0), (12, -1.0), (20, 1.0)]):
+        w13[e, 0, at, 3], w13[e, 0, at, 70], w13[e, 1, at, 5] = 2.0 ** 64, -2.0 ** (64 - k), sign * 2.0 ** 64
+    w13[3, 0, at, 3], w13[3, 1, at, 5] = 2.0 ** 64, 2.0 ** 64  # 2^128
+    w13[4, 0, at, 3], w13[4, 1, at, 5] = 2.0 ** 64, -2.0 ** 64
+    w2[:, :, at] = 2.0 ** -100
+    want = [2.0 ** 28 * (1 - 2.0 ** -9), -2.0 ** 28 * (1 - 2.0 ** -12), 2.0 ** 28 * (1 - 2.0 ** -20), float("inf"),
+            float("-inf")]
+    ws = B.alloc_workspace(B.moe_few_workspace_bytes(tokens, D, F, 5, 1))
+    for e, value in enumerate(want):
+        out = torch.full_like(x, 7.0)
+        B.moe_routed_experts_fwd_few(x, torch.full((tokens, 1), e, dtype=torch.int32, device="cuda"),
+                                     torch.ones(tokens, 1, device="cuda"), w13, w2, out, ws)
+        got = out.double()
+        assert torch.equal(got, torch.full_like(got, got[0, 0])) and (float(got[0, 0]) == value or
+                                                                      abs(float(got[0, 0]) - value) <= 2.0 ** -8 * abs(value)), e
