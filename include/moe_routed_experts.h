@@ -793,8 +793,10 @@ moe_status_t moe_layer_fwd_few(const void *x, const void *logits, int32_t dtype,
  *   token        device int32 [T];  logprob  device fp32 [T], or NULL
  * 1 <= V <= 2^24, T < 2^31. A logit of -inf is never chosen; where there are logits of +inf they share the choice
  * equally. A row of nothing but -inf, or with a logit that is not a number, gets token -1 and a logprob that is not a
- * number. Weights are integers in units of 2^-44 (2^-(62 - log2 V) for V above 2^17), good to about 2^-32 of
- * themselves: their sums are exact, so the choice does not depend on the order of additions.
+ * number. Weights are whole numbers of units, good to 2^-30 of themselves and less than one unit short; their sums are
+ * exact, so the choice does not depend on the order of additions. The unit is 2^-44 of the largest weight for V < 2^19:
+ * tokens below it are never chosen, and shares are off by 2^-30 + V 2^-44 at most. From there on it is the finest, down to
+ * 2^-61, in which the row's weights sum to less than 2^62, and shares are off by 2^-30 + V 2^-60 at most.
  */
 moe_status_t moe_sample(const void *logits, int32_t dtype, const float *uniform, const float *temperature,
                         const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,

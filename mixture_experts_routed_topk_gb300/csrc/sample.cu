@@ -7,11 +7,13 @@
 //   token      the first, by number, whose running sum of kept probabilities exceeds u times their sum
 //
 // Where many small probabilities are added up, two ways of adding disagree about which token a number falls to. So
-// a weight exp((z - max) / temperature) is an integer in units of 2^-shift (44 bits for usual vocabularies), made
+// a weight exp((z - max) / temperature) is an integer in units of 2^-44, of which each loses less than one, made
 // from a logarithm in two floats, a table of 2^(j/256) and a cubic, to 2^-30 of itself (the floats' roundings add up to
 // 8.4e-10; 4.5e-10 is the most that a million random logits showed); sums of them are exact and in any order the same,
 // and cuts and choice are integer comparisons. A row gives the same token whatever the grid, and the one that 64-bit
-// arithmetic gives but for numbers within 2^-30 of a border.
+// arithmetic gives but for numbers within 2^-30 + V 2^-44 of a border. From V = 2^19 on, where sums could pass 63 bits, a
+// pass of its own finds the finest unit, down to 2^-61, in which the row's own sum stays below 2^62: all tokens together
+// then lose V 2^-60 of it at most. (Taken from 2^18 on, that pass made 64 x 262144 bf16 without a filter 109 us from 56.)
 //
 // A row is shared by a cluster of one to eight blocks, each of which owns a run of it. Filters need one histogram of
 // the row: 16 bins to each halving of the weight, with counts and weights, merged over the cluster. The cut lies in
@@ -54,8 +56,10 @@ struct SampleArgs {
     int32_t* token;
     float* logprob;
     int32_t V;
-    int shift;  // weights are in units of 2^-shift
+    int shift;  // weights are in units of 2^-shift, or of finer ones from kWideV on
 };
+constexpr int kShift = 44;
+constexpr int32_t kWideV = 1 << (63 - kShift);  // fewer of the largest weight stay below 2^63
 
 struct Histogram {
     uint32_t count[kBins], lo[kBins], hi[kBins];
@@ -513,6 +517,21 @@ struct Sampler {
         for (int r = 0; r < ranks; ++r) chosen = max(chosen, *cluster.map_shared_rank(&sm.chosen, r));
         return chosen;
     }
+    // The sum of the warps' parts over the cluster, to everyone.
+    __device__ uint64_t cluster_total(uint64_t own) {
+        if (lane == 0) sm.sums[warp] = own;
+        __syncthreads();
+        if (tid == 0) {
+            own = 0u;
+            for (int i = 0; i < kWarps; ++i) own += sm.sums[i];
+            sm.total = own;
+        }
+        cluster.sync();
+        uint64_t whole = 0u;
+        for (int r = 0; r < ranks; ++r) whole += *cluster.map_shared_rank(&sm.total, r);
+        cluster.sync();  // read by all before it is written again
+        return whole;
+    }
     // The sum of weight(key, number) over the warp's tokens, and over each of its runs of steps.
     template <class P, class F>
     __device__ uint64_t warp_sum_of(P piece_may, F weight) const {
@@ -678,7 +697,8 @@ struct Sampler {
     }
 };
 
-template <typename T>
+// kWide: V is kWideV or more.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logits, const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     SampleSmem& sm = *reinterpret_cast<SampleSmem*>(raw);
@@ -771,6 +791,13 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     __syncthreads();
     s.weigh = Weigh{sm.table, largest, sm.c_hi, sm.c_lo, a.shift};
     const Weigh& weigh = s.weigh;
+    if constexpr (kWide) {
+        // A row whose weights are mostly small gets units as fine as a sum below 2^62 allows. In units of 2^-a.shift each
+        // weight loses less than one, so that all + V bounds the sum in finer ones.
+        const uint64_t all = s.cluster_total(
+            s.warp_sum_of([](float) { return true; }, [&](uint32_t key, int32_t) { return weigh(key_value(key)); }));
+        s.weigh.shift = min(61, a.shift + __clzll(static_cast<long long>(all + static_cast<uint64_t>(a.V))) - 2);
+    }
     const uint32_t least_key = sm.least;
     const uint64_t share = sm.share;
     const float u = a.uniform[t];
@@ -873,7 +900,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         if (a.logprob) {
             const float z = to_float(row.z[token]);
             const double x = z == largest ? 0.0 : (static_cast<double>(z) - static_cast<double>(largest)) / static_cast<double>(tau);
-            a.logprob[t] = static_cast<float>(x - log(ldexp(static_cast<double>(total), -a.shift)));
+            a.logprob[t] = static_cast<float>(x - log(ldexp(static_cast<double>(total), -weigh.shift)));
         }
     }
     s.cluster.sync();  // nobody leaves while another may read its memory
@@ -892,9 +919,9 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
-template <typename T>
+template <typename T, bool kWide>
 cudaError_t run(const SampleProblem& p, const SampleArgs& a, cudaStream_t stream) {
-    cudaError_t e = allow_smem<&k_sample<T>>(sizeof(SampleSmem));
+    cudaError_t e = allow_smem<&k_sample<T, kWide>>(sizeof(SampleSmem));
     if (e != cudaSuccess) return e;
     // blocks to a row: two to an SM in all, each with at least 2048 tokens
     int ranks = 8;
@@ -912,17 +939,22 @@ cudaError_t run(const SampleProblem& p, const SampleArgs& a, cudaStream_t stream
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sample<T>, static_cast<const T*>(p.logits), a);
+    return cudaLaunchKernelEx(&cfg, k_sample<T, kWide>, static_cast<const T*>(p.logits), a);
 }
 
 }  // namespace
 
 moe_status_t launch_sample(const SampleProblem& p, cudaStream_t stream) {
-    SampleArgs a{p.uniform, p.temperature, p.top_p, p.min_p, p.top_k, p.token, p.logprob, p.V, 44};
-    while (a.shift + 1 > 62 || (static_cast<int64_t>(p.V) >> (62 - a.shift)) > 0) --a.shift;  // V weights fit 62 bits
-    const cudaError_t e = p.dtype == MOE_DTYPE_F32    ? run<float>(p, a, stream)
-                          : p.dtype == MOE_DTYPE_BF16 ? run<__nv_bfloat16>(p, a, stream)
-                                                      : run<__half>(p, a, stream);
+    SampleArgs a{p.uniform, p.temperature, p.top_p, p.min_p, p.top_k, p.token, p.logprob, p.V, kShift};
+    if (p.V >= kWideV)
+        while ((p.V >> (62 - a.shift)) > 0) --a.shift;  // V of the largest weight stay below 2^62
+    auto of_type = [&](auto t) {
+        using T = decltype(t);
+        return p.V >= kWideV ? run<T, true>(p, a, stream) : run<T, false>(p, a, stream);
+    };
+    const cudaError_t e = p.dtype == MOE_DTYPE_F32    ? of_type(float{})
+                          : p.dtype == MOE_DTYPE_BF16 ? of_type(__nv_bfloat16{})
+                                                      : of_type(__half{});
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
