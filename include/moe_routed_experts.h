@@ -789,7 +789,7 @@ moe_status_t moe_layer_fwd_few(const void *x, const void *logits, int32_t dtype,
  *                token, with logprob 0
  *   top_k        device int32 [T], or NULL; 0 or less, or V or more: off
  *   top_p        device fp32 [T], or NULL; 1 or more, or not a number: off; 0 or less keeps one token
- *   min_p        device fp32 [T], or NULL; 0 or less, or not a number: off
+ *   min_p        device fp32 [T], or NULL; 0 or less, or not a number: off; above 1 keeps one token
  *   token        device int32 [T];  logprob  device fp32 [T], or NULL
  * 1 <= V <= 2^24, T < 2^31. A logit of -inf is never chosen; where there are logits of +inf they share the choice
  * equally. A row of nothing but -inf, or with a logit that is not a number, gets token -1 and a logprob that is not a

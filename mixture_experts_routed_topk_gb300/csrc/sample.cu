@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     }
     griddep_wait();
     griddep_launch_dependents();
-    const float tau = a.temperature ? a.temperature[t] : 1.0f;
+    const float tau = a.temperature ? a.temperature[t] : 1.0f, least = a.min_p ? a.min_p[t] : 0.0f;
     // the largest logit
     uint32_t top = 0u;
     s.each_where(
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     const bool speaks = s.rank == 0 && s.tid == 0;
     // nothing to choose: a logit that is not a number, or nothing but -inf
     const bool none = top == 0xffffffffu || largest == -INFINITY;
-    if (none || !(tau > 0x1p-60f)) {
+    if (none || !(tau > 0x1p-60f) || least > 1.0f) {  // no weight reaches a min_p above 1: the first of the order alone
         uint32_t first = 0u;  // the largest's first token, counted down from 2^32 - 1
         if (!none) {
             s.each_where([&](float z) { return order_key(z) == top; },
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
         return;
     }
     const int32_t k = a.top_k ? a.top_k[t] : 0;
-    const float p = a.top_p ? a.top_p[t] : 1.0f, least = a.min_p ? a.min_p[t] : 0.0f;
+    const float p = a.top_p ? a.top_p[t] : 1.0f;
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.0f;
     if (s.tid == 0) {  // the 64-bit arithmetic, of which an SM has little
         const double c = 256.0 * 1.4426950408889634 / static_cast<double>(tau);

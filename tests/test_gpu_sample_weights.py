@@ -151,3 +151,22 @@ def test_large_vocabularies(T, V, kw):
             sure += 1
             assert int(token[t]) == want, t
     assert sure >= min(T, 12) - 2
+
+
+@pytest.mark.parametrize("least", [1.0, 1.5, math.inf])
+@pytest.mark.parametrize("V", [50, 5000, 70000])
+@pytest.mark.parametrize("tau", [1.0, math.inf])
+def test_floors_that_only_the_largest_passes(V, tau, least):
+    """w >= min_p keeps the tokens that tie for the largest logit at 1, and above 1 only the first of the order."""
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(16, V, generator=g)
+    ties = torch.stack([torch.randperm(V, generator=g)[:5] for _ in range(16)])
+    z.scatter_(1, ties, 9.0)
+    z[1, ties[1]] = math.inf
+    token, logprob = sample(z, torch.arange(16) / 16.0, temperature=tau, min_p=least)
+    for t in range(16):
+        order = sorted(ties[t].tolist())
+        if least > 1.0:
+            assert int(token[t]) == order[0] and float(logprob[t]) == 0.0, t
+        elif tau == 1.0:
+            assert int(token[t]) == order[int(5 * t / 16)] and abs(float(logprob[t]) + math.log(5)) < 1e-6, t
