@@ -44,12 +44,6 @@ struct BwdRows {
 // The ring: up to four stages of the three to five tensors, at least two.
 constexpr int kBwdSmem = 224 * 1024;
 
-// As plain stores under the condition below, nvcc 13.0 sends a first lane's elements of every group to the first
-// group's place; the tests of short odd rows show it.
-__device__ __forceinline__ void store_shared(float* to, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(smem_addr(to)), "f"(v) : "memory");
-}
-
 // What there is of the block's side: nothing (its gradient is da alone), the block, the block and a gate per token.
 enum Side { kNoBlock, kBlock, kTokenGate };
 
@@ -200,8 +194,8 @@ __global__ void __launch_bounds__(kLnThreads, 1) k_bn_bwd(const BwdRows<T> x, co
         for (int e = 0; e < C::kC; ++e) {
             const int n = c * C::kC + e;
             if (cells.has(c, e)) {
-                store_shared(own + cells.index(c, e), n % 2 ? dpre[n / 2].y : dpre[n / 2].x);
-                store_shared(own + kCols + cells.index(c, e), n % 2 ? dpost[n / 2].y : dpost[n / 2].x);
+                own[cells.index(c, e)] = n % 2 ? dpre[n / 2].y : dpre[n / 2].x;
+                own[kCols + cells.index(c, e)] = n % 2 ? dpost[n / 2].y : dpost[n / 2].x;
             }
         }
     }

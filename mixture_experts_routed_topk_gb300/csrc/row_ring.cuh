@@ -240,8 +240,15 @@ struct Cells {
 
     // base: any of the tensors; row: any of the group's rows.
     __device__ Cells(const T* base, int64_t row, int32_t d, int l) : lane(l), lead(0), D(d) {
-        if constexpr (!kWhole)
+        if constexpr (!kWhole) {
             lead = static_cast<int>((reinterpret_cast<uintptr_t>(base) / sizeof(T) + static_cast<uintptr_t>(row) * d) % kC);
+            // Hidden from the compiler's optimizer, which otherwise relates it to the lane: with nvcc 13.0 stores to
+            // own[index(c, e)] in shared memory under has(c, e), own being the group's part of it, then went to the first
+            // group's part for the chunks that are not whole. A kernel of nothing but such stores, with chunks of eight
+            // elements, does it too, as inline assembly as well; not with chunks of four, with global memory, or with
+            // -Xcicc -O1 (-Xptxas -O0 changes nothing).
+            asm volatile("" : "+r"(lead));
+        }
     }
     // The element of the row that is element e of chunk c.
     __device__ int index(int c, int e) const { return (c * kGroup + lane) * kC + e - (kWhole ? 0 : lead); }

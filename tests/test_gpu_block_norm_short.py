@@ -1,5 +1,6 @@
 """The norms around a block with rows shorter than a 16-byte piece, anywhere in memory: values right, nothing of the
-neighbours used or written. Which pieces are read is tests/test_row_pieces.py's."""
+neighbours used or written (which pieces are read is tests/test_row_pieces.py's). And the pieces at the ends of longer
+rows, in groups of every size."""
 
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import block_norm_ref as N
 import train_ops_ref as R
 from mixture_experts_routed_topk_gb300 import binding as B
-from test_gpu_block_norm import EPS, NAMES, make, rand
+from test_gpu_block_norm import EPS, NAMES, back, make, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,15 @@ def test_short_rows(D, dtype, offset, gate):
         for name, g, w, e in zip(NAMES, out, ref, errs):
             R.check(g, w, e + R.round_bound(w, g.dtype), f"{name} T={T}")
         amid.check_around()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D", [13, 121, 505, 519, 777, 1017, 1501, 2041, 3001, 4089, 4103, 6001, 8185])
+def test_first_and_last_chunks_of_every_group(D, dtype):
+    """Column sums of groups of 32 to 512 threads, several to a block, whose rows all lie differently to 16-byte pieces."""
+    for T in (15, 70):
+        c = make(T, D, dtype, F32, gate="channel", seed=3)
+        a, got = back(c, F32, True, 0.7)
+        want, errs = N.bwd(*a.values(), 0.7)
+        for name, w, e in zip(NAMES, want, errs):
+            R.check(got[name], w, e + R.round_bound(w, got[name].dtype), f"{name} T={T}")
