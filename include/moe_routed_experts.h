@@ -749,10 +749,13 @@ size_t moe_few_workspace_bytes(int64_t T, int32_t D, int32_t F, int32_t E, int32
  * Arguments, types and alignment as for moe_routed_experts_fwd; a workspace of
  * moe_few_workspace_bytes(T, D, F, E, K), whose first 4 bytes are the status word. T > 32 or T K > 512:
  * MOE_ERR_UNSUPPORTED_SHAPE.
- * Quicker than moe_routed_experts_fwd while an expert has up to about eight tokens; with more of them that
- * call is (32 tokens with four of 8 experts each take 74 us here, 51 there).
+ * Quicker than moe_routed_experts_fwd for up to 12 tokens whose experts' weights (6 F D bytes for each distinct one) are
+ * less than about 3 GB together. Above that the two are within 5 %, that call ahead; with more tokens it depends on
+ * the layer (24 tokens, D x F = 4096 x 1536, four of 16 experts each: 109 us here and 121 there; 2048 x 1408, six of 64:
+ * 206 and 178).
  * Unlike there, H = SiLU(g) u goes on in two bf16 parts (good to 2^-17), and the pairs' outputs are scaled and added
- * up in fp32: out alone is rounded, once. A pair with a score of 0 is passed over (its expert's weights are not read for
+ * up in fp32: out alone is rounded, once. An H beyond fp32 is infinite, and a score that is not finite leaves its token's
+ * output not finite. A pair with a score of 0 is passed over (its expert's weights are not read for
  * it, and need not be finite). An id outside [0, E) sets MOE_DEV_BAD_EXPERT_ID and contributes 0; ids may
  * repeat. A token without pairs gets a row of zeros. out may not overlap x or the weights.
  */
@@ -793,10 +796,11 @@ moe_status_t moe_layer_fwd_few(const void *x, const void *logits, int32_t dtype,
  *   token        device int32 [T];  logprob  device fp32 [T], or NULL
  * 1 <= V <= 2^24, T < 2^31. A logit of -inf is never chosen; where there are logits of +inf they share the choice
  * equally. A row of nothing but -inf, or with a logit that is not a number, gets token -1 and a logprob that is not a
- * number. Weights are whole numbers of units, good to 2^-30 of themselves and less than one unit short; their sums are
- * exact, so the choice does not depend on the order of additions. The unit is 2^-44 of the largest weight for V < 2^19:
- * tokens below it are never chosen, and shares are off by 2^-30 + V 2^-44 at most. From there on it is the finest, down to
- * 2^-61, in which the row's weights sum to less than 2^62, and shares are off by 2^-30 + V 2^-60 at most.
+ * number. Logits further apart than the largest fp32 number count as infinitely far.
+ * Weights are whole numbers of units, good to 2^-30 of themselves and less than one unit short; their sums are exact, so
+ * the choice does not depend on the order of additions. The unit is 2^-44 of the largest weight for V < 2^19: tokens
+ * below it are never chosen, and shares are off by 2^-30 + V 2^-44 at most. From there on it is the finest, down to 2^-61,
+ * in which the row's weights sum to less than 2^62, and shares are off by 2^-30 + V 2^-60 at most.
  */
 moe_status_t moe_sample(const void *logits, int32_t dtype, const float *uniform, const float *temperature,
                         const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *logprob,

@@ -31,11 +31,14 @@
 // A pair whose score is 0 is passed over: it costs no weights. All sums are fp32, in a fixed order.
 //
 // Measured (calls in a graph, other experts in each; in brackets the weights at the copy rate, then the large forward):
-// 1 x 2048 x 1408, 6 of 64 experts 24 us (15.3; 51); 1 x 7168 x 2048, 8 experts 115 us (104; 167); 8 x 4096 x 1536,
-// 8 of 64 242 us (233; 264); 16 x 7168 x 2048, 8 of 64 765 us (724; 742); 32 x 4096 x 1536, 8 of 128 642 us (622; 636).
-// Furthest from the weights' time are few experts with many tokens, whose columns cost more than the weights they
-// meet: 32 x 2048 x 1408, 4 of 8 experts 74 us (20; 51), 32 x 7168 x 2048, 8 of 32 533 us (416; 449). There tiles of
-// 128 rows are the better layout, and the large forward is the call to make: from some eight tokens an expert on.
+// 1 x 2048 x 1408, 6 of 64 experts 24 us (15.3; 53); 1 x 7168 x 2048, 8 experts 113 us (104; 173); 8 x 4096 x 1536,
+// 8 of 64 236 us (232; 260); 16 x 7168 x 2048, 8 of 64 751 us (726; 727), 8 of 256 1371 us (1339; 1301);
+// 32 x 4096 x 1536, 8 of 128 622 us (614; 618).
+// The large forward takes some 20 us more for its launches, but streams a large layer up to 6 % quicker: the two meet at
+// some 3 GB of weights, and this is the quicker one below for up to 12 tokens (11 layers, 1 to 32 tokens). With more
+// tokens the columns cost more than the weights they meet: 24 x 2048 x 1408, 6 of 64 206 us (146; 178),
+// 32 x 2048 x 1408, 4 of 8 75 us (20; 52), 32 x 7168 x 2048, 8 of 32 514 us (416; 439). There tiles of 128 rows are the
+// better layout. Which call to make is the caller's choice.
 #include <cuda_bf16.h>
 
 #include <algorithm>

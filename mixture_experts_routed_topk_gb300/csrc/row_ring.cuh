@@ -231,7 +231,7 @@ __device__ __forceinline__ void store_two<__half>(__half* to, float2 v) {
 template <typename T, int kGroup, bool kWhole, int kN>
 struct Cells {
     static constexpr int kC = 16 / static_cast<int>(sizeof(T)), kPairs = kC / 2, kChunks = kN / kC;
-    // Whether rows may be shorter than a piece. A larger group has rows of more than half its elements.
+    // Whether rows may be shorter than a piece. A larger group has rows of nearly half its elements or more.
     static constexpr bool kShort = kGroup == 32;
     static_assert(kGroup == 32 || kGroup * kN / 2 >= 2 * kC, "rows of a piece or more");
     using Pairs = float2[kPairs];

@@ -19,8 +19,10 @@
 // the row: 16 bins to each halving of the weight, with counts and weights, merged over the cluster. The cut lies in
 // one bin; its tokens (some hundreds) go to the first block, which sorts them. Bins with more tokens than the
 // list holds are split again by the logits' bits, down to a single logit, whose ties are cut by number. Bound by
-// latency for a few rows (a handful of cluster barriers), by instruction issue for many: a pass over the weights has
-// some 75 instructions for a warp's 32 tokens, one that only looks for the largest logit about 4.
+// latency for a few rows, by instruction issue for many: a pass over the weights has some 75 instructions for a warp's 32
+// tokens, one that only looks for the largest logit about 4. A row without a filter passes four cluster barriers, one with
+// top-k seven; they are the smaller part of a row's time (0.24 us each in a kernel of nothing else, of 512 threads and one to
+// eight blocks), the rest is the passes' own latency and the sorts.
 //
 // Measured (calls in a graph): 1 x 32000 f32 without a filter 10 us, with top-k 17, top-p 22, both 17, min-p 11;
 // 64 x 131072 bf16 33, 25, 96, 25 and 23 us; 256 x 131072 f32 with top-p 274 us, where reading the logits once takes
@@ -389,7 +391,7 @@ struct Sampler {
         return before;
     }
     // The smallest key of the bins up to b, which is not the last one. Passes over the row compare keys with it, which
-    // takes a third of the instructions that a token's bin does (256 x 131072 f32, top-p: 276 us against 295). Each warp
+    // takes a third of the instructions that a token's bin does (256 x 131072 f32, top-p: 274 us against 295). Each warp
     // searches with 32 keys at a time, near the logit that the bin's number stands for (else seven steps of them took
     // 1 us).
     __device__ uint32_t least_key(int b) const {
