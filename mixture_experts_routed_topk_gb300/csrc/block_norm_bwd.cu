@@ -14,8 +14,8 @@
 // token), from which a channel gate's and post_gamma's gradients follow by a factor per channel. They stay in
 // registers; each block writes one row of them, and a second kernel adds the rows in block order.
 //
-// Measured (calls in a graph; in brackets the bytes at the copy rate): 16384 x 7168 bf16 273 us (208), with a gate per
-// token 335 us (277), 4096 x 2048 without a norm after the block 20 us (12), 16384 x 7001 361 us (203), 8192 x 7168 f32
+// Measured (calls in a graph; in brackets the bytes at the copy rate): 16384 x 7168 bf16 275 us (208), with a gate per
+// token 339 us (277), 4096 x 2048 without a norm after the block 20 us (12), 16384 x 7001 359 us (203), 8192 x 7168 f32
 // 373 us (208). Bound by the two dependent sums of a row where it is not the memory: issue is 50 %, and 118 to 128
 // registers (16 of the 16-bit kernels spill 4 to 16 bytes) leave no room for a second row. Without a norm or a gate after
 // the block there is one sum and 102 registers, and one row at a time all the same. Blocks of 1024 threads took 325 us

@@ -13,7 +13,7 @@
 // channel gate, and pre_gamma. Rows longer than a group holds are read three times, mostly from L2.
 //
 // Measured (calls in a graph; in brackets the bytes at the copy rate): 16384 x 7168 bf16 145 us (139), 16 rows 4.4 us,
-// 16384 x 512 14 us (10), 8191 x 1001 f16 with a gate per token 23 us (12), 16384 x 7001 bf16 194 us (135: rows on no
+// 16384 x 512 14 us (10), 8191 x 1001 f16 with a gate per token 23 us (12), 16384 x 7001 bf16 193 us (135: rows on no
 // 16-byte boundary, where every piece is looked at for elements of the neighbours before it is used and before it is
 // written), 8192 x 7168 f32 219 us (139: three readings).
 #include <algorithm>
